@@ -518,6 +518,154 @@ mok_status mok_moe_forward_router(const void* x, const void* Wr, const void* W1,
                                   int32_t* expert_counts, int32_t* expert_offsets, void* saved, void* workspace,
                                   void* stream);
 
+/* ------------------------------------------------------------------------
+ * The layer's steps as separate operators, for a routing or experts of the
+ * caller's own (group limits, capacity drops, adapters, another grouped
+ * product): the pair sort, the row permutation both ways with its gradients,
+ * and expert products with 4-bit integer weights.  They share the conventions
+ * above: device pointers, 16-byte aligned, nothing allocated, nothing
+ * synchronised, every check before the launch.
+ * ------------------------------------------------------------------------ */
+
+/* Element type of the rows these operators move. */
+typedef enum {
+  MOK_DTYPE_F32 = 0,
+  MOK_DTYPE_BF16 = 1,
+  MOK_DTYPE_F16 = 2
+} mok_dtype;
+
+/*
+ * Counting sort of token-expert pairs ([kucoin §01]: count each expert's
+ * tokens, then place them, one expert's rows together), on expert indices of
+ * the caller's own.  Pair p = t*k + j is local when expert_begin <=
+ * topk_idx[p] < expert_end; any other value (another rank's expert, -1 for a
+ * dropped or padded pair, or garbage) is no local pair.  Rows of one expert
+ * ascend by pair; an expert may be named twice by a token.
+ *   topk_idx       int32 [T, k]
+ *   expert_counts  int32 [E]       local pairs per expert (0 outside the range)
+ *   expert_offsets int32 [E+1]     exclusive prefix sum of expert_counts
+ *   row_of_pair    int32 [T, k]    -1 for a pair that is not local
+ *   pair_of_row    int32 [T*k]     -1 past the last local pair's row
+ *   workspace      mok_sort_pairs_workspace_query bytes of scratch (0 bytes up
+ *                  to 2048 pairs: may be NULL); calls in flight at once need
+ *                  one each
+ * 1 <= E <= 1024, 0 <= expert_begin < expert_end <= E, 1 <= k <= 1024,
+ * T*k < 2^31.  T = 0 writes counts and offsets of 0.
+ * Errors: MOK_ERR_INVALID_ARG for a shape outside these bounds or a null or
+ * misaligned pointer; MOK_ERR_HIP for a failed launch.
+ */
+mok_status mok_sort_pairs_workspace_query(int32_t T, int32_t k, int32_t E, size_t* workspace_bytes);
+mok_status mok_sort_pairs(const int32_t* topk_idx, int32_t T, int32_t k, int32_t E, int32_t expert_begin,
+                          int32_t expert_end, int32_t* expert_counts, int32_t* expert_offsets, int32_t* row_of_pair,
+                          int32_t* pair_of_row, void* workspace, void* stream);
+
+/*
+ * Token rows into their experts' rows and back ([kucoin §01] dispatch and
+ * combine, [kucoin §03] the weighted sum), and the gradients of both.  With
+ * w(t,j) = gate[t,j], or 1 when gate is NULL, and row(t,j) = row_of_pair[t,j]:
+ *   mok_permute_rows             xp[row(t,j)] = w(t,j) x[t]
+ *   mok_permute_rows_backward    dx[t] = sum_j w(t,j) dxp[row(t,j)],
+ *                                dgate[t,j] = <x[t], dxp[row(t,j)]>
+ *   mok_unpermute_rows           out[t] = sum_j w(t,j) y[row(t,j)]
+ *   mok_unpermute_rows_backward  dy[row(t,j)] = w(t,j) dout[t],
+ *                                dgate[t,j] = <dout[t], y[row(t,j)]>
+ *   x, dx, out, dout   dtype [T, d]
+ *   xp, dxp, y, dy     dtype [rows, d]   `rows` is the buffer's height
+ *   gate, dgate        float [T, k]
+ *   row_of_pair        int32 [T, k]      from mok_sort_pairs, or any map that
+ *                                        names no row twice
+ * A pair whose row lies outside [0, rows) has no row: it adds nothing to a
+ * sum, its gate is not applied to anything (whatever its value), its dgate is
+ * 0; a token without rows gets 0.  Rows that no pair names are left as they
+ * were.  Sums and products are fp32, slots in ascending order, rounded once to
+ * dtype; without a gate the permutation copies bits.  The gradients of the
+ * gate are asked for by giving dgate and the forward's x (or y), or refused by
+ * NULL for both.  Outputs must not overlap inputs.
+ * 1 <= d <= 2^20 (any width; rows of a multiple of 16 bytes move fastest),
+ * 1 <= k <= 1024, T*k < 2^31, 0 <= rows < 2^31.  T = 0 does nothing.
+ * Errors: as for mok_sort_pairs; MOK_ERR_INVALID_ARG also for one of dgate and
+ * x (or y) without the other.
+ */
+mok_status mok_permute_rows(const void* x, const float* gate, const int32_t* row_of_pair, int32_t T, int32_t k,
+                            int32_t d, mok_dtype dtype, int64_t rows, void* xp, void* stream);
+mok_status mok_permute_rows_backward(const void* dxp, const void* x, const float* gate, const int32_t* row_of_pair,
+                                     int32_t T, int32_t k, int32_t d, mok_dtype dtype, int64_t rows, void* dx,
+                                     float* dgate, void* stream);
+mok_status mok_unpermute_rows(const void* y, const float* gate, const int32_t* row_of_pair, int32_t T, int32_t k,
+                              int32_t d, mok_dtype dtype, int64_t rows, void* out, void* stream);
+mok_status mok_unpermute_rows_backward(const void* dout, const void* y, const float* gate, const int32_t* row_of_pair,
+                                       int32_t T, int32_t k, int32_t d, mok_dtype dtype, int64_t rows, void* dy,
+                                       float* dgate, void* stream);
+
+/* A matrix [N, K] per local expert in 4-bit integers with group scales:
+ *   W[n, i] = scales[n, i / group] * (q[n, i] - zeros[n, i / group])
+ *   codes   [E_loc, N, K/2] bytes; element 2i of a row in the low nibble of
+ *           byte i, element 2i + 1 in the high nibble (0..15)
+ *   scales  dtype [E_loc, N, K/group], finite
+ *   zeros   uint8 [E_loc, N, K/group], or NULL: 8 everywhere (symmetric) */
+typedef struct mok_int4_weights {
+  const uint8_t* codes;
+  const void* scales;
+  const uint8_t* zeros;
+} mok_int4_weights;
+
+typedef struct mok_int4_config {
+  int32_t rows;              /* rows of out (capacity, T*k for a pair map)      */
+  int32_t x_rows;            /* rows of x                                       */
+  int32_t k;                 /* pairs per token, read with pair_of_row only     */
+  int32_t E;                 /* experts of the offsets (1..1024)                */
+  int32_t expert_begin;      /* first local expert                              */
+  int32_t expert_end;        /* one past the last local expert                  */
+  int32_t N;                 /* output width (any)                              */
+  int32_t K;                 /* input width, a multiple of group                */
+  int32_t group;             /* 32, 64 or 128                                   */
+  int32_t dtype;             /* mok_dtype of x, scales and out: BF16 or F16     */
+} mok_int4_config;
+
+/*
+ * Expert products with 4-bit integer weights, for decode steps (an MoE decode
+ * kernel is named as earlier work in [fluid], section "Quand la communication
+ * devient le vrai problème"; 4-bit weights as an analogue of the NVFP4
+ * attempts there):
+ *   out[r] = W_e x_r                          (w_up NULL)
+ *   out[r] = silu(W_e x_r) * (Wup_e x_r)      (the layer's first product)
+ * for every row r of expert e, [expert_offsets[e], expert_offsets[e + 1]) cut
+ * to [0, rows); rows of no local expert are left as they were.
+ *   x               dtype [x_rows, K]
+ *   pair_of_row     int32 [rows] from mok_sort_pairs: x_r = x[pair_of_row[r] /
+ *                   k], the token's row (an entry outside x reads as zeros);
+ *                   NULL: x_r = x[r]
+ *   expert_offsets  int32 [E + 1] from mok_sort_pairs; NULL: one matrix for
+ *                   every row (E = 1, no pair_of_row)
+ *   out             dtype [rows, N]
+ * Codes enter the matrix cores exactly and the scales multiply fp32 sums; one
+ * rounding at the end.  x finite, below 2^100 in magnitude.  Results are the
+ * same bits on every run.  Few rows per expert: each tile of rows reads its
+ * expert's weights again.
+ * rows and x_rows up to 2^24, x below 2 GiB, one expert's codes below 2 GiB.
+ * Errors: MOK_ERR_UNSUPPORTED for MOK_DTYPE_F32; MOK_ERR_INVALID_ARG for a
+ * null or misaligned pointer, a shape outside these bounds, or zeros for one
+ * of two matrices only; MOK_ERR_HIP for a failed launch.
+ */
+mok_status mok_expert_matvec_int4(const void* x, const int32_t* pair_of_row, const int32_t* expert_offsets,
+                                  const mok_int4_weights* w, const mok_int4_weights* w_up,
+                                  const mok_int4_config* cfg, void* out, void* stream);
+
+/*
+ * 4-bit integer quantisation of a matrix along its rows for
+ * mok_expert_matvec_int4, per group of consecutive elements (once per weight):
+ *   zeros NULL  s = amax / 7, q = clamp(rint(v / s) + 8, 0, 15)
+ *   zeros       lo = min(v, 0), hi = max(v, 0), s = (hi - lo) / 15,
+ *               z = clamp(rint(-lo / s), 0, 15), q = clamp(rint(v / s) + z, 0, 15)
+ * s is rounded to dtype first (fp32 arithmetic, ties to even); with s = 0 every
+ * weight of the group is 0.
+ *   src     dtype [rows, K], finite, K a multiple of group; rows * K <= 2^40
+ *   codes, scales, zeros  as in mok_int4_weights, rows in place of E_loc, N
+ * Errors: as for mok_expert_matvec_int4.
+ */
+mok_status mok_quantize_int4(const void* src, int64_t rows, int64_t K, int32_t group, mok_dtype dtype, uint8_t* codes,
+                             void* scales, uint8_t* zeros, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* mok_status_string(mok_status s);
 

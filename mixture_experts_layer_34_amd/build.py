@@ -18,7 +18,8 @@ OUT = os.path.join(PKG, "libmok.so")
 DIAG = os.path.join(PKG, "libmok_diag.so")
 BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["route_sort.hip", "permute_combine.hip", "gemm_bf16.hip", "gemm_stream.hip", "quantize_rows.hip", "gemm_f32.hip", "gemm_mxfp8.hip", "router_gemm.hip",
-           "mok_abi.cpp"]
+           "sort_pairs.hip", "permute_rows.hip", "int4_matvec_bf16.hip", "int4_matvec_f16.hip", "quantize_int4.hip",
+           "mok_abi.cpp", "expert_abi.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17", "-Wall", "-Wno-unused-function",
          # packed fp32 arithmetic stays off: hipcc would otherwise emit packed

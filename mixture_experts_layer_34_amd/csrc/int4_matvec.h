@@ -1,0 +1,32 @@
+// Host-side launchers of the 4-bit integer expert products and their weight
+// quantiser (include/mok.h).  Internal to libmok.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace mok {
+
+struct Int4Args {
+  const void* x;               // [x_rows, K]
+  const int32_t* pair_of_row;  // x row of row r is pair_of_row[r] / k; null: r
+  const int32_t* offsets;      // rows of expert e: [offsets[e], offsets[e + 1]); null: one matrix, every row
+  const uint8_t* codes[2];     // [E_loc, N, K / 2]
+  const void* scales[2];       // [E_loc, N, K / group]
+  const uint8_t* zeros[2];     // like the scales, or null: 8
+  void* out;                   // [rows, N]
+  int rows, x_rows, k;
+  int eb, E_loc;
+  int N, K, group;
+  int dtype;                   // kBF16 or kF16
+  int pair;                    // two matrices: out = silu(first) * second
+};
+// x below 2 GiB and an expert's codes below 4 GiB (32-bit buffer offsets).
+hipError_t launch_int4_matvec_bf16(const Int4Args& a, hipStream_t s);
+hipError_t launch_int4_matvec_f16(const Int4Args& a, hipStream_t s);
+
+// zeros == nullptr: symmetric.
+hipError_t launch_quantize_int4(const void* src, int64_t rows, int64_t K, int group, int dtype, uint8_t* codes,
+                                void* scales, uint8_t* zeros, hipStream_t s);
+
+}  // namespace mok

@@ -1,0 +1,251 @@
+"""The layer's steps as separate operators, for a routing or experts of the
+caller's own: pairs sorted by expert, token rows to the experts' rows and back
+with their gradients, and expert products with 4-bit integer weights.
+
+Torch plumbing around the C ABI (include/mok.h): tensors are checked, outputs
+allocated unless given, and the kernels enqueued on the tensors' device, on
+its current stream.  Inputs that are not contiguous (or not 16-byte aligned)
+are copied; an output given by the caller has to be both."""
+from __future__ import annotations
+
+from dataclasses import dataclass
+
+import torch
+
+from . import mok
+
+_DTYPES = {torch.float32: mok.MOK_DTYPE_F32, torch.bfloat16: mok.MOK_DTYPE_BF16, torch.float16: mok.MOK_DTYPE_F16}
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _on(fn: str, ref: torch.Tensor, *tensors):
+    """Every tensor on the first one's GPU."""
+    _need(ref.is_cuda, f"{fn}: tensors on a GPU expected")
+    for t in tensors:
+        _need(t is None or t.device == ref.device, f"{fn}: tensors on different devices")
+
+
+def _ready(t):
+    """The tensor itself, or a contiguous, 16-byte aligned copy."""
+    if t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+def _output(fn: str, out, shape, dtype, device):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(tuple(out.shape) == tuple(shape) and out.dtype == dtype and out.device == device,
+          f"{fn}: out must be {dtype} {tuple(shape)} on {device}")
+    _need(out.is_contiguous() and out.data_ptr() % 16 == 0, f"{fn}: out must be contiguous and 16-byte aligned")
+    return out
+
+
+def _call(f, device, *args):
+    with torch.cuda.device(device):
+        f(*args, torch.cuda.current_stream(device).cuda_stream)
+
+
+@dataclass
+class PairMap:
+    """Where the T * k token-expert pairs sit in the expert-sorted rows
+    (mok_sort_pairs): int32 counts [E], offsets [E + 1], row_of_pair [T, k]
+    (-1: no row) and pair_of_row [T * k] (-1 past the last row)."""
+    T: int
+    k: int
+    E: int
+    expert_begin: int
+    expert_end: int
+    counts: torch.Tensor
+    offsets: torch.Tensor
+    row_of_pair: torch.Tensor
+    pair_of_row: torch.Tensor
+
+    def __post_init__(self):
+        shapes = ((self.E,), (self.E + 1,), (self.T, self.k), (self.T * self.k,))
+        for t, shape in zip((self.counts, self.offsets, self.row_of_pair, self.pair_of_row), shapes):
+            _need(t.dtype == torch.int32 and tuple(t.shape) == shape and t.device == self.counts.device,
+                  "PairMap: int32 counts [E], offsets [E + 1], row_of_pair [T, k], pair_of_row [T * k] on one device")
+
+
+def sort_pairs(topk_idx: torch.Tensor, E: int, expert_begin: int = 0, expert_end: int | None = None) -> PairMap:
+    """Sorts the pairs of int32 topk_idx [T, k] by expert, stably.  Indices
+    outside [expert_begin, expert_end) (-1: dropped) get no row."""
+    fn = "sort_pairs"
+    _need(topk_idx.dim() == 2 and topk_idx.dtype == torch.int32, f"{fn}: int32 topk_idx [T, k] expected")
+    _on(fn, topk_idx)
+    T, k = topk_idx.shape
+    ee = E if expert_end is None else expert_end
+    dev = topk_idx.device
+    nws = mok.mok_sort_pairs_workspace_query(T, k, E)
+    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
+    m = PairMap(T, k, E, expert_begin, ee, *(torch.empty(s, dtype=torch.int32, device=dev)
+                                             for s in (E, E + 1, (T, k), T * k)))
+    _call(mok.mok_sort_pairs, dev, _ready(topk_idx), T, k, E, expert_begin, ee, m.counts, m.offsets, m.row_of_pair,
+          m.pair_of_row, ws)
+    return m
+
+
+def _rows_args(fn: str, pmap: PairMap, gate, tokens, rows):
+    """Checks one [T, d] tensor, one [rows, d] tensor (either may be None) and
+    the gates against a pair map; returns (d, dtype code)."""
+    ref = tokens if tokens is not None else rows
+    _need(ref.dim() == 2 and ref.dtype in _DTYPES, f"{fn}: fp32, bf16 or fp16 matrices expected")
+    _on(fn, ref, tokens, rows, gate, pmap.row_of_pair)
+    _need(tokens is None or (tokens.dim() == 2 and tokens.shape[0] == pmap.T and tokens.dtype == ref.dtype and
+                             tokens.shape[1] == ref.shape[1]), f"{fn}: token rows [{pmap.T}, d] expected")
+    _need(rows is None or (rows.dim() == 2 and rows.dtype == ref.dtype and rows.shape[1] == ref.shape[1]),
+          f"{fn}: expert rows [rows, d] of the tokens' type expected")
+    _need(gate is None or (gate.dtype == torch.float32 and tuple(gate.shape) == (pmap.T, pmap.k)),
+          f"{fn}: fp32 gate [{pmap.T}, {pmap.k}] expected")
+    return ref.shape[1], _DTYPES[ref.dtype]
+
+
+def permute_rows(x: torch.Tensor, pmap: PairMap, gate: torch.Tensor | None = None,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+    """xp[row(t, j)] = gate[t, j] * x[t]; xp is [T * k, d] (or `out`, of any
+    height).  Rows without a pair are left as they are (uninitialised in a new
+    tensor)."""
+    fn = "permute_rows"
+    d, dt = _rows_args(fn, pmap, gate, x, out)
+    rows = pmap.T * pmap.k if out is None else out.shape[0]
+    out = _output(fn, out, (rows, d), x.dtype, x.device)
+    _call(mok.mok_permute_rows, x.device, _ready(x), _ready(gate), _ready(pmap.row_of_pair), pmap.T, pmap.k, d, dt,
+          rows, out)
+    return out
+
+
+def permute_rows_backward(dxp: torch.Tensor, pmap: PairMap, gate: torch.Tensor | None = None,
+                          x: torch.Tensor | None = None):
+    """(dx, dgate) of permute_rows; dgate (None without x) needs the forward's x."""
+    fn = "permute_rows_backward"
+    d, dt = _rows_args(fn, pmap, gate, x, dxp)
+    dx = torch.empty((pmap.T, d), dtype=dxp.dtype, device=dxp.device)
+    dgate = None if x is None else torch.empty((pmap.T, pmap.k), dtype=torch.float32, device=dxp.device)
+    _call(mok.mok_permute_rows_backward, dxp.device, _ready(dxp), _ready(x), _ready(gate), _ready(pmap.row_of_pair),
+          pmap.T, pmap.k, d, dt, dxp.shape[0], dx, dgate)
+    return dx, dgate
+
+
+def unpermute_rows(y: torch.Tensor, pmap: PairMap, gate: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """out[t] = sum_j gate[t, j] * y[row(t, j)], in fp32, rounded once."""
+    fn = "unpermute_rows"
+    d, dt = _rows_args(fn, pmap, gate, None, y)
+    out = _output(fn, out, (pmap.T, d), y.dtype, y.device)
+    _call(mok.mok_unpermute_rows, y.device, _ready(y), _ready(gate), _ready(pmap.row_of_pair), pmap.T, pmap.k, d, dt,
+          y.shape[0], out)
+    return out
+
+
+def unpermute_rows_backward(dout: torch.Tensor, pmap: PairMap, gate: torch.Tensor | None = None,
+                            y: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """(dy, dgate) of unpermute_rows; dgate (None without y) needs the
+    forward's y.  dy is as high as y (or `out`, or T * k rows); rows without a
+    pair are left as they are."""
+    fn = "unpermute_rows_backward"
+    d, dt = _rows_args(fn, pmap, gate, dout, y)
+    rows = y.shape[0] if y is not None else pmap.T * pmap.k if out is None else out.shape[0]
+    dy = _output(fn, out, (rows, d), dout.dtype, dout.device)
+    dgate = None if y is None else torch.empty((pmap.T, pmap.k), dtype=torch.float32, device=dout.device)
+    _call(mok.mok_unpermute_rows_backward, dout.device, _ready(dout), _ready(y), _ready(gate),
+          _ready(pmap.row_of_pair), pmap.T, pmap.k, d, dt, rows, dy, dgate)
+    return dy, dgate
+
+
+# ------------------------------------------------------------------ 4-bit integer weights
+@dataclass
+class Int4Weights:
+    """Matrices [E, N, K] in 4-bit integers: uint8 codes [E, N, K / 2] (two per
+    byte, the lower element in the low nibble), scales [E, N, K / group] in the
+    activations' type, and uint8 zeros like the scales (None: 8 everywhere)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    zeros: torch.Tensor | None = None
+
+    def __post_init__(self):
+        q, s, z = self.codes, self.scales, self.zeros
+        _need(q.dim() == 3 and q.dtype == torch.uint8 and s.dim() == 3 and s.shape[:2] == q.shape[:2],
+              "Int4Weights: uint8 codes [E, N, K / 2] and scales [E, N, K / group] expected")
+        _need(s.dtype in (torch.bfloat16, torch.float16), "Int4Weights: bf16 or fp16 scales expected")
+        _need(s.shape[2] > 0 and self.K % s.shape[2] == 0 and self.group in (32, 64, 128),
+              "Int4Weights: groups of 32, 64 or 128 expected")
+        _need(z is None or (z.dtype == torch.uint8 and z.shape == s.shape), "Int4Weights: uint8 zeros like the scales")
+        _on("Int4Weights", q, s, z)
+        self.codes, self.scales, self.zeros = _ready(q), _ready(s), _ready(z)
+
+    @property
+    def E(self):
+        return self.codes.shape[0]
+
+    @property
+    def N(self):
+        return self.codes.shape[1]
+
+    @property
+    def K(self):
+        return 2 * self.codes.shape[2]
+
+    @property
+    def group(self):
+        return self.K // self.scales.shape[2]
+
+
+def quantize_int4(w: torch.Tensor, group: int = 128, symmetric: bool = True) -> Int4Weights:
+    """4-bit weights of bf16 or fp16 w [N, K] or [E, N, K], in groups along K."""
+    _need(w.dim() in (2, 3) and w.dtype in (torch.bfloat16, torch.float16),
+          "quantize_int4: bf16 or fp16 w [N, K] or [E, N, K] expected")
+    _on("quantize_int4", w)
+    w = _ready(w if w.dim() == 3 else w[None])
+    E, N, K = w.shape
+    _need(group in (32, 64, 128) and K > 0 and K % group == 0, "quantize_int4: K a multiple of a group of 32, 64 or 128")
+    codes = torch.empty((E, N, K // 2), dtype=torch.uint8, device=w.device)
+    scales = torch.empty((E, N, K // group), dtype=w.dtype, device=w.device)
+    zeros = None if symmetric else torch.empty(scales.shape, dtype=torch.uint8, device=w.device)
+    _call(mok.mok_quantize_int4, w.device, w, E * N, K, group, _DTYPES[w.dtype], codes, scales, zeros)
+    return Int4Weights(codes, scales, zeros)
+
+
+def expert_matvec_int4(x: torch.Tensor, w: Int4Weights, pmap: PairMap | None = None, w_up: Int4Weights | None = None,
+                       from_tokens: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
+    """W_e x of each row's expert, or silu(W_e x) * (Wup_e x) with w_up.
+
+    With a pair map x holds the expert-sorted rows [T * k, K], or with
+    from_tokens the token rows [T, K], and the result the sorted rows
+    [T * k, N] (rows without a pair are left as they are).  Without one, w is
+    one matrix and every row of x is its own."""
+    fn = "expert_matvec_int4"
+    _need(x.dim() == 2 and x.dtype == w.scales.dtype and x.shape[1] == w.K,
+          f"{fn}: x [rows, {w.K}] of the scales' type expected")
+    _on(fn, x, w.codes, None if w_up is None else w_up.codes, None if pmap is None else pmap.offsets)
+    _need(w_up is None or (w_up.codes.shape == w.codes.shape and w_up.scales.shape == w.scales.shape and
+                           w_up.scales.dtype == w.scales.dtype and (w_up.zeros is None) == (w.zeros is None)),
+          f"{fn}: w and w_up of one shape, group and kind expected")
+    if pmap is None:
+        _need(w.E == 1 and not from_tokens, f"{fn}: one matrix expected without a pair map")
+        rows, k, E, eb, ee = x.shape[0], 1, 1, 0, 1
+    else:
+        rows, k, E, eb, ee = pmap.T * pmap.k, pmap.k, pmap.E, pmap.expert_begin, pmap.expert_end
+        _need(w.E == ee - eb, f"{fn}: weights of {ee - eb} experts expected")
+        _need(x.shape[0] == (pmap.T if from_tokens else rows), f"{fn}: x of {pmap.T if from_tokens else rows} rows "
+                                                               "expected")
+    out = _output(fn, out, (rows, w.N), x.dtype, x.device)
+    cfg = mok.mok_int4_config(rows, x.shape[0], k, E, eb, ee, w.N, w.K, w.group, _DTYPES[x.dtype])
+    parts = lambda m: None if m is None else (m.codes, m.scales, m.zeros)
+    _call(mok.mok_expert_matvec_int4, x.device, _ready(x), _ready(pmap.pair_of_row) if from_tokens else None,
+          None if pmap is None else _ready(pmap.offsets), parts(w), parts(w_up), cfg, out)
+    return out
+
+
+def int4_experts(x: torch.Tensor, pmap: PairMap, gate: torch.Tensor, w1: Int4Weights, w3: Int4Weights,
+                 w2: Int4Weights) -> torch.Tensor:
+    """The expert block of a decode step on token rows x [T, d]:
+    out[t] = sum_j gate[t, j] W2_e (silu(W1_e x_t) * (W3_e x_t)), e the expert
+    of pair (t, j); in three launches after sort_pairs."""
+    h = expert_matvec_int4(x, w1, pmap, w_up=w3, from_tokens=True)
+    y = expert_matvec_int4(h, w2, pmap)
+    return unpermute_rows(y, pmap, gate=gate)

@@ -15,6 +15,7 @@ LIB_PATH = os.path.join(_HERE, "libmok.so")
 
 MOK_OK, MOK_ERR_INVALID_ARG, MOK_ERR_UNSUPPORTED, MOK_ERR_WORKSPACE, MOK_ERR_HIP, MOK_ERR_DEVICE = range(6)
 MOK_PREC_F32, MOK_PREC_BF16, MOK_PREC_MXFP8, MOK_PREC_MXFP4 = range(4)
+MOK_DTYPE_F32, MOK_DTYPE_BF16, MOK_DTYPE_F16 = range(3)
 MOK_FLAG_SAVE_FOR_BACKWARD = 0x1
 MOK_FLAG_SIGMOID_GATES = 0x2
 MOK_FLAG_RENORM_GATES = 0x4
@@ -48,6 +49,15 @@ class mok_workspace_layout(ctypes.Structure):
                 ("dy", ctypes.c_size_t), ("dab", ctypes.c_size_t),
                 ("dxp", ctypes.c_size_t), ("wq", ctypes.c_size_t), ("wq_scale", ctypes.c_size_t),
                 ("k_pad", ctypes.c_int64), ("total", ctypes.c_size_t)]
+
+
+class mok_int4_weights(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
+
+
+class mok_int4_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("rows", "x_rows", "k", "E", "expert_begin", "expert_end", "N", "K", "group", "dtype")]
 
 
 MOK_CHECK_LOGITS, MOK_CHECK_INDEX = 0x1, 0x2
@@ -109,6 +119,23 @@ def lib() -> ctypes.CDLL:
         L.mok_router_logits_backward.restype = ctypes.c_int
         L.mok_router_logits_backward.argtypes = [_P, _P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P,
                                                  _P]
+        i32, i64 = ctypes.c_int32, ctypes.c_int64
+        L.mok_sort_pairs_workspace_query.restype = ctypes.c_int
+        L.mok_sort_pairs_workspace_query.argtypes = [i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)]
+        L.mok_sort_pairs.restype = ctypes.c_int
+        L.mok_sort_pairs.argtypes = [_P, i32, i32, i32, i32, i32, _P, _P, _P, _P, _P, _P]
+        for f in (L.mok_permute_rows, L.mok_unpermute_rows):
+            f.restype = ctypes.c_int
+            f.argtypes = [_P, _P, _P, i32, i32, i32, ctypes.c_int, i64, _P, _P]
+        for f in (L.mok_permute_rows_backward, L.mok_unpermute_rows_backward):
+            f.restype = ctypes.c_int
+            f.argtypes = [_P, _P, _P, _P, i32, i32, i32, ctypes.c_int, i64, _P, _P, _P]
+        L.mok_expert_matvec_int4.restype = ctypes.c_int
+        L.mok_expert_matvec_int4.argtypes = [_P, _P, _P, ctypes.POINTER(mok_int4_weights),
+                                             ctypes.POINTER(mok_int4_weights), ctypes.POINTER(mok_int4_config), _P,
+                                             _P]
+        L.mok_quantize_int4.restype = ctypes.c_int
+        L.mok_quantize_int4.argtypes = [_P, i64, i64, i32, ctypes.c_int, _P, _P, _P, _P]
         _lib = L
     return _lib
 
@@ -223,3 +250,52 @@ def mok_router_logits(x, Wr, T, d, E, logits, stream=0):
 def mok_router_logits_backward(x, Wr, dlogits, T, d, E, dx, dWr, stream=0):
     _check(lib().mok_router_logits_backward(_ptr(x), _ptr(Wr), _ptr(dlogits), T, d, E, _ptr(dx), _ptr(dWr),
                                             stream or None), "mok_router_logits_backward")
+
+
+def mok_sort_pairs_workspace_query(T, k, E) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().mok_sort_pairs_workspace_query(T, k, E, ctypes.byref(n)), "mok_sort_pairs_workspace_query")
+    return n.value
+
+
+def mok_sort_pairs(topk_idx, T, k, E, expert_begin, expert_end, expert_counts, expert_offsets, row_of_pair,
+                   pair_of_row, workspace, stream=0):
+    _check(lib().mok_sort_pairs(_ptr(topk_idx), T, k, E, expert_begin, expert_end, _ptr(expert_counts),
+                                _ptr(expert_offsets), _ptr(row_of_pair), _ptr(pair_of_row), _ptr(workspace),
+                                stream or None), "mok_sort_pairs")
+
+
+def mok_permute_rows(x, gate, row_of_pair, T, k, d, dtype, rows, xp, stream=0):
+    _check(lib().mok_permute_rows(_ptr(x), _ptr(gate), _ptr(row_of_pair), T, k, d, dtype, rows, _ptr(xp),
+                                  stream or None), "mok_permute_rows")
+
+
+def mok_permute_rows_backward(dxp, x, gate, row_of_pair, T, k, d, dtype, rows, dx, dgate, stream=0):
+    _check(lib().mok_permute_rows_backward(_ptr(dxp), _ptr(x), _ptr(gate), _ptr(row_of_pair), T, k, d, dtype, rows,
+                                           _ptr(dx), _ptr(dgate), stream or None), "mok_permute_rows_backward")
+
+
+def mok_unpermute_rows(y, gate, row_of_pair, T, k, d, dtype, rows, out, stream=0):
+    _check(lib().mok_unpermute_rows(_ptr(y), _ptr(gate), _ptr(row_of_pair), T, k, d, dtype, rows, _ptr(out),
+                                    stream or None), "mok_unpermute_rows")
+
+
+def mok_unpermute_rows_backward(dout, y, gate, row_of_pair, T, k, d, dtype, rows, dy, dgate, stream=0):
+    _check(lib().mok_unpermute_rows_backward(_ptr(dout), _ptr(y), _ptr(gate), _ptr(row_of_pair), T, k, d, dtype, rows,
+                                             _ptr(dy), _ptr(dgate), stream or None), "mok_unpermute_rows_backward")
+
+
+def _int4(w):
+    """mok_int4_weights of (codes, scales, zeros or None)."""
+    return mok_int4_weights(*(_ptr(v) for v in w))
+
+
+def mok_expert_matvec_int4(x, pair_of_row, expert_offsets, w, w_up, cfg: mok_int4_config, out, stream=0):
+    up = None if w_up is None else ctypes.byref(_int4(w_up))
+    _check(lib().mok_expert_matvec_int4(_ptr(x), _ptr(pair_of_row), _ptr(expert_offsets), ctypes.byref(_int4(w)), up,
+                                        ctypes.byref(cfg), _ptr(out), stream or None), "mok_expert_matvec_int4")
+
+
+def mok_quantize_int4(src, rows, K, group, dtype, codes, scales, zeros, stream=0):
+    _check(lib().mok_quantize_int4(_ptr(src), rows, K, group, dtype, _ptr(codes), _ptr(scales), _ptr(zeros),
+                                   stream or None), "mok_quantize_int4")

@@ -1,0 +1,607 @@
+"""The separate expert operators on the GPU against plain implementations in
+64 bits: the pair sort, the row permutation both ways with its gradients,
+expert products with 4-bit integer weights and their quantiser, and a decode
+step of them together.
+
+Tolerances.  u = 2^-24 bounds one fp32 rounding, h(t) half a step of the output
+type.  A weighted copy is one fp32 product and one rounding; a sum over k slots
+k fused steps; a dot product over d elements at most d / 64 + 24 steps in one
+chain (elements of a thread, then the lanes' and waves' tree).  A 4-bit product
+accumulates 32 products and the running value per matrix instruction (33 steps
+of at most 2 u each, should it not round to nearest), then the group's
+correction and the sum over groups and waves."""
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_34_amd import expert_ops as X
+from mixture_experts_layer_34_amd import mok
+from tests.gpu_case import note
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+TINY = {"f32": 2.0 ** -149, "bf16": 2.0 ** -133, "f16": 2.0 ** -24}  # a subnormal step
+
+
+def _gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def _randn(g, shape, dt="f32"):
+    return torch.randn(shape, generator=g).to(DT[dt]).cuda()
+
+
+def _close(got, ref, tol, what):
+    got, ref = got.double().cpu(), ref.double().cpu()
+    bad = (got - ref).abs() - tol.double().cpu()
+    assert not torch.isnan(got).any(), what
+    assert bad.numel() == 0 or float(bad.max()) <= 0, f"{what}: {float((got - ref).abs().max())} off"
+
+
+# ------------------------------------------------------------------ sort
+def _sort_ref(idx, E, eb, ee):
+    e = idx.reshape(-1).numpy()
+    pairs = [np.flatnonzero(e == q) if eb <= q < ee else np.zeros(0, np.int64) for q in range(E)]
+    counts = np.array([len(p) for p in pairs])
+    order = np.concatenate(pairs).astype(np.int64) if E else np.zeros(0, np.int64)
+    row = np.full(e.size, -1, np.int64)
+    row[order] = np.arange(order.size)
+    pair = np.full(e.size, -1, np.int64)
+    pair[:order.size] = order
+    return counts, np.concatenate([[0], np.cumsum(counts)]), row.reshape(tuple(idx.shape)), pair
+
+
+def _check_sort(idx, E, eb, ee):
+    m = X.sort_pairs(idx.cuda(), E, eb, ee)
+    for got, ref, name in zip((m.counts, m.offsets, m.row_of_pair, m.pair_of_row), _sort_ref(idx, E, eb, ee),
+                              ("counts", "offsets", "row_of_pair", "pair_of_row")):
+        assert np.array_equal(got.cpu().numpy(), ref), name
+    return m
+
+
+@pytest.mark.parametrize("T,k,E,eb,ee", [
+    (0, 2, 8, 0, 8), (1, 1, 1, 0, 1), (1, 8, 128, 0, 128), (3, 5, 17, 0, 17), (16, 8, 128, 0, 128),
+    (256, 8, 64, 0, 64),             # exactly one chunk
+    (257, 8, 64, 0, 64),             # one pair row past it
+    (1000, 6, 1024, 0, 1024), (2000, 3, 1000, 17, 900), (8192, 8, 256, 32, 64),
+    (16384, 8, 128, 0, 128),         # 64 chunks: the most the placing workgroups sum themselves
+    (16385, 8, 128, 0, 128),         # the table's prefix by a launch of its own
+    (70001, 7, 129, 3, 129),         # 240 chunks, the last one ragged
+    (90000, 6, 40, 0, 40),           # 264 chunks: two rounds of the prefix
+])
+def test_sort_pairs(T, k, E, eb, ee):
+    note(f"sort T={T} k={k} E={E} [{eb}, {ee})")
+    idx = torch.randint(-1, E + 2, (T, k), generator=_gen(T + k + E), dtype=torch.int32)
+    _check_sort(idx, E, eb, ee)
+
+
+@pytest.mark.parametrize("kind", ["one", "none", "extreme", "repeats"])
+def test_sort_pairs_skewed(kind):
+    T, k, E = 777, 4, 48
+    idx = torch.randint(0, E, (T, k), generator=_gen(5), dtype=torch.int32)
+    if kind == "one":
+        idx[:] = 31
+    elif kind == "none":
+        idx[:] = -1
+    elif kind == "extreme":
+        idx[::3] = 2 ** 31 - 1
+        idx[1::3] = -2 ** 31
+    else:
+        idx[:, 1:] = idx[:, :1]      # the same expert in every slot of a token
+    m = _check_sort(idx, E, 0, E)
+    x = _randn(_gen(1), (T, 40))
+    out = X.unpermute_rows(X.permute_rows(x, m, out=torch.zeros((T * k, 40), device="cuda")), m)
+    live = ((idx >= 0) & (idx < E)).sum(1, keepdim=True).cuda()
+    assert torch.equal(out, x * live)    # k <= 4 copies: exact up to 4 x
+
+
+# ------------------------------------------------------------------ rows
+def _routing(T, k, E, seed, drop=0.15):
+    g = _gen(seed)
+    idx = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)
+    idx[torch.rand((T, k), generator=g) < drop] = -1
+    if T > 2:
+        idx[T // 2] = -1                                      # a token without any row
+    gate = torch.rand((T, k), generator=g)
+    gate[idx < 0] = float("nan")                              # never applied
+    return idx.cuda(), gate.cuda()
+
+
+def _rows64(a, rows, gate, row):
+    """(sum_j w rows[row], sum_j |w rows[row]|, <a, rows[row]>, <|a|, |rows[row]|>) in 64 bits."""
+    live = row >= 0
+    w = torch.where(live, torch.ones_like(row, dtype=torch.float64) if gate is None else gate.double(), 0.0)
+    r = rows.double()[row.clamp(min=0).long()] * live[..., None]
+    r = torch.where(live[..., None], r, torch.zeros_like(r))
+    wr = r * w[..., None]
+    ar = None if a is None else a.double()[:, None] * r
+    return wr.sum(1), wr.abs().sum(1), None if a is None else ar.sum(2), None if a is None else ar.abs().sum(2)
+
+
+ROWS = [(1, 1, 1, 1, "bf16"), (5, 2, 4, 8, "f32"), (7, 3, 4, 64, "bf16"), (33, 8, 16, 256, "f16"),
+        (20, 2, 4, 1024, "bf16"), (20, 2, 4, 1032, "bf16"), (12, 8, 8, 4096, "bf16"), (9, 6, 4, 2500, "f32"),
+        (50, 6, 8, 1411, "f32"), (11, 4, 8, 1411, "bf16"), (11, 4, 8, 1410, "f16"), (13, 9, 8, 130, "bf16"),
+        (6, 19, 8, 520, "f32"), (4, 17, 8, 2050, "f16"), (300, 1, 3, 77, "f16"), (3, 8, 4, 7168, "bf16")]
+
+
+@pytest.mark.parametrize("T,k,E,d,dt", ROWS)
+@pytest.mark.parametrize("gated", [False, True])
+def test_permute_unpermute_and_gradients(T, k, E, d, dt, gated):
+    note(f"rows T={T} k={k} E={E} d={d} {dt} gated={gated}")
+    g = _gen(T * 31 + d)
+    idx, gate = _routing(T, k, E, T + d)
+    gate = gate if gated else None
+    m = X.sort_pairs(idx, E)
+    row, P = m.row_of_pair, int(m.offsets[E])
+    x, rows = _randn(g, (T, d), dt), _randn(g, (T * k, d), dt)
+    rows[P:] = float("nan")                                   # no pair's rows
+    live = (row >= 0).reshape(-1)
+    at = row.reshape(-1)[live].long()
+
+    def check_scatter(got, src, what):
+        assert torch.isnan(got[P:]).all(), f"{what}: rows without a pair were written"
+        want = src.double().repeat_interleave(k, 0)[live]
+        if gate is None:
+            assert torch.equal(got[at].double(), want), what
+        else:
+            want = want * gate.reshape(-1)[live].double()[:, None]
+            _close(got[at], want, want.abs() * (HALF[dt] + 2 * U) + TINY[dt], what)
+
+    dots_tol = (d / 64 + 24) * U
+    sink = torch.full((T * k, d), float("nan"), dtype=DT[dt], device="cuda")
+    check_scatter(X.permute_rows(x, m, gate=gate, out=sink.clone()), x, "permute")
+    ref, mag, dots, dmag = _rows64(x, rows, gate, row)
+    sum_tol = ref.abs() * HALF[dt] + mag * (k + 1) * U + TINY[dt]
+    _close(X.unpermute_rows(rows, m, gate=gate), ref, sum_tol, "unpermute")
+    dx, none = X.permute_rows_backward(rows, m, gate=gate)
+    assert none is None
+    _close(dx, ref, sum_tol, "dx alone")
+    dx2, dgate = X.permute_rows_backward(rows, m, gate=gate, x=x)
+    assert torch.equal(dx, dx2)
+    _close(dgate, dots, dmag * dots_tol, "permute's dgate")
+    dy, none = X.unpermute_rows_backward(x, m, gate=gate, out=sink.clone())
+    assert none is None
+    check_scatter(dy, x, "dy alone")
+    dy2, dgate2 = X.unpermute_rows_backward(x, m, gate=gate, y=rows, out=sink.clone())
+    check_scatter(dy2, x, "dy")
+    assert torch.equal(dy[at], dy2[at])
+    _close(dgate2, dots, dmag * dots_tol, "unpermute's dgate")
+
+
+def test_gradients_against_differences():
+    """The gradients of L = <permute or unpermute, v>, fp32, against central
+    differences in 64 bits of the operators' definition (linear in each
+    argument, so the differences are exact up to 64-bit rounding)."""
+    T, k, E, d = 6, 3, 4, 24
+    idx, gate = _routing(T, k, E, 3)
+    gate = torch.nan_to_num(gate, nan=0.5)
+    m = X.sort_pairs(idx, E)
+    row = m.row_of_pair
+    g = _gen(8)
+    x, y, v, u = (_randn(g, s) for s in ((T, d), (T * k, d), (T * k, d), (T, d)))
+
+    def loss_permute(x_, gate_):
+        live = row >= 0
+        return float((torch.where(live, gate_, 0.0)[..., None] * x_[:, None] * v.double()[row.clamp(min=0).long()]).sum())
+
+    def loss_unpermute(y_, gate_):
+        return float((_rows64(None, y_, gate_, row)[0] * u.double()).sum())
+
+    def differences(f, a):
+        out = torch.zeros_like(a)
+        for i in range(a.numel()):
+            e = torch.zeros_like(a).view(-1)
+            e[i] = 0.5
+            out.view(-1)[i] = f(a + e.view_as(a)) - f(a - e.view_as(a))
+        return out
+
+    xd, yd, gd = x.double(), y.double(), gate.double()
+    dx, dg = X.permute_rows_backward(v, m, gate=gate, x=x)
+    tol = torch.tensor(64 * U * 64.0)   # sums of at most 24 terms of magnitude below 16
+    _close(dx, differences(lambda a: loss_permute(a, gd), xd), tol, "dx")
+    _close(dg, differences(lambda a: loss_permute(xd, a), gd), tol, "permute's dgate")
+    dy, dg = X.unpermute_rows_backward(u, m, gate=gate, y=y, out=torch.zeros_like(y))
+    _close(dy, differences(lambda a: loss_unpermute(a, gd), yd), tol, "dy")
+    _close(dg, differences(lambda a: loss_unpermute(yd, a), gd), tol, "unpermute's dgate")
+
+
+def test_bad_maps_and_nonfinite_values():
+    """Row indices outside the buffer are no rows; infinities and NaN stay in
+    the rows that hold them."""
+    T, k, d = 4, 2, 264
+    g = _gen(2)
+    x, rows = _randn(g, (T, d), "bf16"), _randn(g, (6, d), "bf16")
+    rop = torch.tensor([[0, 6], [5, -7], [2 ** 31 - 1, -2 ** 31], [1, 4]], dtype=torch.int32, device="cuda")
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    m = X.PairMap(T, k, 2, 0, 2, z(2), z(3), rop, z(T * k))
+    x[1, 3], x[3, 7], rows[2, 0], rows[4, 9] = float("inf"), float("nan"), float("nan"), float("inf")
+    gate = torch.full((T, k), 0.5, device="cuda")
+    xp = X.permute_rows(x, m, gate=gate, out=torch.full_like(rows, 7.0))
+    want = torch.full_like(rows, 7.0)
+    for r, t in ((0, 0), (5, 1), (1, 3), (4, 3)):
+        want[r] = (x[t].float() * 0.5).bfloat16()
+    assert torch.equal(torch.nan_to_num(xp.float(), nan=99.0), torch.nan_to_num(want.float(), nan=99.0))
+    out = X.unpermute_rows(rows, m)
+    want = torch.stack([rows[0], rows[5], torch.zeros_like(rows[0]), (rows[1].float() + rows[4].float()).bfloat16()])
+    assert torch.equal(out, want)
+    dy, dgate = X.unpermute_rows_backward(x, m, gate=gate, y=rows, out=torch.zeros_like(rows))
+    assert torch.equal(dgate[2], torch.zeros(2, device="cuda")) and dgate[0, 1] == 0 and dgate[1, 1] == 0
+    assert torch.isnan(dgate[3]).all() and torch.isinf(dgate[1, 0])
+    assert torch.equal(dy[2:4], torch.zeros_like(dy[2:4]))
+
+
+def test_rows_past_four_gigabytes():
+    """Row offsets past 32 bits: a buffer of 70,000 rows of 64 KiB."""
+    d, rows = 32768, 70000
+    x = _randn(_gen(4), (2, d), "bf16")
+    rop = torch.tensor([[rows - 1, 65536], [0, rows - 2]], dtype=torch.int32, device="cuda")
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    m = X.PairMap(2, 2, 1, 0, 1, z(1), z(2), rop, z(4))
+    buf = torch.zeros((rows, d), dtype=torch.bfloat16, device="cuda")
+    X.permute_rows(x, m, out=buf)
+    for r, t in ((rows - 1, 0), (65536, 0), (0, 1), (rows - 2, 1)):
+        assert torch.equal(buf[r], x[t])
+    assert int((buf != 0).any(1).sum()) == 4
+    assert torch.equal(X.unpermute_rows(buf, m), (x.float() * 2).bfloat16())
+
+
+# ------------------------------------------------------------------ 4-bit products
+def _weights(g, E, N, K, group, zeros, dt):
+    codes = torch.randint(0, 256, (E, N, K // 2), generator=g, dtype=torch.uint8)
+    scales = ((torch.rand((E, N, K // group), generator=g) + 0.5) / (4.6 * K ** 0.5)).to(DT[dt])
+    z = torch.randint(0, 16, scales.shape, generator=g, dtype=torch.uint8) if zeros else None
+    return X.Int4Weights(codes.cuda(), scales.cuda(), None if z is None else z.cuda())
+
+
+def _unpack(w):
+    """(W, s (16 + q) + s (16 + z)) in 64 bits: the weights, and the magnitudes
+    that the two sums of a group run over."""
+    q = torch.stack((w.codes & 15, w.codes >> 4), -1).flatten(-2).double()
+    s = w.scales.double().repeat_interleave(w.group, 2)
+    z = torch.full_like(q, 8.0) if w.zeros is None else w.zeros.double().repeat_interleave(w.group, 2)
+    return (q - z) * s, (32 + q + z) * s
+
+
+def _product_ref(xr, expert, w, w_up, dt):
+    """Values and tolerances of rows xr (64 bits) with expert ids."""
+    def one(m):
+        W, mag = _unpack(m)
+        v = torch.zeros((xr.shape[0], m.N), dtype=torch.float64, device="cuda")
+        t = torch.zeros_like(v)
+        for e in range(m.E):
+            r = torch.where(expert == e)[0]
+            v[r] = xr[r] @ W[e].t()
+            t[r] = xr[r].abs() @ mag[e].t()
+        # per matrix instruction 33 steps, at most four in a chain; then the
+        # correction, the sum over groups, eight waves
+        return v, t * (4 * 33 * 2 + m.K / m.group + 12) * U
+    a, ta = one(w)
+    if w_up is None:
+        return a, a.abs() * HALF[dt] + ta + TINY[dt]
+    b, tb = one(w_up)
+    s = a * torch.sigmoid(a)
+    h = s * b
+    return h, h.abs() * (HALF[dt] + 2.0 ** -18) + 1.1 * ta * (b.abs() + tb) + (s.abs() + 1.1 * ta) * tb + TINY[dt]
+
+
+MATVEC = [  # T, k, E, N, K, group, zeros, pair, dtype
+    (1, 1, 1, 16, 32, 32, False, False, "bf16"), (1, 8, 16, 64, 128, 32, True, True, "bf16"),
+    (2, 2, 4, 33, 256, 64, False, False, "f16"), (4, 6, 8, 100, 384, 128, True, True, "f16"),
+    (5, 2, 8, 48, 96, 32, False, True, "bf16"), (16, 4, 5, 70, 160, 32, True, False, "bf16"),
+    (17, 3, 2, 64, 192, 64, True, False, "bf16"), (40, 2, 3, 31, 512, 128, False, True, "bf16"),
+    (64, 4, 2, 80, 320, 64, False, False, "f16"), (9, 8, 300, 17, 64, 64, True, True, "bf16"),
+    (130, 2, 4, 40, 1024, 128, True, False, "bf16"), (3, 2, 1024, 20, 128, 128, False, False, "f16"),
+    (12, 2, 4, 128, 4096, 32, True, True, "bf16"), (300, 1, 2, 65, 288, 32, False, False, "f16"),
+]
+
+
+@pytest.mark.parametrize("T,k,E,N,K,group,zeros,pair,dt", MATVEC)
+@pytest.mark.parametrize("from_tokens", [False, True])
+def test_expert_matvec(T, k, E, N, K, group, zeros, pair, dt, from_tokens):
+    note(f"matvec T={T} k={k} E={E} N={N} K={K} g={group} zeros={zeros} pair={pair} {dt} tokens={from_tokens}")
+    g = _gen(T + N + K)
+    idx, _ = _routing(T, k, E, N + K, drop=0.1)
+    m = X.sort_pairs(idx, E)
+    P = int(m.offsets[E])
+    w = [_weights(g, E, N, K, group, zeros, dt) for _ in range(2)]
+    x = _randn(g, (T if from_tokens else T * k, K), dt)
+    if not from_tokens:
+        x[P:] = float("nan")
+    out = torch.full((T * k, N), float("nan"), dtype=DT[dt], device="cuda")
+    got = X.expert_matvec_int4(x, w[0], m, w_up=w[1] if pair else None, from_tokens=from_tokens, out=out)
+    assert got is out and torch.isnan(got[P:]).all()
+    pr = m.pair_of_row[:P].long()
+    xr = x.double()[pr // k] if from_tokens else x[:P].double()
+    ref, tol = _product_ref(xr, idx.reshape(-1)[pr].long(), w[0], w[1] if pair else None, dt)
+    _close(got[:P], ref, tol, "product")
+    again = X.expert_matvec_int4(x, w[0], m, w_up=w[1] if pair else None, from_tokens=from_tokens)
+    assert torch.equal(again[:P], got[:P])
+
+
+@pytest.mark.parametrize("rows,N,K,group,zeros,pair,dt", [
+    (0, 16, 32, 32, False, False, "bf16"), (1, 1, 32, 32, True, False, "bf16"), (1, 4099, 7168, 128, True, False, "f16"),
+    (3, 130, 2048, 64, False, True, "bf16"), (5, 64, 1408, 128, False, False, "bf16"), (8, 96, 512, 32, True, True, "f16"),
+    (16, 50, 736, 32, True, False, "bf16"), (17, 64, 256, 32, False, False, "bf16"), (33, 64, 640, 128, True, True, "bf16"),
+    (64, 256, 1024, 64, False, False, "f16"), (65, 48, 128, 32, True, False, "bf16"), (200, 80, 384, 128, True, False, "bf16"),
+])
+def test_dense_matvec(rows, N, K, group, zeros, pair, dt):
+    note(f"dense rows={rows} N={N} K={K} g={group} {dt}")
+    g = _gen(rows + N)
+    w = [_weights(g, 1, N, K, group, zeros, dt) for _ in range(2)]
+    x = _randn(g, (rows, K), dt)
+    got = X.expert_matvec_int4(x, w[0], w_up=w[1] if pair else None)
+    ref, tol = _product_ref(x.double(), torch.zeros(rows, dtype=torch.long, device="cuda"), w[0],
+                            w[1] if pair else None, dt)
+    _close(got, ref, tol, "dense product")
+
+
+def test_matvec_exact_integers():
+    """Small integer x, power-of-two scales: every sum is exact in fp32, so the
+    result is the rounded exact value, whatever the order (bf16 and fp16, each
+    code and zero point)."""
+    for dt in ("bf16", "f16"):
+        K, N, rows = 256, 256, 7
+        codes = torch.arange(N, dtype=torch.uint8)[:, None].expand(N, K // 2).contiguous()[None].cuda()
+        zeros = (torch.arange(N * K // 32) % 16).to(torch.uint8).view(1, N, K // 32).cuda()
+        scales = torch.full((1, N, K // 32), 0.25, dtype=DT[dt], device="cuda")
+        w = X.Int4Weights(codes, scales, zeros)
+        x = torch.randint(-3, 4, (rows, K), generator=_gen(1)).to(DT[dt]).cuda()
+        ref = x.double() @ _unpack(w)[0][0].t()
+        assert torch.equal(X.expert_matvec_int4(x, w), ref.to(DT[dt]))
+
+
+def test_matvec_local_experts_and_bad_maps():
+    """An expert-parallel share: weights of the local experts only; and offsets
+    and pairs that leave their buffers are cut, not followed."""
+    T, k, E, N, K = 10, 3, 12, 40, 128
+    g = _gen(6)
+    idx = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32).cuda()
+    m = X.sort_pairs(idx, E, 4, 9)
+    P = int(m.offsets[E])
+    w = _weights(g, 5, N, K, 64, True, "bf16")
+    x = _randn(g, (T, K), "bf16")
+    got = X.expert_matvec_int4(x, w, m, from_tokens=True)
+    pr = m.pair_of_row[:P].long()
+    ref, tol = _product_ref(x.double()[pr // k], idx.reshape(-1)[pr].long() - 4, w, None, "bf16")
+    _close(got[:P], ref, tol, "local share")
+    bad = m.offsets.clone()
+    bad[4], bad[5], bad[6], bad[9] = -50, 2, 5, 1 << 30
+    pairs = m.pair_of_row.clone()
+    pairs[0], pairs[1] = 1 << 30, -5
+    bm = X.PairMap(T, k, E, 4, 9, m.counts, bad, m.row_of_pair, pairs)
+    out = X.expert_matvec_int4(x, w, bm, from_tokens=True)
+    assert torch.equal(out[:2], torch.zeros_like(out[:2]))      # experts 4's rows 0 and 1 with x outside: zeros
+    assert torch.isfinite(out[2:5]).all()
+
+
+# ------------------------------------------------------------------ quantiser
+def _quant_ref(v, group, symmetric, dt):
+    f = v.float().view(v.shape[0], -1, group)
+    lo, hi = f.amin(2).clamp(max=0), f.amax(2).clamp(min=0)
+    s = ((torch.maximum(hi, -lo) / 7) if symmetric else ((hi - lo) / 15)).to(DT[dt])
+    sf = s.float()[..., None]
+    one = torch.where(sf > 0, sf, torch.ones_like(sf))
+    z = torch.full_like(sf, 8.0) if symmetric else torch.where(sf > 0, torch.round(-lo[..., None] / one), 0 * sf).clamp(0, 15)
+    q = torch.where(sf > 0, (torch.round(f / one) + z).clamp(0, 15), z + 0 * f).view(v.shape).to(torch.uint8)
+    return q[:, 0::2] | (q[:, 1::2] << 4), s, z[..., 0].to(torch.uint8)
+
+
+@pytest.mark.parametrize("rows,K,group,symmetric,dt", [
+    (1, 32, 32, True, "bf16"), (5, 96, 32, False, "f16"), (16, 256, 64, True, "f16"), (33, 1408, 128, False, "bf16"),
+    (7, 640, 128, True, "bf16"), (300, 2048, 32, False, "bf16")])
+def test_quantize_int4(rows, K, group, symmetric, dt):
+    v = torch.randn((rows, K), generator=_gen(K)).to(DT[dt])
+    v[0, :group] = 0                                            # a group of zeros
+    if rows > 2:
+        v[1] = v[1].abs()                                       # one sign only
+        v[2] = -v[2].abs()
+    w = X.quantize_int4(v.cuda(), group, symmetric)
+    codes, s, z = _quant_ref(v, group, symmetric, dt)
+    assert torch.equal(w.codes[0].cpu(), codes) and torch.equal(w.scales[0].cpu(), s)
+    assert (w.zeros is None) if symmetric else torch.equal(w.zeros[0].cpu(), z)
+    # every weight within half a step of its value, and half a type's step of
+    # the scale (a clamp moves none further: the scale is at most half a step
+    # of its type short of the range)
+    W = _unpack(w)[0][0].cpu()
+    sd = s.double().repeat_interleave(group, 1)
+    assert float(((W - v.double()).abs() - sd * (0.5 + 15 * 2 * HALF[dt]) - 2 ** -20).max()) <= 0
+
+
+# ------------------------------------------------------------------ together
+def _decode(T=6, k=3, E=8, d=256, F=192, group=64, zeros=True, dt="bf16"):
+    g = _gen(17)
+    idx, gate = _routing(T, k, E, 2, drop=0.1)
+    gate = torch.nan_to_num(gate, nan=0.0)
+    w1, w3, w2 = (_weights(g, E, n, m, group, zeros, dt) for n, m in ((F, d), (F, d), (d, F)))
+    return idx, gate, _randn(g, (T, d), dt), w1, w3, w2
+
+
+def test_decode_step_together():
+    """sort -> gate/up -> down -> weighted back, against 64 bits with the
+    roundings of h and y between the products."""
+    idx, gate, x, w1, w3, w2 = _decode()
+    T, k = idx.shape
+    m = X.sort_pairs(idx, 8)
+    out = X.int4_experts(x, m, gate, w1, w3, w2)
+    W1, W3, W2 = (_unpack(w)[0] for w in (w1, w3, w2))
+    ref = torch.zeros((T, 256), dtype=torch.float64, device="cuda")
+    tol = torch.zeros_like(ref)
+    for t in range(T):
+        for j in range(k):
+            e = int(idx[t, j])
+            if e < 0:
+                continue
+            a, b = W1[e] @ x[t].double(), W3[e] @ x[t].double()
+            h = a * torch.sigmoid(a) * b
+            y = W2[e] @ h
+            gt = float(gate[t, j])
+            ref[t] += gt * y
+            # h off by half a step (and the products' own error, below a
+            # quarter of it at these sizes), y by half a step of itself
+            tol[t] += gt * (1.5 * HALF["bf16"] * (W2[e].abs() @ h.abs()) + 1.5 * HALF["bf16"] * y.abs())
+    tol += ref.abs() * HALF["bf16"] + 2.0 ** -20
+    _close(out, ref, tol, "decode step")
+
+
+def test_training_step_together():
+    """The permutation around plain expert products: the way there and back,
+    and its gradients, as a user's own experts would be trained."""
+    T, k, E, d = 200, 2, 4, 96
+    g = _gen(12)
+    idx, gate = _routing(T, k, E, 9, drop=0.1)
+    gate = torch.nan_to_num(gate, nan=0.0)
+    x, dout = _randn(g, (T, d)), _randn(g, (T, d))
+    A = _randn(g, (E, d, d)) / d ** 0.5
+    m = X.sort_pairs(idx, E)
+    offs = m.offsets.tolist()
+    xp = X.permute_rows(x, m, out=torch.zeros((T * k, d), device="cuda"))
+    y = torch.zeros_like(xp)
+    for e in range(E):
+        y[offs[e]:offs[e + 1]] = xp[offs[e]:offs[e + 1]] @ A[e].t()
+    out = X.unpermute_rows(y, m, gate=gate)
+    dy, dgate = X.unpermute_rows_backward(dout, m, gate=gate, y=y, out=torch.zeros_like(y))
+    dxp = torch.zeros_like(xp)
+    for e in range(E):
+        dxp[offs[e]:offs[e + 1]] = dy[offs[e]:offs[e + 1]] @ A[e]
+    dx, _ = X.permute_rows_backward(dxp, m)
+
+    xd, gd = x.double().requires_grad_(), gate.double().requires_grad_()
+    ref = torch.zeros((T, d), dtype=torch.float64, device="cuda")
+    for j in range(k):
+        for e in range(E):
+            sel = (idx[:, j] == e).double()[:, None]
+            ref = ref + sel * gd[:, j, None] * (xd @ A[e].double().t())
+    ref.backward(dout.double())
+    # products of 96 terms of magnitude about 1: 200 roundings of values below 64
+    tol = torch.tensor(200 * U * 64.0)
+    _close(out, ref.detach(), tol, "out")
+    _close(dx, xd.grad, tol, "dx")
+    _close(dgate, gd.grad, tol * d ** 0.5, "dgate")
+
+
+# ------------------------------------------------------------------ how they are called
+def test_inputs_of_other_layouts():
+    """Strided and misaligned inputs give the contiguous ones' results; an
+    output that is neither is refused."""
+    idx, gate, x, w1, w3, w2 = _decode()
+    T, d = x.shape
+    m = X.sort_pairs(idx, 8)
+    ref = X.int4_experts(x, m, gate, w1, w3, w2)
+    wide = torch.zeros((T, 2 * d), dtype=x.dtype, device="cuda")
+    wide[:, 1:1 + 2 * d:2][:, :d] = x
+    flat = torch.zeros(T * d + 1, dtype=x.dtype, device="cuda")
+    flat[1:] = x.reshape(-1)
+    gt = torch.zeros((gate.shape[1], T), device="cuda")
+    gt.copy_(gate.t())
+    it = idx.t().contiguous().t()
+    m2 = X.sort_pairs(it, 8)
+    assert torch.equal(m2.row_of_pair, m.row_of_pair)
+    for xv in (wide[:, 1::2], flat[1:].view(T, d)):
+        assert torch.equal(X.int4_experts(xv, m, gt.t(), w1, w3, w2), ref)
+        assert torch.equal(X.unpermute_rows(X.permute_rows(xv, m, out=torch.zeros((T * 3, d), dtype=x.dtype, device="cuda")), m),
+                           X.unpermute_rows(X.permute_rows(x, m, out=torch.zeros((T * 3, d), dtype=x.dtype, device="cuda")), m))
+    with pytest.raises(ValueError, match="contiguous"):
+        X.permute_rows(x, m, out=torch.zeros((T * 3, 2 * d), dtype=x.dtype, device="cuda")[:, ::2])
+    with pytest.raises(ValueError, match="out must be"):
+        X.unpermute_rows(torch.zeros((T * 3, d), dtype=x.dtype, device="cuda"), m, out=torch.zeros((T, d), device="cuda"))
+    with pytest.raises(ValueError, match="gate"):
+        X.permute_rows(x, m, gate=gate[:, :2])
+    with pytest.raises(ValueError, match="devices"):
+        X.permute_rows(x, m, gate=gate.cpu())
+    with pytest.raises(ValueError, match="tokens' type"):
+        X.permute_rows_backward(torch.zeros((T * 3, d), device="cuda"), m, x=torch.zeros((T, d + 1), device="cuda"))
+    with pytest.raises(ValueError, match="experts"):
+        X.expert_matvec_int4(x, w1, X.sort_pairs(idx, 9), from_tokens=True)
+    with pytest.raises(ValueError, match="rows"):
+        X.expert_matvec_int4(x, w1, m)
+    with pytest.raises(ValueError, match="one matrix"):
+        X.expert_matvec_int4(x, w1)
+
+
+def test_two_streams_and_reruns():
+    """Calls on two streams at once, each with its own workspace, give the
+    bits of calls one after the other, ten times."""
+    T, k, E, d = 3000, 4, 64, 264
+    sets = []
+    for s in range(2):
+        g = _gen(30 + s)
+        sets.append((torch.randint(0, E, (T, k), generator=g, dtype=torch.int32).cuda(), _randn(g, (T, d), "bf16"),
+                     torch.rand((T, k), generator=g).cuda()))
+
+    def step(idx, x, gate):
+        m = X.sort_pairs(idx, E)
+        xp = X.permute_rows(x, m, gate=gate)
+        return (m.pair_of_row, xp, *X.permute_rows_backward(xp, m, gate=gate, x=x),
+                *X.unpermute_rows_backward(x, m, gate=gate, y=xp))
+    refs = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for rep in range(10):
+        outs = []
+        for st, s in zip(streams, sets):
+            with torch.cuda.stream(st):
+                outs.append(step(*s))
+        torch.cuda.synchronize()
+        for a, b in zip(refs, outs):
+            for u, v in zip(a, b):
+                assert torch.equal(u, v), rep
+
+
+def test_captured_and_replayed():
+    """A decode step and a permutation with its gradients captured into graphs
+    and replayed on new inputs, against the eager calls."""
+    idx, gate, x, w1, w3, w2 = _decode(T=9, k=4)
+    T, k = idx.shape
+
+    def step():
+        m = X.sort_pairs(idx, 8)
+        xp = X.permute_rows(x, m, gate=gate, out=xp_buf)
+        dx, dg = X.permute_rows_backward(xp, m, gate=gate, x=x)
+        return X.int4_experts(x, m, gate, w1, w3, w2), m.counts, m.pair_of_row, xp, dx, dg
+    xp_buf = torch.zeros((T * k, 256), dtype=x.dtype, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for rep in range(4):
+        g = _gen(100 + rep)
+        idx.copy_(torch.randint(-1, 8, (T, k), generator=g, dtype=torch.int32))
+        x.copy_(torch.randn((T, 256), generator=g).bfloat16())
+        gate.copy_(torch.rand((T, k), generator=g))
+        xp_buf.zero_()
+        want = [v.clone() for v in step()]
+        xp_buf.zero_()
+        for v in held:
+            v.zero_() if v is not held[3] else None
+        graph.replay()
+        torch.cuda.synchronize()
+        for u, v in zip(want, held):
+            assert torch.equal(u, v), rep
+
+
+def test_empty_calls():
+    """No tokens, and tokens without any row."""
+    m = X.sort_pairs(torch.zeros((0, 2), dtype=torch.int32, device="cuda"), 4)
+    assert torch.equal(m.offsets.cpu(), torch.zeros(5, dtype=torch.int32))
+    x = torch.zeros((0, 64), device="cuda")
+    assert X.permute_rows(x, m).shape == (0, 64) and X.unpermute_rows(x, m).shape == (0, 64)
+    assert X.permute_rows_backward(x, m, x=x)[1].shape == (0, 2)
+    assert X.unpermute_rows_backward(x, m, y=x)[0].shape == (0, 64)
+    m = X.sort_pairs(torch.full((5, 2), -1, dtype=torch.int32, device="cuda"), 4)
+    y = torch.full((10, 64), float("nan"), device="cuda")
+    assert torch.equal(X.unpermute_rows(y, m), torch.zeros((5, 64), device="cuda"))
+    w = _weights(_gen(1), 4, 32, 64, 32, False, "bf16")
+    out = torch.full((10, 32), 3.0, dtype=torch.bfloat16, device="cuda")
+    X.expert_matvec_int4(torch.zeros((5, 64), dtype=torch.bfloat16, device="cuda"), w, m, from_tokens=True, out=out)
+    assert (out == 3).all()
+    assert mok.MOK_OK == 0
