@@ -642,7 +642,8 @@ typedef struct mok_int4_config {
  * rounding at the end.  x finite, below 2^100 in magnitude.  Results are the
  * same bits on every run.  Few rows per expert: each tile of rows reads its
  * expert's weights again.
- * rows and x_rows up to 2^24, x below 2 GiB, one expert's codes below 2 GiB.
+ * rows and x_rows up to 2^24, rows * N < 2^36, x below 2 GiB, one expert's codes
+ * below 2 GiB, all experts' below 256 GiB.
  * Errors: MOK_ERR_UNSUPPORTED for MOK_DTYPE_F32; MOK_ERR_INVALID_ARG for a
  * null or misaligned pointer, a shape outside these bounds, or zeros for one
  * of two matrices only; MOK_ERR_HIP for a failed launch.

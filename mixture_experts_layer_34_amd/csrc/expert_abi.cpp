@@ -108,6 +108,9 @@ mok_status mok_expert_matvec_int4(const void* x, const int32_t* pair_of_row, con
   if ((int64_t)c.x_rows * c.K * 2 >= (int64_t(1) << 31) || (int64_t)c.N * (c.K / 2) >= (int64_t(1) << 31))
     return MOK_ERR_INVALID_ARG;
   const int32_t E_loc = c.expert_end - c.expert_begin;
+  // units of 4 rows by 16 columns, and of an expert by 16 columns, are counted in 32 bits
+  if ((int64_t)c.rows * c.N >= (int64_t(1) << 36) || (int64_t)E_loc * c.N * (c.K / 2) >= (int64_t(1) << 38))
+    return MOK_ERR_INVALID_ARG;
   if (!expert_offsets && (E_loc != 1 || pair_of_row)) return MOK_ERR_INVALID_ARG;
   if (!pair_of_row && c.x_rows < c.rows) return MOK_ERR_INVALID_ARG;
   if (!good(x, c.x_rows) || !good(out, c.rows) || !aligned16(pair_of_row) || !aligned16(expert_offsets))

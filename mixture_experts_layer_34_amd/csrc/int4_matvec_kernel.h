@@ -32,6 +32,7 @@
 #pragma once
 #include "elem.h"
 #include "int4_matvec.h"
+#include "mok_internal.h"
 #include "pair_ops.h"
 
 namespace mok {
@@ -40,7 +41,6 @@ namespace {
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 constexpr int kChunk = 128;  // K per round: 16 bytes of codes a lane
-constexpr int kMaxExperts = 1024;
 constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every buffer: reads as zero
 
 __device__ __forceinline__ rsrc_t buffer(const void* p, int64_t bytes) {
@@ -54,11 +54,11 @@ __device__ __forceinline__ u32x4_t load16(rsrc_t rs, uint32_t off) {
 template <int DT> struct Mma;
 template <> struct Mma<kBF16> {
   static constexpr uint32_t kMask = 0x00780078u, kSixteen = 0x41804180u, kOnes = 0x3F803F80u;
-  __device__ __forceinline__ static void place(uint32_t w, uint32_t (&d)[4]) {
-    d[0] = ((w << 3) & kMask) | kSixteen;
-    d[1] = ((w >> 1) & kMask) | kSixteen;
-    d[2] = ((w >> 5) & kMask) | kSixteen;
-    d[3] = ((w >> 9) & kMask) | kSixteen;
+  __device__ __forceinline__ static void place(uint32_t w, uint32_t mask, uint32_t sixteen, uint32_t (&d)[4]) {
+    d[0] = ((w << 3) & mask) | sixteen;
+    d[1] = ((w >> 1) & mask) | sixteen;
+    d[2] = ((w >> 5) & mask) | sixteen;
+    d[3] = ((w >> 9) & mask) | sixteen;
   }
   __device__ __forceinline__ static f32x4_t mfma(const uint32_t (&a)[4], const uint32_t (&b)[4], f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, (u32x4_t{a[0], a[1], a[2], a[3]})),
@@ -68,11 +68,11 @@ template <> struct Mma<kBF16> {
 };
 template <> struct Mma<kF16> {
   static constexpr uint32_t kMask = 0x03C003C0u, kSixteen = 0x4C004C00u, kOnes = 0x3C003C00u;
-  __device__ __forceinline__ static void place(uint32_t w, uint32_t (&d)[4]) {
-    d[0] = ((w << 6) & kMask) | kSixteen;
-    d[1] = ((w << 2) & kMask) | kSixteen;
-    d[2] = ((w >> 2) & kMask) | kSixteen;
-    d[3] = ((w >> 6) & kMask) | kSixteen;
+  __device__ __forceinline__ static void place(uint32_t w, uint32_t mask, uint32_t sixteen, uint32_t (&d)[4]) {
+    d[0] = ((w << 6) & mask) | sixteen;
+    d[1] = ((w << 2) & mask) | sixteen;
+    d[2] = ((w >> 2) & mask) | sixteen;
+    d[3] = ((w >> 6) & mask) | sixteen;
   }
   __device__ __forceinline__ static f32x4_t mfma(const uint32_t (&a)[4], const uint32_t (&b)[4], f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, (u32x4_t{a[0], a[1], a[2], a[3]})),
@@ -99,41 +99,76 @@ __device__ __forceinline__ void order_like_codes(const u32x4_t& v, uint32_t (&d)
   d[3] = __builtin_amdgcn_perm(v[3], v[1], 0x07060302u);
 }
 
-// NM matrices (a pair for SwiGLU), MT tiles of 16 rows, groups of GS.
-template <int DT, int NM, int MT, int GS>
-__global__ __launch_bounds__(512) void int4_matvec_kernel(Int4Args a) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int NSC = kChunk / GS;   // groups in a chunk
-  constexpr int RT = 16 * MT;        // rows per tile
-  const int tid = threadIdx.x, lane = tid & 63, kr = __builtin_amdgcn_readfirstlane(tid >> 6), KS = blockDim.x >> 6;
-  const int n16 = lane & 15, g4 = lane >> 4;
-  const int N = a.N, K = a.K, G = K / GS, E_loc = a.E_loc;
-  const int ntn = (N + 15) / 16;
-  extern __shared__ f32x4_t red[];  // [KS - 1][MT][NM][64]
-  __shared__ int32_t tp[kMaxExperts + 1];  // tiles of the experts before e
+// The dword v of lane quarter q in every quarter, for q = 0..3.
+__device__ __forceinline__ void spread_quarters(uint32_t v, uint32_t (&o)[4]) {
+  const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  const auto a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+  const auto b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+  o[0] = a[0];
+  o[1] = a[1];
+  o[2] = b[0];
+  o[3] = b[1];
+}
 
-  // tiles of each expert's rows, and their prefix over the experts
-  if (a.offsets) {
-    __shared__ int32_t wsum[8];
+// NM matrices (a pair for SwiGLU), NG groups of 16 weight rows of each, tiles
+// of RT rows, groups of GS; of a workgroup's waves KS split K and NW lie side
+// by side along N; x is staged SCH chunks at a time.
+template <int DT, int NM, int NG, int RT, int GS, int KS, int NW, int SCH>
+__global__ __launch_bounds__(64 * KS * NW)
+void int4_matvec_kernel(Int4Args a, const int32_t* __restrict__ offsets,
+                                                                   const int32_t* __restrict__ pair_of_row) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int NB = NM * NG;
+  constexpr int NSC = kChunk / GS;          // groups in a chunk
+  constexpr int SW = NSC > 2 ? 2 : 1;       // dwords of a chunk's scales of one weight row
+  constexpr bool QUAD = RT == 4;            // a tile row on each quad of MFMA rows
+  constexpr int MT = QUAD ? 1 : RT / 16;    // MFMA tiles of rows
+  constexpr int IR = QUAD ? 1 : 4;          // results of a lane that hold rows
+  constexpr int JC = SCH / KS;              // chunks of a stage that are this wave's
+  constexpr int XROW = SCH * 256 + 16;      // bytes of a staged row (+16: no bank conflicts)
+  constexpr int XP = SCH * 16;              // 16-byte pieces of a staged row
+  constexpr int NT = 64 * KS * NW;
+  constexpr int XA = (RT * XP + NT - 1) / NT;  // pieces each thread stages
+  static_assert(JC >= 1 && JC * KS == SCH && (JC == 1 || JC % 2 == 0), "every wave has chunks of each stage");
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kr = wave / NW, nw = wave % NW;
+  const int n16 = lane & 15, g4 = lane >> 4;
+  // constants kept in registers: an and-or takes one operand of another kind only
+  uint32_t mask = Mma<DT>::kMask, sixteen = Mma<DT>::kSixteen;
+  asm("" : "+v"(mask), "+v"(sixteen));
+  const int N = a.N, K = a.K, G = K / GS, E_loc = a.E_loc;
+  constexpr int NU = 16 * NG * NW;          // weight rows of a unit
+  const int ntn = (N + NU - 1) / NU;
+  __shared__ __align__(16) uint8_t xs[2][RT * XROW];
+  __shared__ f32x4_t red[KS > 1 ? (KS - 1) * NW * MT * NB * 64 : 1];
+
+  extern __shared__ int32_t tp[];           // [E_loc + 1] tiles of the experts before e
+  int32_t *s_row = tp + E_loc + 1, *s_end = s_row + E_loc;  // and each one's rows
+
+  if (offsets) {
+    __shared__ int32_t wsum[KS * NW];
     int carry = 0;
-    for (int e0 = 0; e0 < E_loc; e0 += blockDim.x) {
+    for (int e0 = 0; e0 < E_loc; e0 += NT) {
       const int e = e0 + tid;
       int n = 0;
       if (e < E_loc) {
-        const int lo = max(a.offsets[a.eb + e], 0), hi = min(a.offsets[a.eb + e + 1], a.rows);
-        n = hi > lo ? (hi - lo + RT - 1) / RT : 0;
+        const int lo = max(offsets[a.eb + e], 0), hi = min(offsets[a.eb + e + 1], a.rows);
+        n = (max(hi - lo, 0) + RT - 1) / RT;
+        s_row[e] = lo;
+        s_end[e] = hi;
       }
       int s = n;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(s, o, 64);
-        if (lane >= o) s += u;
+        const int v = __shfl_up(s, o, 64);
+        if (lane >= o) s += v;
       }
-      if (lane == 63) wsum[kr] = s;
+      if (lane == 63) wsum[wave] = s;
       __syncthreads();
       int base = carry;
-      for (int q = 0; q < KS; ++q) {
-        base += q < kr ? wsum[q] : 0;
+#pragma unroll
+      for (int q = 0; q < KS * NW; ++q) {
+        base += q < wave ? wsum[q] : 0;
         carry += wsum[q];
       }
       if (e < E_loc) tp[e] = base + s - n;
@@ -143,166 +178,319 @@ __global__ __launch_bounds__(512) void int4_matvec_kernel(Int4Args a) {
   } else if (tid == 0) {
     tp[0] = 0;
     tp[1] = (a.rows + RT - 1) / RT;
+    s_row[0] = 0;
+    s_end[0] = a.rows;
   }
   __syncthreads();
-  const int64_t total = (int64_t)tp[E_loc] * ntn;
+  // a sorted map's tiles are no more than this; overlapping offsets' are cut
+  const int most = (a.rows + RT - 1) / RT + min(E_loc, a.rows);
+  const int total = min(__builtin_amdgcn_readfirstlane(tp[E_loc]), most) * ntn;
 
   const int nch = (K + kChunk - 1) / kChunk;
-  const int c0 = nch * kr / KS, c1 = nch * (kr + 1) / KS;
+  const int nst = (nch + SCH - 1) / SCH, nloc = nst * JC;  // stages, this wave's chunks
+  // this wave's i-th chunk
+  auto chunk_of = [&](int i) { return (i / JC) * SCH + kr * JC + i % JC; };
+  const bool whole = K % kChunk == 0;  // a chunk's scales and zeros are one aligned access
+  const bool has_zeros = a.zeros[0] != nullptr;
   const rsrc_t rx = buffer(a.x, (int64_t)a.x_rows * K * 2);
-  for (int64_t u = blockIdx.x; u < total; u += gridDim.x) {
-    const int q = (int)(u / ntn), n0 = (int)(u % ntn) * 16;
-    int lo = 0, hi = E_loc - 1;
-    while (lo < hi) {  // the expert of tile q
-      const int mid = (lo + hi + 1) >> 1;
-      if (tp[mid] <= q) lo = mid; else hi = mid - 1;
+  for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    const int q = u / ntn, n0 = (u % ntn) * NU + 16 * NG * nw;
+    // the expert of tile q, the last one whose tiles start at or before it: 64
+    // prefixes at a time, every share'th and then those of the share
+    int lo = 0;
+    if (E_loc > 1) {
+      const int share = (E_loc + 63) / 64;
+      lo = share * (__popcll(__ballot(lane * share < E_loc && tp[min(lane * share, E_loc)] <= q)) - 1);
+      if (share > 1) lo += __popcll(__ballot(lane < share && lo + lane < E_loc && tp[min(lo + lane, E_loc)] <= q)) - 1;
     }
-    lo = __builtin_amdgcn_readfirstlane(lo);
-    const int first = a.offsets ? max(a.offsets[a.eb + lo], 0) : 0;
-    const int last = a.offsets ? min(a.offsets[a.eb + lo + 1], a.rows) : a.rows;
-    const int row0 = first + (q - tp[lo]) * RT;
-    const int nrow = min(last - row0, RT);
+    const int row0 = __builtin_amdgcn_readfirstlane(s_row[lo] + (q - tp[lo]) * RT);
+    const int nrow = min(__builtin_amdgcn_readfirstlane(s_end[lo]) - row0, RT);
 
-    // this lane's x row (MFMA row lane % 16) and weight row n0 + lane % 16
-    uint32_t xo[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int r = 16 * m + 4 * (n16 & 3) + (n16 >> 2);
-      int64_t src = -1;
-      if (r < nrow) src = a.pair_of_row ? (a.pair_of_row[row0 + r] >= 0 ? a.pair_of_row[row0 + r] / a.k : -1) : row0 + r;
-      xo[m] = src >= 0 && src < a.x_rows ? (uint32_t)(src * K * 2) : kNowhere;
-    }
     const int64_t wrow = (int64_t)lo * N + n0;
     rsrc_t rw[NM], rs[NM], rz[NM];
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
       rw[m] = buffer(a.codes[m] + wrow * (K / 2), (int64_t)(N - n0) * (K / 2));
       rs[m] = buffer((const uint16_t*)a.scales[m] + wrow * G, (int64_t)(N - n0) * G * 2);
-      rz[m] = buffer(a.zeros[m] ? a.zeros[m] + wrow * G : nullptr, a.zeros[m] ? (int64_t)(N - n0) * G : 0);
+      rz[m] = buffer(has_zeros ? a.zeros[m] + wrow * G : nullptr, has_zeros ? (int64_t)(N - n0) * G : 0);
     }
 
-    f32x4_t tot[MT][NM];
+    // A ring of four chunks of codes, two of them (a whole cache line of each
+    // weight row) on their way while two are multiplied.  Loads past K read
+    // zeros.
+    u32x4_t wv[4][NB];
+    uint32_t sv[NB][SW], zv[NB];  // of four chunks, lane quarter q holding chunk q's
+    auto load_codes = [&](int buf, int i) {
+      const int k = chunk_of(i) * kChunk + 32 * g4;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        wv[buf][b] = load16(rw[b / NG], i < nloc && k < K ? (uint32_t)((16 * (b % NG) + n16) * (K / 2) + k / 2) : kNowhere);
+    };
+    auto load_scales = [&](int i0) {
+      const int c = chunk_of(i0 + g4);
+      const bool in_c = i0 + g4 < nloc && c < nch;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int row = (16 * (b % NG) + n16) * G;
+        const rsrc_t r = rs[b / NG], z = rz[b / NG];
+        if (whole) {
+          const uint32_t at = in_c ? (uint32_t)(row + c * NSC) : kNowhere;
+          const uint32_t o = in_c ? 2 * at : kNowhere;
+          if constexpr (NSC == 4) {
+            const auto v = __builtin_amdgcn_raw_buffer_load_b64(r, o, 0, 0);
+            sv[b][0] = v[0];
+            sv[b][SW - 1] = v[1];
+            zv[b] = has_zeros ? __builtin_amdgcn_raw_buffer_load_b32(z, at, 0, 0) : 0x08080808u;
+          } else if constexpr (NSC == 2) {
+            sv[b][0] = __builtin_amdgcn_raw_buffer_load_b32(r, o, 0, 0);
+            zv[b] = has_zeros ? (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(z, at, 0, 0) : 0x0808u;
+          } else {
+            sv[b][0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, o, 0, 0);
+            zv[b] = has_zeros ? (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(z, at, 0, 0) : 0x08u;
+          }
+        } else {
+#pragma unroll
+          for (int w = 0; w < SW; ++w) sv[b][w] = 0;
+          zv[b] = has_zeros ? 0u : 0x08080808u;
+#pragma unroll
+          for (int i = 0; i < NSC; ++i) {
+            const int gi = c * NSC + i;
+            const bool in = in_c && gi < G;
+            const uint32_t v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, in ? 2 * (row + gi) : kNowhere, 0, 0);
+            sv[b][i / 2] |= v << (16 * (i % 2));
+            if (has_zeros)
+              zv[b] |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(z, in ? row + gi : kNowhere, 0, 0)
+                       << (8 * i);
+          }
+        }
+      }
+    };
+    load_codes(0, 0);
+    load_codes(1, 1);
+    load_scales(0);
+    // x by stages of SCH chunks through LDS: a wave takes 64 pieces of 16
+    // bytes of one row at a time, puts them in the codes' order and the row
+    // where the MFMA takes it.  Rows past the tile's are not staged: what an
+    // MFMA row holds stays in its own results, and theirs are not stored.
+    auto row_at = [&](int i) { return (i * (KS * NW) + wave) * 64 / XP; };
+    auto piece_at = [&](int i) { return (i * (KS * NW) + wave) * 64 % XP + lane; };
+    uint32_t xo[XA];
+#pragma unroll
+    for (int i = 0; i < XA; ++i) {
+      const int r = row_at(i);
+      int src = -1;
+      if (r < nrow) {
+        src = row0 + r;
+        if (pair_of_row) {
+          const int p = pair_of_row[src];
+          src = p < 0 ? -1 : (int)((uint32_t)p / (uint32_t)a.k);
+        }
+      }
+      src = __builtin_amdgcn_readfirstlane(src);
+      xo[i] = src >= 0 && src < a.x_rows ? (uint32_t)src * (uint32_t)(K * 2) : kNowhere;
+    }
+    u32x4_t xr[XA];
+    auto load_x = [&](int st) {
+#pragma unroll
+      for (int i = 0; i < XA; ++i) {
+        const int k = st * SCH * kChunk + 8 * piece_at(i);
+        if (row_at(i) < nrow) xr[i] = load16(rx, st < nst && k < K && xo[i] != kNowhere ? xo[i] + 2 * k : kNowhere);
+      }
+    };
+    auto store_x = [&](int buf) {
+#pragma unroll
+      for (int i = 0; i < XA; ++i) {
+        const int r = row_at(i);
+        if (r >= nrow) continue;
+        // MFMA row of tile row r: 4 (r % 4) + r / 4 % 4 within its sixteen
+        const int p = QUAD ? r : (r & ~15) + 4 * (r & 3) + ((r >> 2) & 3);
+        uint32_t d[4];
+        order_like_codes(xr[i], d);
+        *reinterpret_cast<u32x4_t*>(&xs[buf][p * XROW + 16 * piece_at(i)]) = u32x4_t{d[0], d[1], d[2], d[3]};
+      }
+    };
+    load_x(0);
+    store_x(0);
+    __syncthreads();
+
+    f32x4_t tot[MT][NB];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int b = 0; b < NM; ++b) tot[m][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int c = c0; c < c1; ++c) {
-      const int kq = c * kChunk + 32 * g4;  // the K range this lane loads
-      u32x4_t wv[NM];
-      uint32_t sv[NM][NSC], zv[NM][NSC];
+      for (int b = 0; b < NB; ++b) tot[m][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    const uint32_t ones[4] = {Mma<DT>::kOnes, Mma<DT>::kOnes, Mma<DT>::kOnes, Mma<DT>::kOnes};
+    int cur = 0;
+    for (int i0 = 0; i0 < nloc; i0 += 4) {
+      uint32_t sc[NB][SW][4], zc[NB][4];  // the four chunks' scales and 16 + zeros, in every lane quarter
 #pragma unroll
-      for (int b = 0; b < NM; ++b) {
-        wv[b] = load16(rw[b], kq < K ? (uint32_t)(n16 * (K / 2) + kq / 2) : kNowhere);
+      for (int b = 0; b < NB; ++b) {
 #pragma unroll
-        for (int i = 0; i < NSC; ++i) {
-          const int gi = c * NSC + i;
-          sv[b][i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs[b], gi < G ? (n16 * G + gi) * 2 : kNowhere, 0, 0);
-          zv[b][i] = a.zeros[b] ? (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rz[b], gi < G ? n16 * G + gi : kNowhere, 0, 0)
-                                : 8;
-        }
+        for (int w = 0; w < SW; ++w) spread_quarters(sv[b][w], sc[b][w]);
+        spread_quarters(zv[b] + 0x10101010u, zc[b]);
       }
-      u32x4_t xv[MT][4];
+      load_scales(i0 + 4);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int st = 0; st < 4; ++st) {
-          const int k = c * kChunk + 32 * st + 8 * g4;
-          xv[m][st] = load16(rx, k < K && xo[m] != kNowhere ? xo[m] + 2 * k : kNowhere);
+      for (int j = 0; j < 4; ++j) {
+        if (i0 + j >= nloc) break;
+        if (j % JC == 0) load_x((i0 + j) / JC + 1);
+        if (j % 2 == 0) {
+          load_codes((j + 2) % 4, i0 + j + 2);
+          load_codes((j + 3) % 4, i0 + j + 3);
         }
-      uint32_t ones[4] = {Mma<DT>::kOnes, Mma<DT>::kOnes, Mma<DT>::kOnes, Mma<DT>::kOnes};
+        __builtin_amdgcn_sched_barrier(0);
+        if (chunk_of(i0 + j) < nch) {
+          // this lane's pieces of x: its MFMA row, K 32 st + 8 g4 of the chunk
+          const int cs = kr * JC + j % JC;  // chunk of the stage
+          const uint8_t* xb = &xs[cur][cs * 256 + 16 * g4];
+          u32x4_t xq;
+          if constexpr (QUAD) xq = *reinterpret_cast<const u32x4_t*>(xb + (n16 >> 2) * XROW + 64 * (n16 & 3));
 #pragma unroll
-      for (int b = 0; b < NM; ++b) transpose_quarters(wv[b]);
+          for (int b = 0; b < NB; ++b) transpose_quarters(wv[j][b]);
 #pragma unroll
-      for (int i = 0; i < NSC; ++i) {
-        f32x4_t ax[MT], aw[MT][NM];
+          for (int i = 0; i < NSC; ++i) {
+            float sf[NB], zz[NB];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          ax[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            for (int b = 0; b < NB; ++b) {
+              const uint32_t sw = sc[b][i / 2][j];
+              sf[b] = i % 2 ? Elem<DT>::hi(sw) : Elem<DT>::lo(sw);
+              zz[b] = (float)((zc[b][j] >> (8 * i)) & 255u);
+            }
+            constexpr int GST = 4 / NSC;  // MFMA steps of a group
+            const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+            f32x4_t ax[MT], aw[MT][NB];
 #pragma unroll
-          for (int b = 0; b < NM; ++b) aw[m][b] = ax[m];
-        }
+            for (int st = i * GST; st < (i + 1) * GST; ++st) {
+              const bool first = QUAD || st == i * GST;
+              uint32_t wd[NB][4];
 #pragma unroll
-        for (int st = i * (4 / NSC); st < (i + 1) * (4 / NSC); ++st) {
-          uint32_t wd[NM][4];
+              for (int b = 0; b < NB; ++b) Mma<DT>::place(wv[j][b][st], mask, sixteen, wd[b]);
 #pragma unroll
-          for (int b = 0; b < NM; ++b) Mma<DT>::place(wv[b][st], wd[b]);
+              for (int m = 0; m < MT; ++m) {
+                if (MT > 1 && 16 * m >= nrow) continue;
+                if constexpr (!QUAD) xq = *reinterpret_cast<const u32x4_t*>(xb + (16 * m + n16) * XROW + 64 * st);
+                const uint32_t xd[4] = {xq[0], xq[1], xq[2], xq[3]};
+                ax[m] = Mma<DT>::mfma(xd, ones, first ? zero : ax[m]);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            uint32_t xd[4];
-            order_like_codes(xv[m][st], xd);
-            ax[m] = Mma<DT>::mfma(xd, ones, ax[m]);
+                for (int b = 0; b < NB; ++b) aw[m][b] = Mma<DT>::mfma(xd, wd[b], first ? zero : aw[m][b]);
+              }
+              if constexpr (QUAD) {
+                // the lanes of a quad hold x of the steps 0..3: result st is step st's
 #pragma unroll
-            for (int b = 0; b < NM; ++b) aw[m][b] = Mma<DT>::mfma(xd, wd[b], aw[m][b]);
+                for (int b = 0; b < NB; ++b)
+                  tot[0][b][0] = fmaf(sf[b], fmaf(-zz[b], ax[0][st], aw[0][b][st]), tot[0][b][0]);
+              }
+            }
+            if constexpr (!QUAD) {
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                if (MT > 1 && 16 * m >= nrow) continue;
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    tot[m][b][e] = fmaf(sf[b], fmaf(-zz[b], ax[m][e], aw[m][b][e]), tot[m][b][e]);
+              }
+            }
           }
         }
-#pragma unroll
-        for (int b = 0; b < NM; ++b) {
-          const float sc = Elem<DT>::lo(sv[b][i]), zz = 16.0f + (float)zv[b][i];
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) tot[m][b][e] = fmaf(sc, fmaf(-zz, ax[m][e], aw[m][b][e]), tot[m][b][e]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (j % JC == JC - 1) {  // the next stage of x is in place before anyone reads it
+          if (i0 + j + 1 < nloc) store_x(cur ^ 1);
+          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+          __builtin_amdgcn_s_barrier();
+          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+          cur ^= 1;
         }
       }
     }
 
-    // the waves' sums, in wave order
-    if (kr > 0)
+    // the sums of the waves that split K, in wave order
+    if (KS > 1) {
+      if (kr > 0)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int b = 0; b < NM; ++b) red[(((kr - 1) * MT + m) * NM + b) * 64 + lane] = tot[m][b];
-    __syncthreads();
+          for (int b = 0; b < NB; ++b) red[((((kr - 1) * NW + nw) * MT + m) * NB + b) * 64 + lane] = tot[m][b];
+      __syncthreads();
+    }
     if (kr == 0) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
+#pragma unroll
         for (int w = 0; w < KS - 1; ++w)
 #pragma unroll
-          for (int b = 0; b < NM; ++b) tot[m][b] += red[((w * MT + m) * NM + b) * 64 + lane];
-        const int n = n0 + n16;
+          for (int b = 0; b < NB; ++b) tot[m][b] += red[(((w * NW + nw) * MT + m) * NB + b) * 64 + lane];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 16 * m + 4 * e + g4;  // MFMA row 4 g4 + e holds tile row 4 e + g4
-          if (r < nrow && n < N) {
-            const float v = NM == 2 ? tot[m][0][e] * sigmoidf_(tot[m][0][e]) * tot[m][NM - 1][e] : tot[m][0][e];
-            ((uint16_t*)a.out)[(int64_t)(row0 + r) * N + n] = (uint16_t)Elem<DT>::pack(v, 0.f);
+        for (int gi = 0; gi < NG; ++gi) {
+          const int n = n0 + 16 * gi + n16;
+#pragma unroll
+          for (int e = 0; e < IR; ++e) {
+            const int r = 16 * m + 4 * e + g4;  // MFMA row 4 g4 + e holds tile row 4 e + g4 (QUAD: g4)
+            if (r < nrow && n < N) {
+              const float p = tot[m][gi][e];
+              const float v = NM == 2 ? p * sigmoidf_(p) * tot[m][NB - NG + gi][e] : p;
+              ((uint16_t*)a.out)[(int64_t)(row0 + r) * N + n] = (uint16_t)Elem<DT>::pack(v, 0.f);
+            }
           }
         }
       }
     }
-    __syncthreads();  // the sums are read before the next unit writes them
+    // the stage's last barrier lets the next unit stage x; with a split K the
+    // sums have to be read before they are written again, which that unit's
+    // barriers see to
   }
 #endif
 }
 
-template <int DT, int NM, int MT, int GS> hipError_t run(const Int4Args& a, hipStream_t s) {
-  constexpr int RT = 16 * MT;
-  const int64_t ntn = (a.N + 15) / 16;
+template <int DT, int NM, int NG, int RT, int GS, int KS, int NW, int SCH>
+hipError_t run_cfg(const Int4Args& a, hipStream_t s) {
+  constexpr int64_t NU = 16 * NG * NW;
+  const int64_t ntn = (a.N + NU - 1) / NU;
   const int64_t tiles = (a.rows + RT - 1) / RT + (a.offsets ? (a.E_loc < a.rows ? a.E_loc : a.rows) : 0);
   const int64_t units = tiles * ntn;
   if (units == 0) return hipSuccess;
-  const int waves = 4;
   const unsigned grid = (unsigned)(units < 65536 ? units : 65536);
-  hipLaunchKernelGGL((int4_matvec_kernel<DT, NM, MT, GS>), dim3(grid), dim3(64 * waves),
-                     (size_t)(waves - 1) * MT * NM * 64 * sizeof(f32x4_t), s, a);
+  hipLaunchKernelGGL((int4_matvec_kernel<DT, NM, NG, RT, GS, KS, NW, SCH>), dim3(grid), dim3(64 * KS * NW),
+                     (3 * a.E_loc + 1) * sizeof(int32_t), s, a,
+                     a.offsets, a.pair_of_row);
   return hipGetLastError();
 }
 
-template <int DT, int NM, int MT> hipError_t run_group(const Int4Args& a, hipStream_t s) {
+// Waves along K.  A wave by itself on its columns needs no sum and no more
+// barriers than x's, so K is split only as far as it takes to have eight waves
+// for each compute unit: gate / up of one token (768 columns groups of 8
+// experts) 22.1 / 18.1 / 16.5 / 20.1 us for splits of 1 / 2 / 4 / 8, a dense
+// 4099 x 7168 product of three rows 23.8 / 15.2 / 11.9 / 10.2 us; sixteen
+// tokens' gate / up (about 7,900 groups) 137 / 132 / 164 / 262 us.
+template <int DT, int NM, int NG, int RT, int GS> hipError_t run(const Int4Args& a, hipStream_t s) {
+  // expected tiles: every expert that can have a row, and whole tiles past those
+  const int64_t tiles = (a.E_loc < a.rows ? a.E_loc : a.rows) + a.rows / RT - a.rows / RT / 2;
+  const int64_t waves = (a.offsets ? tiles : (a.rows + RT - 1) / RT) * ((a.N + 16 * NG - 1) / (16 * NG));
+  constexpr int64_t kWanted = 8 * kNumCUs;
+  if (waves * 4 < kWanted) return run_cfg<DT, NM, NG, RT, GS, 8, 1, 8>(a, s);
+  if (waves * 2 < kWanted) return run_cfg<DT, NM, NG, RT, GS, 4, 1, 4>(a, s);
+  if (waves < kWanted) return run_cfg<DT, NM, NG, RT, GS, 2, 2, 4>(a, s);
+  return run_cfg<DT, NM, NG, RT, GS, 1, 4, 4>(a, s);
+}
+
+template <int DT, int NM, int NG, int RT> hipError_t run_group(const Int4Args& a, hipStream_t s) {
   switch (a.group) {
-    case 32: return run<DT, NM, MT, 32>(a, s);
-    case 64: return run<DT, NM, MT, 64>(a, s);
-    case 128: return run<DT, NM, MT, 128>(a, s);
+    case 32: return run<DT, NM, NG, RT, 32>(a, s);
+    case 64: return run<DT, NM, NG, RT, 64>(a, s);
+    case 128: return run<DT, NM, NG, RT, 128>(a, s);
   }
   return hipErrorInvalidValue;
 }
 
-template <int DT, int NM> hipError_t run_tile(const Int4Args& a, hipStream_t s) {
-  return run_group<DT, NM, 1>(a, s);
-}
-
+// Rows per tile: four while an expert has two rows or fewer on average (its
+// x costs a quarter; experts with more take several tiles), else sixteen.
+// Gate / up of 128 experts, 16 tokens (a row an expert): 137 us in fours, 155
+// in sixteens; 128 tokens (eight rows an expert): 304 and 178 us.
 template <int DT> hipError_t run_dtype(const Int4Args& a, hipStream_t s) {
-  return a.pair ? run_tile<DT, 2>(a, s) : run_tile<DT, 1>(a, s);
+  const bool few = a.offsets ? a.rows <= 2 * (int64_t)a.E_loc : a.rows <= 4;
+  if (a.pair) return few ? run_group<DT, 2, 1, 4>(a, s) : run_group<DT, 2, 1, 16>(a, s);
+  return few ? run_group<DT, 1, 1, 4>(a, s) : run_group<DT, 1, 1, 16>(a, s);
 }
 
 }  // namespace
