@@ -17,16 +17,17 @@ from . import mok
 _DTYPES = {torch.float32: mok.MOK_DTYPE_F32, torch.bfloat16: mok.MOK_DTYPE_BF16, torch.float16: mok.MOK_DTYPE_F16}
 
 
-def _need(ok: bool, what: str):
+def _need(ok: bool, fn: str, what: str):
     if not ok:
-        raise ValueError(what)
+        raise ValueError(f"{fn}: {what}")
 
 
 def _on(fn: str, ref: torch.Tensor, *tensors):
     """Every tensor on the first one's GPU."""
-    _need(ref.is_cuda, f"{fn}: tensors on a GPU expected")
+    _need(ref.is_cuda, fn, "tensors on a GPU expected")
+    i = ref.get_device()
     for t in tensors:
-        _need(t is None or t.device == ref.device, f"{fn}: tensors on different devices")
+        _need(t is None or t.get_device() == i, fn, "tensors on different devices")
 
 
 def _ready(t):
@@ -39,15 +40,23 @@ def _ready(t):
 def _output(fn: str, out, shape, dtype, device):
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _need(tuple(out.shape) == tuple(shape) and out.dtype == dtype and out.device == device,
-          f"{fn}: out must be {dtype} {tuple(shape)} on {device}")
-    _need(out.is_contiguous() and out.data_ptr() % 16 == 0, f"{fn}: out must be contiguous and 16-byte aligned")
+    if tuple(out.shape) != shape or out.dtype != dtype or out.device != device:
+        raise ValueError(f"{fn}: out must be {dtype} {shape} on {device}")
+    _need(out.is_contiguous() and out.data_ptr() % 16 == 0, fn, "out must be contiguous and 16-byte aligned")
     return out
 
 
-def _call(f, device, *args):
-    with torch.cuda.device(device):
-        f(*args, torch.cuda.current_stream(device).cuda_stream)
+def _call(f, ref, *args):
+    """f(*args, stream) on ref's device, on that device's current stream (its
+    handle alone: building a torch Stream object takes longer than a small
+    call's other checks together)."""
+    i = ref.get_device()
+    stream = torch._C._cuda_getCurrentRawStream(i)
+    if i == torch.cuda.current_device():
+        f(*args, stream)
+    else:
+        with torch.cuda.device(i):
+            f(*args, stream)
 
 
 @dataclass
@@ -69,24 +78,33 @@ class PairMap:
         shapes = ((self.E,), (self.E + 1,), (self.T, self.k), (self.T * self.k,))
         for t, shape in zip((self.counts, self.offsets, self.row_of_pair, self.pair_of_row), shapes):
             _need(t.dtype == torch.int32 and tuple(t.shape) == shape and t.device == self.counts.device,
-                  "PairMap: int32 counts [E], offsets [E + 1], row_of_pair [T, k], pair_of_row [T * k] on one device")
+                  "PairMap", "int32 counts [E], offsets [E + 1], row_of_pair [T, k], pair_of_row [T * k] on one device")
+
+    @classmethod
+    def _of(cls, *fields):
+        """A map whose arrays are known to fit."""
+        m = object.__new__(cls)
+        (m.T, m.k, m.E, m.expert_begin, m.expert_end, m.counts, m.offsets, m.row_of_pair, m.pair_of_row) = fields
+        return m
 
 
 def sort_pairs(topk_idx: torch.Tensor, E: int, expert_begin: int = 0, expert_end: int | None = None) -> PairMap:
     """Sorts the pairs of int32 topk_idx [T, k] by expert, stably.  Indices
     outside [expert_begin, expert_end) (-1: dropped) get no row."""
     fn = "sort_pairs"
-    _need(topk_idx.dim() == 2 and topk_idx.dtype == torch.int32, f"{fn}: int32 topk_idx [T, k] expected")
+    _need(topk_idx.dim() == 2 and topk_idx.dtype == torch.int32, fn, "int32 topk_idx [T, k] expected")
     _on(fn, topk_idx)
     T, k = topk_idx.shape
     ee = E if expert_end is None else expert_end
-    dev = topk_idx.device
-    nws = mok.mok_sort_pairs_workspace_query(T, k, E)
-    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
-    m = PairMap(T, k, E, expert_begin, ee, *(torch.empty(s, dtype=torch.int32, device=dev)
-                                             for s in (E, E + 1, (T, k), T * k)))
-    _call(mok.mok_sort_pairs, dev, _ready(topk_idx), T, k, E, expert_begin, ee, m.counts, m.offsets, m.row_of_pair,
-          m.pair_of_row, ws)
+    nws = mok.mok_sort_pairs_workspace_query(T, k, E) // 4
+    # one allocation, each array on a 16-byte boundary
+    sizes = []
+    for n in (E, E + 1, T * k, T * k, nws):
+        sizes += (n, -n % 4)
+    buf = torch.empty(sum(sizes), dtype=torch.int32, device=topk_idx.device).split(sizes)
+    counts, offsets, row, pair, ws = buf[::2]
+    m = PairMap._of(T, k, E, expert_begin, ee, counts, offsets, row.view(T, k), pair)
+    _call(mok.mok_sort_pairs, topk_idx, _ready(topk_idx), T, k, E, expert_begin, ee, counts, offsets, row, pair, ws)
     return m
 
 
@@ -94,15 +112,16 @@ def _rows_args(fn: str, pmap: PairMap, gate, tokens, rows):
     """Checks one [T, d] tensor, one [rows, d] tensor (either may be None) and
     the gates against a pair map; returns (d, dtype code)."""
     ref = tokens if tokens is not None else rows
-    _need(ref.dim() == 2 and ref.dtype in _DTYPES, f"{fn}: fp32, bf16 or fp16 matrices expected")
+    dt = _DTYPES.get(ref.dtype)
+    _need(dt is not None and ref.dim() == 2, fn, "fp32, bf16 or fp16 matrices expected")
+    d = ref.shape[1]
+    _need(tokens is None or tuple(tokens.shape) == (pmap.T, d), fn, "token rows [T, d] expected")
+    _need(rows is None or (rows.dim() == 2 and rows.dtype == ref.dtype and rows.shape[1] == d),
+          fn, "expert rows [rows, d] of the tokens' type expected")
+    _need(gate is None or (gate.dtype == torch.float32 and gate.shape == pmap.row_of_pair.shape),
+          fn, "fp32 gate [T, k] expected")
     _on(fn, ref, tokens, rows, gate, pmap.row_of_pair)
-    _need(tokens is None or (tokens.dim() == 2 and tokens.shape[0] == pmap.T and tokens.dtype == ref.dtype and
-                             tokens.shape[1] == ref.shape[1]), f"{fn}: token rows [{pmap.T}, d] expected")
-    _need(rows is None or (rows.dim() == 2 and rows.dtype == ref.dtype and rows.shape[1] == ref.shape[1]),
-          f"{fn}: expert rows [rows, d] of the tokens' type expected")
-    _need(gate is None or (gate.dtype == torch.float32 and tuple(gate.shape) == (pmap.T, pmap.k)),
-          f"{fn}: fp32 gate [{pmap.T}, {pmap.k}] expected")
-    return ref.shape[1], _DTYPES[ref.dtype]
+    return d, dt
 
 
 def permute_rows(x: torch.Tensor, pmap: PairMap, gate: torch.Tensor | None = None,
@@ -114,7 +133,7 @@ def permute_rows(x: torch.Tensor, pmap: PairMap, gate: torch.Tensor | None = Non
     d, dt = _rows_args(fn, pmap, gate, x, out)
     rows = pmap.T * pmap.k if out is None else out.shape[0]
     out = _output(fn, out, (rows, d), x.dtype, x.device)
-    _call(mok.mok_permute_rows, x.device, _ready(x), _ready(gate), _ready(pmap.row_of_pair), pmap.T, pmap.k, d, dt,
+    _call(mok.mok_permute_rows, x, _ready(x), _ready(gate), _ready(pmap.row_of_pair), pmap.T, pmap.k, d, dt,
           rows, out)
     return out
 
@@ -126,7 +145,7 @@ def permute_rows_backward(dxp: torch.Tensor, pmap: PairMap, gate: torch.Tensor |
     d, dt = _rows_args(fn, pmap, gate, x, dxp)
     dx = torch.empty((pmap.T, d), dtype=dxp.dtype, device=dxp.device)
     dgate = None if x is None else torch.empty((pmap.T, pmap.k), dtype=torch.float32, device=dxp.device)
-    _call(mok.mok_permute_rows_backward, dxp.device, _ready(dxp), _ready(x), _ready(gate), _ready(pmap.row_of_pair),
+    _call(mok.mok_permute_rows_backward, dxp, _ready(dxp), _ready(x), _ready(gate), _ready(pmap.row_of_pair),
           pmap.T, pmap.k, d, dt, dxp.shape[0], dx, dgate)
     return dx, dgate
 
@@ -137,7 +156,7 @@ def unpermute_rows(y: torch.Tensor, pmap: PairMap, gate: torch.Tensor | None = N
     fn = "unpermute_rows"
     d, dt = _rows_args(fn, pmap, gate, None, y)
     out = _output(fn, out, (pmap.T, d), y.dtype, y.device)
-    _call(mok.mok_unpermute_rows, y.device, _ready(y), _ready(gate), _ready(pmap.row_of_pair), pmap.T, pmap.k, d, dt,
+    _call(mok.mok_unpermute_rows, y, _ready(y), _ready(gate), _ready(pmap.row_of_pair), pmap.T, pmap.k, d, dt,
           y.shape[0], out)
     return out
 
@@ -152,7 +171,7 @@ def unpermute_rows_backward(dout: torch.Tensor, pmap: PairMap, gate: torch.Tenso
     rows = y.shape[0] if y is not None else pmap.T * pmap.k if out is None else out.shape[0]
     dy = _output(fn, out, (rows, d), dout.dtype, dout.device)
     dgate = None if y is None else torch.empty((pmap.T, pmap.k), dtype=torch.float32, device=dout.device)
-    _call(mok.mok_unpermute_rows_backward, dout.device, _ready(dout), _ready(y), _ready(gate),
+    _call(mok.mok_unpermute_rows_backward, dout, _ready(dout), _ready(y), _ready(gate),
           _ready(pmap.row_of_pair), pmap.T, pmap.k, d, dt, rows, dy, dgate)
     return dy, dgate
 
@@ -170,11 +189,11 @@ class Int4Weights:
     def __post_init__(self):
         q, s, z = self.codes, self.scales, self.zeros
         _need(q.dim() == 3 and q.dtype == torch.uint8 and s.dim() == 3 and s.shape[:2] == q.shape[:2],
-              "Int4Weights: uint8 codes [E, N, K / 2] and scales [E, N, K / group] expected")
-        _need(s.dtype in (torch.bfloat16, torch.float16), "Int4Weights: bf16 or fp16 scales expected")
+              "Int4Weights", "uint8 codes [E, N, K / 2] and scales [E, N, K / group] expected")
+        _need(s.dtype in (torch.bfloat16, torch.float16), "Int4Weights", "bf16 or fp16 scales expected")
         _need(s.shape[2] > 0 and self.K % s.shape[2] == 0 and self.group in (32, 64, 128),
-              "Int4Weights: groups of 32, 64 or 128 expected")
-        _need(z is None or (z.dtype == torch.uint8 and z.shape == s.shape), "Int4Weights: uint8 zeros like the scales")
+              "Int4Weights", "groups of 32, 64 or 128 expected")
+        _need(z is None or (z.dtype == torch.uint8 and z.shape == s.shape), "Int4Weights", "uint8 zeros like the scales")
         _on("Int4Weights", q, s, z)
         self.codes, self.scales, self.zeros = _ready(q), _ready(s), _ready(z)
 
@@ -198,15 +217,15 @@ class Int4Weights:
 def quantize_int4(w: torch.Tensor, group: int = 128, symmetric: bool = True) -> Int4Weights:
     """4-bit weights of bf16 or fp16 w [N, K] or [E, N, K], in groups along K."""
     _need(w.dim() in (2, 3) and w.dtype in (torch.bfloat16, torch.float16),
-          "quantize_int4: bf16 or fp16 w [N, K] or [E, N, K] expected")
+          "quantize_int4", "bf16 or fp16 w [N, K] or [E, N, K] expected")
     _on("quantize_int4", w)
     w = _ready(w if w.dim() == 3 else w[None])
     E, N, K = w.shape
-    _need(group in (32, 64, 128) and K > 0 and K % group == 0, "quantize_int4: K a multiple of a group of 32, 64 or 128")
+    _need(group in (32, 64, 128) and K > 0 and K % group == 0, "quantize_int4", "K a multiple of a group of 32, 64 or 128")
     codes = torch.empty((E, N, K // 2), dtype=torch.uint8, device=w.device)
     scales = torch.empty((E, N, K // group), dtype=w.dtype, device=w.device)
     zeros = None if symmetric else torch.empty(scales.shape, dtype=torch.uint8, device=w.device)
-    _call(mok.mok_quantize_int4, w.device, w, E * N, K, group, _DTYPES[w.dtype], codes, scales, zeros)
+    _call(mok.mok_quantize_int4, w, w, E * N, K, group, _DTYPES[w.dtype], codes, scales, zeros)
     return Int4Weights(codes, scales, zeros)
 
 
@@ -220,23 +239,22 @@ def expert_matvec_int4(x: torch.Tensor, w: Int4Weights, pmap: PairMap | None = N
     one matrix and every row of x is its own."""
     fn = "expert_matvec_int4"
     _need(x.dim() == 2 and x.dtype == w.scales.dtype and x.shape[1] == w.K,
-          f"{fn}: x [rows, {w.K}] of the scales' type expected")
+          fn, "x [rows, K] of the scales' type expected")
     _on(fn, x, w.codes, None if w_up is None else w_up.codes, None if pmap is None else pmap.offsets)
     _need(w_up is None or (w_up.codes.shape == w.codes.shape and w_up.scales.shape == w.scales.shape and
                            w_up.scales.dtype == w.scales.dtype and (w_up.zeros is None) == (w.zeros is None)),
-          f"{fn}: w and w_up of one shape, group and kind expected")
+          fn, "w and w_up of one shape, group and kind expected")
     if pmap is None:
-        _need(w.E == 1 and not from_tokens, f"{fn}: one matrix expected without a pair map")
+        _need(w.E == 1 and not from_tokens, fn, "one matrix expected without a pair map")
         rows, k, E, eb, ee = x.shape[0], 1, 1, 0, 1
     else:
         rows, k, E, eb, ee = pmap.T * pmap.k, pmap.k, pmap.E, pmap.expert_begin, pmap.expert_end
-        _need(w.E == ee - eb, f"{fn}: weights of {ee - eb} experts expected")
-        _need(x.shape[0] == (pmap.T if from_tokens else rows), f"{fn}: x of {pmap.T if from_tokens else rows} rows "
-                                                               "expected")
+        _need(w.E == ee - eb, fn, "weights of the map's local experts expected")
+        _need(x.shape[0] == (pmap.T if from_tokens else rows), fn, "x of T token rows or T * k sorted rows expected")
     out = _output(fn, out, (rows, w.N), x.dtype, x.device)
     cfg = mok.mok_int4_config(rows, x.shape[0], k, E, eb, ee, w.N, w.K, w.group, _DTYPES[x.dtype])
     parts = lambda m: None if m is None else (m.codes, m.scales, m.zeros)
-    _call(mok.mok_expert_matvec_int4, x.device, _ready(x), _ready(pmap.pair_of_row) if from_tokens else None,
+    _call(mok.mok_expert_matvec_int4, x, _ready(x), _ready(pmap.pair_of_row) if from_tokens else None,
           None if pmap is None else _ready(pmap.offsets), parts(w), parts(w_up), cfg, out)
     return out
 
