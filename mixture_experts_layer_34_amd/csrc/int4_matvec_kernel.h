@@ -110,6 +110,20 @@ __device__ __forceinline__ void spread_quarters(uint32_t v, uint32_t (&o)[4]) {
   o[3] = b[1];
 }
 
+// Inclusive sum over the lanes of a wave: within rows of 16 lanes by shifts,
+// then the row before's and the half before's total.
+template <int CTRL, int ROWS> __device__ __forceinline__ int dpp_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ int wave_prefix(int v) {
+  v = dpp_add<0x111, 0xf>(v);  // row_shr 1
+  v = dpp_add<0x112, 0xf>(v);  // row_shr 2
+  v = dpp_add<0x114, 0xf>(v);  // row_shr 4
+  v = dpp_add<0x118, 0xf>(v);  // row_shr 8
+  v = dpp_add<0x142, 0xa>(v);  // row_bcast 15 into rows 1 and 3
+  return dpp_add<0x143, 0xc>(v);  // row_bcast 31 into rows 2 and 3
+}
+
 // NM matrices (a pair for SwiGLU), NG groups of 16 weight rows of each, tiles
 // of RT rows, groups of GS; of a workgroup's waves KS split K and NW lie side
 // by side along N; x is staged SCH chunks at a time.
@@ -129,6 +143,7 @@ void int4_matvec_kernel(Int4Args a, const int32_t* __restrict__ offsets,
   constexpr int XP = SCH * 16;              // 16-byte pieces of a staged row
   constexpr int NT = 64 * KS * NW;
   constexpr int XA = (RT * XP + NT - 1) / NT;  // pieces each thread stages
+  constexpr int RING = 4;                   // chunks of codes in registers
   static_assert(JC >= 1 && JC * KS == SCH && (JC == 1 || JC % 2 == 0), "every wave has chunks of each stage");
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int kr = wave / NW, nw = wave % NW;
@@ -157,12 +172,7 @@ void int4_matvec_kernel(Int4Args a, const int32_t* __restrict__ offsets,
         s_row[e] = lo;
         s_end[e] = hi;
       }
-      int s = n;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int v = __shfl_up(s, o, 64);
-        if (lane >= o) s += v;
-      }
+      const int s = wave_prefix(n);
       if (lane == 63) wsum[wave] = s;
       __syncthreads();
       int base = carry;
@@ -215,10 +225,10 @@ void int4_matvec_kernel(Int4Args a, const int32_t* __restrict__ offsets,
       rz[m] = buffer(has_zeros ? a.zeros[m] + wrow * G : nullptr, has_zeros ? (int64_t)(N - n0) * G : 0);
     }
 
-    // A ring of four chunks of codes, two of them (a whole cache line of each
-    // weight row) on their way while two are multiplied.  Loads past K read
+    // A ring of chunks of codes, all but two of them on their way while two (a
+    // whole cache line of each weight row) are multiplied.  Loads past K read
     // zeros.
-    u32x4_t wv[4][NB];
+    u32x4_t wv[RING][NB];
     uint32_t sv[NB][SW], zv[NB];  // of four chunks, lane quarter q holding chunk q's
     auto load_codes = [&](int buf, int i) {
       const int k = chunk_of(i) * kChunk + 32 * g4;
@@ -265,8 +275,8 @@ void int4_matvec_kernel(Int4Args a, const int32_t* __restrict__ offsets,
         }
       }
     };
-    load_codes(0, 0);
-    load_codes(1, 1);
+#pragma unroll
+    for (int i = 0; i < RING - 2; ++i) load_codes(i, i);
     load_scales(0);
     // x by stages of SCH chunks through LDS: a wave takes 64 pieces of 16
     // bytes of one row at a time, puts them in the codes' order and the row
@@ -321,22 +331,24 @@ void int4_matvec_kernel(Int4Args a, const int32_t* __restrict__ offsets,
 
     const uint32_t ones[4] = {Mma<DT>::kOnes, Mma<DT>::kOnes, Mma<DT>::kOnes, Mma<DT>::kOnes};
     int cur = 0;
-    for (int i0 = 0; i0 < nloc; i0 += 4) {
-      uint32_t sc[NB][SW][4], zc[NB][4];  // the four chunks' scales and 16 + zeros, in every lane quarter
+    for (int i0 = 0; i0 < nloc; i0 += RING) {
+      uint32_t sc[NB][SW][4], zc[NB][4];  // four chunks' scales and 16 + zeros, in every lane quarter
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-#pragma unroll
-        for (int w = 0; w < SW; ++w) spread_quarters(sv[b][w], sc[b][w]);
-        spread_quarters(zv[b] + 0x10101010u, zc[b]);
-      }
-      load_scales(i0 + 4);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < RING; ++j) {
         if (i0 + j >= nloc) break;
+        if (j % 4 == 0) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int w = 0; w < SW; ++w) spread_quarters(sv[b][w], sc[b][w]);
+            spread_quarters(zv[b] + 0x10101010u, zc[b]);
+          }
+          load_scales(i0 + j + 4);
+        }
         if (j % JC == 0) load_x((i0 + j) / JC + 1);
         if (j % 2 == 0) {
-          load_codes((j + 2) % 4, i0 + j + 2);
-          load_codes((j + 3) % 4, i0 + j + 3);
+          load_codes((j + RING - 2) % RING, i0 + j + RING - 2);
+          load_codes((j + RING - 1) % RING, i0 + j + RING - 1);
         }
         __builtin_amdgcn_sched_barrier(0);
         if (chunk_of(i0 + j) < nch) {
@@ -352,9 +364,9 @@ void int4_matvec_kernel(Int4Args a, const int32_t* __restrict__ offsets,
             float sf[NB], zz[NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-              const uint32_t sw = sc[b][i / 2][j];
+              const uint32_t sw = sc[b][i / 2][j % 4];
               sf[b] = i % 2 ? Elem<DT>::hi(sw) : Elem<DT>::lo(sw);
-              zz[b] = (float)((zc[b][j] >> (8 * i)) & 255u);
+              zz[b] = (float)((zc[b][j % 4] >> (8 * i)) & 255u);
             }
             constexpr int GST = 4 / NSC;  // MFMA steps of a group
             const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
@@ -367,7 +379,6 @@ void int4_matvec_kernel(Int4Args a, const int32_t* __restrict__ offsets,
               for (int b = 0; b < NB; ++b) Mma<DT>::place(wv[j][b][st], mask, sixteen, wd[b]);
 #pragma unroll
               for (int m = 0; m < MT; ++m) {
-                if (MT > 1 && 16 * m >= nrow) continue;
                 if constexpr (!QUAD) xq = *reinterpret_cast<const u32x4_t*>(xb + (16 * m + n16) * XROW + 64 * st);
                 const uint32_t xd[4] = {xq[0], xq[1], xq[2], xq[3]};
                 ax[m] = Mma<DT>::mfma(xd, ones, first ? zero : ax[m]);
@@ -384,7 +395,6 @@ void int4_matvec_kernel(Int4Args a, const int32_t* __restrict__ offsets,
             if constexpr (!QUAD) {
 #pragma unroll
               for (int m = 0; m < MT; ++m) {
-                if (MT > 1 && 16 * m >= nrow) continue;
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -457,40 +467,55 @@ hipError_t run_cfg(const Int4Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Waves along K.  A wave by itself on its columns needs no sum and no more
-// barriers than x's, so K is split only as far as it takes to have eight waves
-// for each compute unit: gate / up of one token (768 columns groups of 8
-// experts) 22.1 / 18.1 / 16.5 / 20.1 us for splits of 1 / 2 / 4 / 8, a dense
-// 4099 x 7168 product of three rows 23.8 / 15.2 / 11.9 / 10.2 us; sixteen
-// tokens' gate / up (about 7,900 groups) 137 / 132 / 164 / 262 us.
-template <int DT, int NM, int NG, int RT, int GS> hipError_t run(const Int4Args& a, hipStream_t s) {
-  // expected tiles: every expert that can have a row, and whole tiles past those
-  const int64_t tiles = (a.E_loc < a.rows ? a.E_loc : a.rows) + a.rows / RT - a.rows / RT / 2;
-  const int64_t waves = (a.offsets ? tiles : (a.rows + RT - 1) / RT) * ((a.N + 16 * NG - 1) / (16 * NG));
-  constexpr int64_t kWanted = 8 * kNumCUs;
-  if (waves * 4 < kWanted) return run_cfg<DT, NM, NG, RT, GS, 8, 1, 8>(a, s);
-  if (waves * 2 < kWanted) return run_cfg<DT, NM, NG, RT, GS, 4, 1, 4>(a, s);
-  if (waves < kWanted) return run_cfg<DT, NM, NG, RT, GS, 2, 2, 4>(a, s);
-  return run_cfg<DT, NM, NG, RT, GS, 1, 4, 4>(a, s);
+constexpr int64_t kWanted = 8 * kNumCUs;  // waves that fill the device
+
+// Waves of a call whose waves do not split K: the tiles it can expect (every
+// expert with rows has a last tile half full on average) times N's columns.
+inline int64_t waves_of(const Int4Args& a, int rt, int ng) {
+  const int64_t experts = a.E_loc < a.rows ? a.E_loc : a.rows;
+  const int64_t tiles = a.offsets ? experts + a.rows / rt / 2 : (a.rows + rt - 1) / rt;
+  return tiles * ((a.N + 16 * ng - 1) / (16 * ng));
 }
 
-template <int DT, int NM, int NG, int RT> hipError_t run_group(const Int4Args& a, hipStream_t s) {
+// A wave by itself on its columns needs no sum and no more barriers than x's,
+// so K is split only as far as it takes to fill the device: gate / up of one
+// token (768 groups of 16 columns) 22.1 / 18.1 / 16.5 / 20.1 us for splits of
+// 1 / 2 / 4 / 8, a dense 4099 x 7168 product of three rows 23.8 / 15.2 / 11.9 /
+// 10.2 us; sixteen tokens' gate / up (7,900 groups) 137 / 132 / 164 / 262 us.
+template <int DT, int NM, int RT, int GS> hipError_t run(const Int4Args& a, hipStream_t s) {
+  const int64_t waves = waves_of(a, RT, 1);
+  if (waves * 4 < kWanted) return run_cfg<DT, NM, 1, RT, GS, 8, 1, 8>(a, s);
+  if (waves * 2 < kWanted) return run_cfg<DT, NM, 1, RT, GS, 4, 1, 4>(a, s);
+  if (waves < kWanted) return run_cfg<DT, NM, 1, RT, GS, 2, 2, 4>(a, s);
+  return run_cfg<DT, NM, 1, RT, GS, 1, 4, 4>(a, s);
+}
+
+// Rows per tile, from an expert's rows on average: four up to two rows (x then
+// costs a quarter; experts with more take several tiles), sixteen, and
+// thirty-two past sixteen rows, where taking the codes apart bounds the
+// product, if that still fills the device.  Gate / up of 128 experts: 16
+// tokens (a row an expert) 137 us in fours, 155 in sixteens; 128 tokens (eight
+// rows) 304 / 178 us; of 8 experts with 128 rows each 88 us in sixteens, 73 in
+// thirty-twos.  A single matrix with sixteen rows or more takes 32 columns a
+// wave on the same condition (128 experts' down product of 128 tokens 115 ->
+// 108 us): x is then read once for both.
+template <int DT, int GS> hipError_t run_group(const Int4Args& a, hipStream_t s) {
+  const int64_t experts = a.offsets ? a.E_loc : 1;
+  const int ng = a.pair ? 1 : 2;
+  if (a.rows <= (a.offsets ? 2 : 4) * experts) return a.pair ? run<DT, 2, 4, GS>(a, s) : run<DT, 1, 4, GS>(a, s);
+  if (a.rows > 16 * experts && waves_of(a, 32, ng) >= kWanted)
+    return a.pair ? run_cfg<DT, 2, 1, 32, GS, 1, 4, 4>(a, s) : run_cfg<DT, 1, 2, 32, GS, 1, 4, 4>(a, s);
+  if (!a.pair && waves_of(a, 16, 2) >= kWanted) return run_cfg<DT, 1, 2, 16, GS, 1, 4, 4>(a, s);
+  return a.pair ? run<DT, 2, 16, GS>(a, s) : run<DT, 1, 16, GS>(a, s);
+}
+
+template <int DT> hipError_t run_dtype(const Int4Args& a, hipStream_t s) {
   switch (a.group) {
-    case 32: return run<DT, NM, NG, RT, 32>(a, s);
-    case 64: return run<DT, NM, NG, RT, 64>(a, s);
-    case 128: return run<DT, NM, NG, RT, 128>(a, s);
+    case 32: return run_group<DT, 32>(a, s);
+    case 64: return run_group<DT, 64>(a, s);
+    case 128: return run_group<DT, 128>(a, s);
   }
   return hipErrorInvalidValue;
-}
-
-// Rows per tile: four while an expert has two rows or fewer on average (its
-// x costs a quarter; experts with more take several tiles), else sixteen.
-// Gate / up of 128 experts, 16 tokens (a row an expert): 137 us in fours, 155
-// in sixteens; 128 tokens (eight rows an expert): 304 and 178 us.
-template <int DT> hipError_t run_dtype(const Int4Args& a, hipStream_t s) {
-  const bool few = a.offsets ? a.rows <= 2 * (int64_t)a.E_loc : a.rows <= 4;
-  if (a.pair) return few ? run_group<DT, 2, 1, 4>(a, s) : run_group<DT, 2, 1, 16>(a, s);
-  return few ? run_group<DT, 1, 1, 4>(a, s) : run_group<DT, 1, 1, 16>(a, s);
 }
 
 }  // namespace
