@@ -96,14 +96,11 @@ def sort_pairs(topk_idx: torch.Tensor, E: int, expert_begin: int = 0, expert_end
     _on(fn, topk_idx)
     T, k = topk_idx.shape
     ee = E if expert_end is None else expert_end
-    nws = mok.mok_sort_pairs_workspace_query(T, k, E) // 4
-    # one allocation, each array on a 16-byte boundary
-    sizes = []
-    for n in (E, E + 1, T * k, T * k, nws):
-        sizes += (n, -n % 4)
-    buf = torch.empty(sum(sizes), dtype=torch.int32, device=topk_idx.device).split(sizes)
-    counts, offsets, row, pair, ws = buf[::2]
-    m = PairMap._of(T, k, E, expert_begin, ee, counts, offsets, row.view(T, k), pair)
+    dev = topk_idx.device
+    nws = mok.mok_sort_pairs_workspace_query(T, k, E)
+    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
+    counts, offsets, row, pair = (torch.empty(s, dtype=torch.int32, device=dev) for s in (E, E + 1, (T, k), T * k))
+    m = PairMap._of(T, k, E, expert_begin, ee, counts, offsets, row, pair)
     _call(mok.mok_sort_pairs, topk_idx, _ready(topk_idx), T, k, E, expert_begin, ee, counts, offsets, row, pair, ws)
     return m
 

@@ -300,7 +300,24 @@ MATVEC = [  # T, k, E, N, K, group, zeros, pair, dtype
 ]
 
 
-@pytest.mark.parametrize("T,k,E,N,K,group,zeros,pair,dt", MATVEC)
+# Every way the launcher shares out a call: tiles of 4 rows (at most two an
+# expert on average), 16 and 32, K over 1, 2, 4 and 8 waves, one and two column
+# groups a wave; narrow K, so that N can be wide.
+VARIANTS = [
+    (32, 8, 128, 208, 96, 32, True, False, "bf16"), (32, 8, 128, 112, 160, 32, True, True, "f16"),
+    (32, 8, 128, 64, 256, 128, False, True, "bf16"), (4, 8, 16, 40, 2048, 64, True, False, "bf16"),
+    (32, 4, 8, 2740, 64, 64, True, True, "bf16"), (32, 4, 8, 1500, 192, 64, False, True, "f16"),
+    (32, 4, 8, 800, 128, 32, True, True, "bf16"), (32, 4, 8, 72, 2176, 128, True, True, "bf16"),
+    (32, 4, 8, 2740, 96, 32, True, False, "bf16"), (32, 4, 8, 1500, 128, 128, False, False, "bf16"),
+    (32, 4, 8, 800, 160, 32, True, False, "f16"), (32, 4, 8, 72, 3200, 64, True, False, "bf16"),
+    (32, 4, 8, 5503, 96, 32, True, False, "bf16"), (32, 4, 8, 5504, 128, 128, False, False, "f16"),
+    (64, 2, 2, 8210, 160, 32, True, True, "bf16"), (64, 2, 2, 8208, 256, 128, False, True, "f16"),
+    (64, 2, 2, 16411, 64, 64, True, False, "bf16"), (64, 2, 2, 16416, 96, 32, True, False, "f16"),
+    (300, 8, 1024, 17, 64, 64, True, False, "bf16"),
+]
+
+
+@pytest.mark.parametrize("T,k,E,N,K,group,zeros,pair,dt", MATVEC + VARIANTS)
 @pytest.mark.parametrize("from_tokens", [False, True])
 def test_expert_matvec(T, k, E, N, K, group, zeros, pair, dt, from_tokens):
     note(f"matvec T={T} k={k} E={E} N={N} K={K} g={group} zeros={zeros} pair={pair} {dt} tokens={from_tokens}")
@@ -328,6 +345,7 @@ def test_expert_matvec(T, k, E, N, K, group, zeros, pair, dt, from_tokens):
     (3, 130, 2048, 64, False, True, "bf16"), (5, 64, 1408, 128, False, False, "bf16"), (8, 96, 512, 32, True, True, "f16"),
     (16, 50, 736, 32, True, False, "bf16"), (17, 64, 256, 32, False, False, "bf16"), (33, 64, 640, 128, True, True, "bf16"),
     (64, 256, 1024, 64, False, False, "f16"), (65, 48, 128, 32, True, False, "bf16"), (200, 80, 384, 128, True, False, "bf16"),
+    (70, 21860, 96, 32, True, False, "bf16"), (70, 10923, 128, 128, False, True, "f16"),
 ])
 def test_dense_matvec(rows, N, K, group, zeros, pair, dt):
     note(f"dense rows={rows} N={N} K={K} g={group} {dt}")
