@@ -602,7 +602,8 @@ mok_status mok_unpermute_rows_backward(const void* dout, const void* y, const fl
  *   codes   [E_loc, N, K/2] bytes; element 2i of a row in the low nibble of
  *           byte i, element 2i + 1 in the high nibble (0..15)
  *   scales  dtype [E_loc, N, K/group], finite
- *   zeros   uint8 [E_loc, N, K/group], or NULL: 8 everywhere (symmetric) */
+ *   zeros   uint8 [E_loc, N, K/group], 0..15, or NULL: 8 everywhere
+ *           (symmetric) */
 typedef struct mok_int4_weights {
   const uint8_t* codes;
   const void* scales;
@@ -617,7 +618,7 @@ typedef struct mok_int4_config {
   int32_t expert_begin;      /* first local expert                              */
   int32_t expert_end;        /* one past the last local expert                  */
   int32_t N;                 /* output width (any)                              */
-  int32_t K;                 /* input width, a multiple of group                */
+  int32_t K;                 /* input width, a multiple of group, up to 2^20    */
   int32_t group;             /* 32, 64 or 128                                   */
   int32_t dtype;             /* mok_dtype of x, scales and out: BF16 or F16     */
 } mok_int4_config;

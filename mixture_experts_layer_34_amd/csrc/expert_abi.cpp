@@ -101,7 +101,7 @@ mok_status mok_expert_matvec_int4(const void* x, const int32_t* pair_of_row, con
   if (c.rows < 0 || c.rows > (1 << 24) || c.x_rows < 0 || c.x_rows > (1 << 24) || c.k < 1 || c.N < 1 || c.K < 1) return MOK_ERR_INVALID_ARG;
   if (bad_experts(c.E, c.expert_begin, c.expert_end)) return MOK_ERR_INVALID_ARG;
   if (c.group != 32 && c.group != 64 && c.group != 128) return MOK_ERR_INVALID_ARG;
-  if (c.K % c.group) return MOK_ERR_INVALID_ARG;
+  if (c.K % c.group || c.K > (1 << 20)) return MOK_ERR_INVALID_ARG;
   if (c.dtype == MOK_DTYPE_F32) return MOK_ERR_UNSUPPORTED;
   if (c.dtype != MOK_DTYPE_BF16 && c.dtype != MOK_DTYPE_F16) return MOK_ERR_INVALID_ARG;
   // x and one expert's codes are addressed in 32 bits

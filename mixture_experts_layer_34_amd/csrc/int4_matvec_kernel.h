@@ -18,17 +18,37 @@
 //
 // v_mfma_f32_16x16x32: A = the tile's rows of x (lane: row lane % 16, K
 // 8 (lane / 16) + i), B = weight rows (lane: n = lane % 16, same K), result:
-// n = lane % 16, MFMA rows 4 (lane / 16) + i.  Tile row r sits on MFMA row
-// 4 (r % 4) + r / 4, so that four rows fill only i = 0.  A lane loads 16 bytes
-// of one weight row (32 codes; its wave 64 bytes of 16 rows, K 128 of them):
+// n = lane % 16, MFMA rows 4 (lane / 16) + i.  A lane loads 16 bytes of one
+// weight row (32 codes; its wave 64 bytes of 16 rows, K 128 of them, a chunk):
 // lane quarter g then holds K [32 g, 32 g + 32) and a step of the MFMA would
 // mix four groups of 32, so the 4 x 4 words of the four quarters are
-// transposed by lane swaps (two per pair of words).  The eight codes of a word
-// come out as the pairs (0,4) (1,5) (2,6) (3,7); x is put in the same order.
+// transposed by lane swaps (one per word).  The eight codes of a word come out
+// as the pairs (0,4) (1,5) (2,6) (3,7); x is put in the same order.
 //
-// A workgroup takes one (row tile, 16 NG weight rows) unit; its waves split K
-// and their fp32 sums meet in LDS, added in wave order: the same bits on every
-// run.
+// Tile row r sits on MFMA row 4 (r % 4) + r / 4 % 4.  In tiles of four rows
+// the quad of MFMA rows 4 r .. 4 r + 3 belongs to row r, its lanes holding x
+// of the chunk's steps 0 .. 3: step st's result st is the product of step st
+// with itself (the others are products of unlike steps, and dropped), so one
+// load of x serves the four steps.
+//
+// A workgroup takes one (row tile, 16 NG NW weight rows) unit.  Its waves lie
+// side by side along N, sharing the tile's x through LDS (a lane's own load of
+// x touches sixteen rows, as many cache lines as its codes: with those loads
+// straight from cache 128 experts' gate / up of 128 tokens took 233 us, 178
+// through LDS, against 156 for the codes alone), or split K where there are
+// too few units, their fp32 sums then meeting in LDS, added in wave order: the
+// same bits on every run.
+//
+// Measured: gate / up of 128 experts (d 4096, F 1536) 177 us for 128 tokens
+// (groups of 128; 4.7 TB/s of codes and scales), 137 us for 16 tokens (82
+// experts, groups of 32 with zero points; 4.5 TB/s), 16.2 us for one (8
+// experts; 3.2 TB/s, 6 us of it the launch and the first loads).  A deeper
+// ring (eight chunks) changed nothing or lost up to 20 %, all of x in LDS at
+// once won 0.3 us at three rows and lost 10 % at sixteen tokens' down product,
+// group sums of x taken while staging in place of the products with ones lost
+// 2 to 25 %, non-temporal loads of the codes nothing.  With 64 rows on one
+// matrix (4096 x 8192: 23.6 us) the two thousand waves spend two thirds of
+// their issue slots taking the codes apart, once for each sixteen rows.
 #pragma once
 #include "elem.h"
 #include "int4_matvec.h"
@@ -128,8 +148,7 @@ __device__ __forceinline__ int wave_prefix(int v) {
 // of RT rows, groups of GS; of a workgroup's waves KS split K and NW lie side
 // by side along N; x is staged SCH chunks at a time.
 template <int DT, int NM, int NG, int RT, int GS, int KS, int NW, int SCH>
-__global__ __launch_bounds__(64 * KS * NW)
-void int4_matvec_kernel(Int4Args a, const int32_t* __restrict__ offsets,
+__global__ __launch_bounds__(64 * KS * NW) void int4_matvec_kernel(Int4Args a, const int32_t* __restrict__ offsets,
                                                                    const int32_t* __restrict__ pair_of_row) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NB = NM * NG;

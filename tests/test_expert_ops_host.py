@@ -90,8 +90,10 @@ def _matvec(cfg_over=None, **over):
     dict(rows=-1), dict(rows=(1 << 24) + 1), dict(x_rows=-1), dict(x_rows=(1 << 24) + 1), dict(k=0), dict(E=0),
     dict(E=1025), dict(expert_begin=-1), dict(expert_begin=4), dict(expert_end=5), dict(N=0), dict(K=0),
     dict(K=120), dict(K=96, group=64), dict(group=16), dict(group=256), dict(dtype=3),
+    dict(K=(1 << 20) + 128, x_rows=1, rows=1), dict(rows=1 << 24, N=4096),
     dict(x_rows=1 << 23, K=128),            # x of 2 GiB
     dict(N=1 << 20, K=4096),                # an expert's codes of 2 GiB
+    dict(N=1 << 19, K=4096, E=257, expert_end=257),   # all experts' codes of 256 GiB
 ])
 def test_matvec_refuses_shapes(cfg):
     assert _matvec(cfg) == BAD

@@ -373,6 +373,18 @@ def test_matvec_exact_integers():
         assert torch.equal(X.expert_matvec_int4(x, w), ref.to(DT[dt]))
 
 
+def test_matvec_subnormal_inputs():
+    """fp16 inputs below the normal range count with their value: multiples of
+    2^-24 up to 2^-21, scales of 2^14, again exact sums."""
+    K, N, rows = 256, 64, 5
+    w = _weights(_gen(3), 1, N, K, 64, True, "f16")
+    w.scales.fill_(2.0 ** 14)
+    x = (torch.randint(-8, 9, (rows, K), generator=_gen(2)).double() * 2.0 ** -24).half().cuda()
+    ref = x.double() @ _unpack(w)[0][0].t()
+    assert float(ref.abs().max()) > 0
+    assert torch.equal(X.expert_matvec_int4(x, w), ref.half())
+
+
 def test_matvec_local_experts_and_bad_maps():
     """An expert-parallel share: weights of the local experts only; and offsets
     and pairs that leave their buffers are cut, not followed."""
