@@ -1,5 +1,5 @@
 // Element types of the separate expert operators: storage, and vectors of VE
-// consecutive elements moved as one access.
+// consecutive elements moved as one access; and a wave's prefix sum.
 #pragma once
 #include "mok_device.h"
 
@@ -66,5 +66,19 @@ template <int DT, int VE> struct Vec {
     return v;
   }
 };
+
+// Inclusive sum over the lanes of a wave: within rows of 16 lanes by shifts,
+// then the row before's and the half before's total.
+template <int CTRL, int ROWS> __device__ __forceinline__ int dpp_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ int wave_prefix(int v) {
+  v = dpp_add<0x111, 0xf>(v);  // row_shr 1
+  v = dpp_add<0x112, 0xf>(v);  // row_shr 2
+  v = dpp_add<0x114, 0xf>(v);  // row_shr 4
+  v = dpp_add<0x118, 0xf>(v);  // row_shr 8
+  v = dpp_add<0x142, 0xa>(v);  // row_bcast 15 into rows 1 and 3
+  return dpp_add<0x143, 0xc>(v);  // row_bcast 31 into rows 2 and 3
+}
 
 }  // namespace mok

@@ -130,20 +130,6 @@ __device__ __forceinline__ void spread_quarters(uint32_t v, uint32_t (&o)[4]) {
   o[3] = b[1];
 }
 
-// Inclusive sum over the lanes of a wave: within rows of 16 lanes by shifts,
-// then the row before's and the half before's total.
-template <int CTRL, int ROWS> __device__ __forceinline__ int dpp_add(int v) {
-  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
-}
-__device__ __forceinline__ int wave_prefix(int v) {
-  v = dpp_add<0x111, 0xf>(v);  // row_shr 1
-  v = dpp_add<0x112, 0xf>(v);  // row_shr 2
-  v = dpp_add<0x114, 0xf>(v);  // row_shr 4
-  v = dpp_add<0x118, 0xf>(v);  // row_shr 8
-  v = dpp_add<0x142, 0xa>(v);  // row_bcast 15 into rows 1 and 3
-  return dpp_add<0x143, 0xc>(v);  // row_bcast 31 into rows 2 and 3
-}
-
 // NM matrices (a pair for SwiGLU), NG groups of 16 weight rows of each, tiles
 // of RT rows, groups of GS; of a workgroup's waves KS split K and NW lie side
 // by side along N; x is staged SCH chunks at a time.

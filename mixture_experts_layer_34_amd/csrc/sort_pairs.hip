@@ -12,7 +12,7 @@
 // inside its wave is the count before plus the lower lanes'.  The counts'
 // prefix over waves, chunks and experts turns ranks into rows.  Bound by
 // latency: 4 bytes read and 8 written per pair.
-#include "mok_device.h"
+#include "elem.h"
 #include "pair_ops.h"
 
 namespace mok {
@@ -69,12 +69,7 @@ __device__ __forceinline__ void walk(SortShared& sh, const int32_t* __restrict__
 // Exclusive prefix over the workgroup's 1024 threads; the sum in sh.total.
 __device__ __forceinline__ int block_prefix(SortShared& sh, int v) {
   const int lane = lane_id(), w = threadIdx.x >> 6;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(x, o, 64);
-    if (lane >= o) x += u;
-  }
+  const int x = wave_prefix(v);
   if (lane == 63) sh.wsum[w] = x;
   __syncthreads();
   int base = 0, tot = 0;
@@ -114,12 +109,7 @@ __global__ __launch_bounds__(256) void column_prefix_kernel(int32_t* __restrict_
   for (int64_t c0 = 0; c0 < nch; c0 += 256) {
     const int64_t c = c0 + threadIdx.x;
     const int v = c < nch ? table[c * E + e] : 0;
-    int x = v;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(x, o, 64);
-      if (lane >= o) x += u;
-    }
+    const int x = wave_prefix(v);
     if (lane == 63) wsum[w] = x;
     __syncthreads();
     int base = carry;

@@ -174,41 +174,32 @@ def unpermute_rows_backward(dout: torch.Tensor, pmap: PairMap, gate: torch.Tenso
 
 
 # ------------------------------------------------------------------ 4-bit integer weights
-@dataclass
+@dataclass(frozen=True)
 class Int4Weights:
     """Matrices [E, N, K] in 4-bit integers: uint8 codes [E, N, K / 2] (two per
     byte, the lower element in the low nibble), scales [E, N, K / group] in the
-    activations' type, and uint8 zeros like the scales (None: 8 everywhere)."""
+    activations' type, and uint8 zeros (0..15) like the scales (None: 8
+    everywhere)."""
     codes: torch.Tensor
     scales: torch.Tensor
     zeros: torch.Tensor | None = None
 
     def __post_init__(self):
+        fn = "Int4Weights"
         q, s, z = self.codes, self.scales, self.zeros
-        _need(q.dim() == 3 and q.dtype == torch.uint8 and s.dim() == 3 and s.shape[:2] == q.shape[:2],
-              "Int4Weights", "uint8 codes [E, N, K / 2] and scales [E, N, K / group] expected")
-        _need(s.dtype in (torch.bfloat16, torch.float16), "Int4Weights", "bf16 or fp16 scales expected")
-        _need(s.shape[2] > 0 and self.K % s.shape[2] == 0 and self.group in (32, 64, 128),
-              "Int4Weights", "groups of 32, 64 or 128 expected")
-        _need(z is None or (z.dtype == torch.uint8 and z.shape == s.shape), "Int4Weights", "uint8 zeros like the scales")
-        _on("Int4Weights", q, s, z)
-        self.codes, self.scales, self.zeros = _ready(q), _ready(s), _ready(z)
-
-    @property
-    def E(self):
-        return self.codes.shape[0]
-
-    @property
-    def N(self):
-        return self.codes.shape[1]
-
-    @property
-    def K(self):
-        return 2 * self.codes.shape[2]
-
-    @property
-    def group(self):
-        return self.K // self.scales.shape[2]
+        _need(q.dim() == 3 and q.dtype == torch.uint8 and s.dim() == 3 and s.shape[:2] == q.shape[:2], fn,
+              "uint8 codes [E, N, K / 2] and scales [E, N, K / group] expected")
+        _need(s.dtype in (torch.bfloat16, torch.float16), fn, "bf16 or fp16 scales expected")
+        E, N, K = q.shape[0], q.shape[1], 2 * q.shape[2]
+        group = K // max(s.shape[2], 1)
+        _need(group in (32, 64, 128) and group * s.shape[2] == K, fn, "groups of 32, 64 or 128 expected")
+        _need(z is None or (z.dtype == torch.uint8 and z.shape == s.shape), fn, "uint8 zeros like the scales")
+        _on(fn, q, s, z)
+        q, s, z = _ready(q), _ready(s), _ready(z)
+        # the arrays cannot be replaced, so the C view of them is made once
+        for name, v in (("codes", q), ("scales", s), ("zeros", z), ("E", E), ("N", N), ("K", K), ("group", group),
+                        ("_c", mok.int4_weights(q, s, z))):
+            object.__setattr__(self, name, v)
 
 
 def quantize_int4(w: torch.Tensor, group: int = 128, symmetric: bool = True) -> Int4Weights:
@@ -238,9 +229,10 @@ def expert_matvec_int4(x: torch.Tensor, w: Int4Weights, pmap: PairMap | None = N
     _need(x.dim() == 2 and x.dtype == w.scales.dtype and x.shape[1] == w.K,
           fn, "x [rows, K] of the scales' type expected")
     _on(fn, x, w.codes, None if w_up is None else w_up.codes, None if pmap is None else pmap.offsets)
-    _need(w_up is None or (w_up.codes.shape == w.codes.shape and w_up.scales.shape == w.scales.shape and
-                           w_up.scales.dtype == w.scales.dtype and (w_up.zeros is None) == (w.zeros is None)),
-          fn, "w and w_up of one shape, group and kind expected")
+    if w_up is not None:
+        _need(w_up.codes.shape == w.codes.shape and w_up.scales.shape == w.scales.shape and
+              w_up.scales.dtype == w.scales.dtype and (w_up.zeros is None) == (w.zeros is None), fn,
+              "w and w_up of one shape, group and kind expected")
     if pmap is None:
         _need(w.E == 1 and not from_tokens, fn, "one matrix expected without a pair map")
         rows, k, E, eb, ee = x.shape[0], 1, 1, 0, 1
@@ -250,9 +242,8 @@ def expert_matvec_int4(x: torch.Tensor, w: Int4Weights, pmap: PairMap | None = N
         _need(x.shape[0] == (pmap.T if from_tokens else rows), fn, "x of T token rows or T * k sorted rows expected")
     out = _output(fn, out, (rows, w.N), x.dtype, x.device)
     cfg = mok.mok_int4_config(rows, x.shape[0], k, E, eb, ee, w.N, w.K, w.group, _DTYPES[x.dtype])
-    parts = lambda m: None if m is None else (m.codes, m.scales, m.zeros)
     _call(mok.mok_expert_matvec_int4, x, _ready(x), _ready(pmap.pair_of_row) if from_tokens else None,
-          None if pmap is None else _ready(pmap.offsets), parts(w), parts(w_up), cfg, out)
+          None if pmap is None else _ready(pmap.offsets), w._c, None if w_up is None else w_up._c, cfg, out)
     return out
 
 

@@ -285,15 +285,15 @@ def mok_unpermute_rows_backward(dout, y, gate, row_of_pair, T, k, d, dtype, rows
                                              _ptr(dy), _ptr(dgate), stream or None), "mok_unpermute_rows_backward")
 
 
-def _int4(w):
-    """mok_int4_weights of (codes, scales, zeros or None)."""
-    return mok_int4_weights(*(_ptr(v) for v in w))
+def int4_weights(codes, scales, zeros) -> mok_int4_weights:
+    return mok_int4_weights(_ptr(codes), _ptr(scales), _ptr(zeros))
 
 
-def mok_expert_matvec_int4(x, pair_of_row, expert_offsets, w, w_up, cfg: mok_int4_config, out, stream=0):
-    up = None if w_up is None else ctypes.byref(_int4(w_up))
-    _check(lib().mok_expert_matvec_int4(_ptr(x), _ptr(pair_of_row), _ptr(expert_offsets), ctypes.byref(_int4(w)), up,
-                                        ctypes.byref(cfg), _ptr(out), stream or None), "mok_expert_matvec_int4")
+def mok_expert_matvec_int4(x, pair_of_row, expert_offsets, w: mok_int4_weights, w_up: mok_int4_weights | None,
+                           cfg: mok_int4_config, out, stream=0):
+    _check(lib().mok_expert_matvec_int4(_ptr(x), _ptr(pair_of_row), _ptr(expert_offsets), ctypes.byref(w),
+                                        None if w_up is None else ctypes.byref(w_up), ctypes.byref(cfg), _ptr(out),
+                                        stream or None), "mok_expert_matvec_int4")
 
 
 def mok_quantize_int4(src, rows, K, group, dtype, codes, scales, zeros, stream=0):
