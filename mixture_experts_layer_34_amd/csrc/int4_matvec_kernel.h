@@ -132,8 +132,14 @@ __device__ __forceinline__ void spread_quarters(uint32_t v, uint32_t (&o)[4]) {
 
 // NM matrices (a pair for SwiGLU), NG groups of 16 weight rows of each, tiles
 // of RT rows, groups of GS; of a workgroup's waves KS split K and NW lie side
-// by side along N; x is staged SCH chunks at a time.
-template <int DT, int NM, int NG, int RT, int GS, int KS, int NW, int SCH>
+// by side along N; x is staged SCH chunks at a time; WHOLE: K is a whole number
+// of chunks, whose scales and zeros are then one aligned access.
+//
+// The loop's loads, and what first takes their results, are free of branches
+// (a load that is not wanted is sent past its buffer's end): where a load may
+// or may not be outstanding, the compiler can no longer count those in flight
+// and waits for all of them, which empties the ring once a round.
+template <int DT, int NM, int NG, int RT, int GS, int KS, int NW, int SCH, bool WHOLE>
 __global__ __launch_bounds__(64 * KS * NW) void int4_matvec_kernel(Int4Args a, const int32_t* __restrict__ offsets,
                                                                    const int32_t* __restrict__ pair_of_row) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -205,8 +211,8 @@ __global__ __launch_bounds__(64 * KS * NW) void int4_matvec_kernel(Int4Args a, c
   const int nst = (nch + SCH - 1) / SCH, nloc = nst * JC;  // stages, this wave's chunks
   // this wave's i-th chunk
   auto chunk_of = [&](int i) { return (i / JC) * SCH + kr * JC + i % JC; };
-  const bool whole = K % kChunk == 0;  // a chunk's scales and zeros are one aligned access
   const bool has_zeros = a.zeros[0] != nullptr;
+  const uint32_t zbias = has_zeros ? 0x10101010u : 0x18181818u;  // 16 + z byte by byte, z = 8 without zeros
   const rsrc_t rx = buffer(a.x, (int64_t)a.x_rows * K * 2);
   for (int u = blockIdx.x; u < total; u += gridDim.x) {
     const int q = u / ntn, n0 = (u % ntn) * NU + 16 * NG * nw;
@@ -248,34 +254,32 @@ __global__ __launch_bounds__(64 * KS * NW) void int4_matvec_kernel(Int4Args a, c
       for (int b = 0; b < NB; ++b) {
         const int row = (16 * (b % NG) + n16) * G;
         const rsrc_t r = rs[b / NG], z = rz[b / NG];
-        if (whole) {
+        if constexpr (WHOLE) {
           const uint32_t at = in_c ? (uint32_t)(row + c * NSC) : kNowhere;
           const uint32_t o = in_c ? 2 * at : kNowhere;
           if constexpr (NSC == 4) {
             const auto v = __builtin_amdgcn_raw_buffer_load_b64(r, o, 0, 0);
             sv[b][0] = v[0];
             sv[b][SW - 1] = v[1];
-            zv[b] = has_zeros ? __builtin_amdgcn_raw_buffer_load_b32(z, at, 0, 0) : 0x08080808u;
+            zv[b] = __builtin_amdgcn_raw_buffer_load_b32(z, at, 0, 0);
           } else if constexpr (NSC == 2) {
             sv[b][0] = __builtin_amdgcn_raw_buffer_load_b32(r, o, 0, 0);
-            zv[b] = has_zeros ? (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(z, at, 0, 0) : 0x0808u;
+            zv[b] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(z, at, 0, 0);
           } else {
             sv[b][0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, o, 0, 0);
-            zv[b] = has_zeros ? (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(z, at, 0, 0) : 0x08u;
+            zv[b] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(z, at, 0, 0);
           }
         } else {
 #pragma unroll
           for (int w = 0; w < SW; ++w) sv[b][w] = 0;
-          zv[b] = has_zeros ? 0u : 0x08080808u;
+          zv[b] = 0;
 #pragma unroll
           for (int i = 0; i < NSC; ++i) {
             const int gi = c * NSC + i;
             const bool in = in_c && gi < G;
             const uint32_t v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, in ? 2 * (row + gi) : kNowhere, 0, 0);
             sv[b][i / 2] |= v << (16 * (i % 2));
-            if (has_zeros)
-              zv[b] |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(z, in ? row + gi : kNowhere, 0, 0)
-                       << (8 * i);
+            zv[b] |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(z, in ? row + gi : kNowhere, 0, 0) << (8 * i);
           }
         }
       }
@@ -285,8 +289,7 @@ __global__ __launch_bounds__(64 * KS * NW) void int4_matvec_kernel(Int4Args a, c
     load_scales(0);
     // x by stages of SCH chunks through LDS: a wave takes 64 pieces of 16
     // bytes of one row at a time, puts them in the codes' order and the row
-    // where the MFMA takes it.  Rows past the tile's are not staged: what an
-    // MFMA row holds stays in its own results, and theirs are not stored.
+    // where the MFMA takes it.  Rows past the tile's are zeros.
     auto row_at = [&](int i) { return (i * (KS * NW) + wave) * 64 / XP; };
     auto piece_at = [&](int i) { return (i * (KS * NW) + wave) * 64 % XP + lane; };
     uint32_t xo[XA];
@@ -309,14 +312,13 @@ __global__ __launch_bounds__(64 * KS * NW) void int4_matvec_kernel(Int4Args a, c
 #pragma unroll
       for (int i = 0; i < XA; ++i) {
         const int k = st * SCH * kChunk + 8 * piece_at(i);
-        if (row_at(i) < nrow) xr[i] = load16(rx, st < nst && k < K && xo[i] != kNowhere ? xo[i] + 2 * k : kNowhere);
+        xr[i] = load16(rx, st < nst && k < K && xo[i] != kNowhere ? xo[i] + 2 * k : kNowhere);
       }
     };
     auto store_x = [&](int buf) {
 #pragma unroll
       for (int i = 0; i < XA; ++i) {
         const int r = row_at(i);
-        if (r >= nrow) continue;
         // MFMA row of tile row r: 4 (r % 4) + r / 4 % 4 within its sixteen
         const int p = QUAD ? r : (r & ~15) + 4 * (r & 3) + ((r >> 2) & 3);
         uint32_t d[4];
@@ -340,13 +342,13 @@ __global__ __launch_bounds__(64 * KS * NW) void int4_matvec_kernel(Int4Args a, c
       uint32_t sc[NB][SW][4], zc[NB][4];  // four chunks' scales and 16 + zeros, in every lane quarter
 #pragma unroll
       for (int j = 0; j < RING; ++j) {
-        if (i0 + j >= nloc) break;
+        if (j > 0 && j % JC == 0 && i0 + j >= nloc) break;  // whole stages
         if (j % 4 == 0) {
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
 #pragma unroll
             for (int w = 0; w < SW; ++w) spread_quarters(sv[b][w], sc[b][w]);
-            spread_quarters(zv[b] + 0x10101010u, zc[b]);
+            spread_quarters(zv[b] + zbias, zc[b]);
           }
           load_scales(i0 + j + 4);
         }
@@ -458,7 +460,7 @@ __global__ __launch_bounds__(64 * KS * NW) void int4_matvec_kernel(Int4Args a, c
 #endif
 }
 
-template <int DT, int NM, int NG, int RT, int GS, int KS, int NW, int SCH>
+template <int DT, int NM, int NG, int RT, int GS, int KS, int NW, int SCH, bool WHOLE = true>
 hipError_t run_cfg(const Int4Args& a, hipStream_t s) {
   constexpr int64_t NU = 16 * NG * NW;
   const int64_t ntn = (a.N + NU - 1) / NU;
@@ -466,7 +468,7 @@ hipError_t run_cfg(const Int4Args& a, hipStream_t s) {
   const int64_t units = tiles * ntn;
   if (units == 0) return hipSuccess;
   const unsigned grid = (unsigned)(units < 65536 ? units : 65536);
-  hipLaunchKernelGGL((int4_matvec_kernel<DT, NM, NG, RT, GS, KS, NW, SCH>), dim3(grid), dim3(64 * KS * NW),
+  hipLaunchKernelGGL((int4_matvec_kernel<DT, NM, NG, RT, GS, KS, NW, SCH, WHOLE>), dim3(grid), dim3(64 * KS * NW),
                      (3 * a.E_loc + 1) * sizeof(int32_t), s, a,
                      a.offsets, a.pair_of_row);
   return hipGetLastError();
@@ -505,6 +507,14 @@ template <int DT, int NM, int RT, int GS> hipError_t run(const Int4Args& a, hipS
 // wave on the same condition (128 experts' down product of 128 tokens 115 ->
 // 108 us): x is then read once for both.
 template <int DT, int GS> hipError_t run_group(const Int4Args& a, hipStream_t s) {
+  if constexpr (GS < kChunk) {
+    // a last chunk that is not whole: scales and zeros one by one, in sixteens
+    if (a.K % kChunk) {
+      const bool many = waves_of(a, 16, 1) >= kWanted;
+      if (a.pair) return many ? run_cfg<DT, 2, 1, 16, GS, 1, 4, 4, false>(a, s) : run_cfg<DT, 2, 1, 16, GS, 4, 1, 4, false>(a, s);
+      return many ? run_cfg<DT, 1, 1, 16, GS, 1, 4, 4, false>(a, s) : run_cfg<DT, 1, 1, 16, GS, 4, 1, 4, false>(a, s);
+    }
+  }
   const int64_t experts = a.offsets ? a.E_loc : 1;
   const int ng = a.pair ? 1 : 2;
   if (a.rows <= (a.offsets ? 2 : 4) * experts) return a.pair ? run<DT, 2, 4, GS>(a, s) : run<DT, 1, 4, GS>(a, s);
