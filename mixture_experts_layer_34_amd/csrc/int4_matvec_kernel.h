@@ -489,37 +489,48 @@ inline int64_t waves_of(const Int4Args& a, int rt, int ng) {
 // token (768 groups of 16 columns) 22.1 / 18.1 / 16.5 / 20.1 us for splits of
 // 1 / 2 / 4 / 8, a dense 4099 x 7168 product of three rows 23.8 / 15.2 / 11.9 /
 // 10.2 us; sixteen tokens' gate / up (7,900 groups) 137 / 132 / 164 / 262 us.
+// With sixteen rows a tile, x is the larger part, and the waves that split K
+// keep others beside them to share it (eight in a workgroup): 2048 x 4096 with
+// 64 rows 10.6 us by four waves, 9.6 by eight; 8192 x 4096 with 32 rows 14.9
+// and 13.6; where K is whole, four are better (128 experts' gate / up of 128
+// tokens 176 us, 197 by eight).
 template <int DT, int NM, int RT, int GS> hipError_t run(const Int4Args& a, hipStream_t s) {
+  constexpr int kBeside = RT == 4 ? 1 : 2;
   const int64_t waves = waves_of(a, RT, 1);
   if (waves * 4 < kWanted) return run_cfg<DT, NM, 1, RT, GS, 8, 1, 8>(a, s);
-  if (waves * 2 < kWanted) return run_cfg<DT, NM, 1, RT, GS, 4, 1, 4>(a, s);
-  if (waves < kWanted) return run_cfg<DT, NM, 1, RT, GS, 2, 2, 4>(a, s);
+  if (waves * 2 < kWanted) return run_cfg<DT, NM, 1, RT, GS, 4, kBeside, 4>(a, s);
+  if (waves < kWanted) return run_cfg<DT, NM, 1, RT, GS, 2, 2 * kBeside, 4>(a, s);
   return run_cfg<DT, NM, 1, RT, GS, 1, 4, 4>(a, s);
 }
 
 // Rows per tile, from an expert's rows on average: four up to two rows (x then
 // costs a quarter; experts with more take several tiles), sixteen, and
 // thirty-two past sixteen rows, where taking the codes apart bounds the
-// product, if that still fills the device.  Gate / up of 128 experts: 16
+// product, if that still fills half the device.  Gate / up of 128 experts: 16
 // tokens (a row an expert) 137 us in fours, 155 in sixteens; 128 tokens (eight
-// rows) 304 / 178 us; of 8 experts with 128 rows each 88 us in sixteens, 73 in
-// thirty-twos.  A single matrix with sixteen rows or more takes 32 columns a
-// wave on the same condition (128 experts' down product of 128 tokens 115 ->
-// 108 us): x is then read once for both.
+// rows) 304 / 178 us; of 8 experts with 128 rows each 87 us in sixteens, 69 in
+// thirty-twos, their down product 70 and 47; 8192 x 4096 with 64 rows 22.4 and
+// 18.8.  A single matrix in sixteens takes 32 columns a wave where that fills
+// the device (128 experts' down product of 128 tokens 115 -> 108 us): x is
+// then read once for both.
 template <int DT, int GS> hipError_t run_group(const Int4Args& a, hipStream_t s) {
   if constexpr (GS < kChunk) {
     // a last chunk that is not whole: scales and zeros one by one, in sixteens
     if (a.K % kChunk) {
       const bool many = waves_of(a, 16, 1) >= kWanted;
-      if (a.pair) return many ? run_cfg<DT, 2, 1, 16, GS, 1, 4, 4, false>(a, s) : run_cfg<DT, 2, 1, 16, GS, 4, 1, 4, false>(a, s);
-      return many ? run_cfg<DT, 1, 1, 16, GS, 1, 4, 4, false>(a, s) : run_cfg<DT, 1, 1, 16, GS, 4, 1, 4, false>(a, s);
+      if (a.pair) return many ? run_cfg<DT, 2, 1, 16, GS, 1, 4, 4, false>(a, s) : run_cfg<DT, 2, 1, 16, GS, 4, 2, 4, false>(a, s);
+      return many ? run_cfg<DT, 1, 1, 16, GS, 1, 4, 4, false>(a, s) : run_cfg<DT, 1, 1, 16, GS, 4, 2, 4, false>(a, s);
     }
   }
   const int64_t experts = a.offsets ? a.E_loc : 1;
-  const int ng = a.pair ? 1 : 2;
   if (a.rows <= (a.offsets ? 2 : 4) * experts) return a.pair ? run<DT, 2, 4, GS>(a, s) : run<DT, 1, 4, GS>(a, s);
-  if (a.rows > 16 * experts && waves_of(a, 32, ng) >= kWanted)
-    return a.pair ? run_cfg<DT, 2, 1, 32, GS, 1, 4, 4>(a, s) : run_cfg<DT, 1, 2, 32, GS, 1, 4, 4>(a, s);
+  if (a.rows > 16 * experts) {
+    const int64_t waves = waves_of(a, 32, 1);
+    if (waves >= kWanted)
+      return a.pair ? run_cfg<DT, 2, 1, 32, GS, 1, 4, 4>(a, s) : run_cfg<DT, 1, 1, 32, GS, 1, 8, 4>(a, s);
+    if (2 * waves >= kWanted)
+      return a.pair ? run_cfg<DT, 2, 1, 32, GS, 2, 4, 4>(a, s) : run_cfg<DT, 1, 1, 32, GS, 2, 4, 4>(a, s);
+  }
   if (!a.pair && waves_of(a, 16, 2) >= kWanted) return run_cfg<DT, 1, 2, 16, GS, 1, 4, 4>(a, s);
   return a.pair ? run<DT, 2, 16, GS>(a, s) : run<DT, 1, 16, GS>(a, s);
 }

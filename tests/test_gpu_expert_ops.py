@@ -313,7 +313,10 @@ VARIANTS = [
     (32, 4, 8, 5503, 96, 32, True, False, "bf16"), (32, 4, 8, 5504, 128, 128, False, False, "f16"),
     (64, 2, 2, 8210, 160, 32, True, True, "bf16"), (64, 2, 2, 8208, 256, 128, False, True, "f16"),
     (64, 2, 2, 16411, 64, 64, True, False, "bf16"), (64, 2, 2, 16416, 96, 32, True, False, "f16"),
-    (300, 8, 1024, 17, 64, 64, True, False, "bf16"),
+    (64, 2, 2, 4110, 256, 64, True, True, "bf16"), (64, 2, 2, 4104, 640, 128, False, False, "f16"),
+    (64, 2, 2, 8210, 256, 32, True, False, "bf16"), (32, 4, 8, 1500, 256, 32, True, False, "bf16"),
+    (32, 4, 8, 800, 640, 128, True, True, "f16"), (32, 4, 8, 5503, 256, 64, True, False, "f16"),
+    (300, 8, 1024, 17, 64, 64, True, False, "bf16"), (300, 8, 1024, 17, 128, 64, True, False, "bf16"),
 ]
 
 
