@@ -5,7 +5,8 @@ with their gradients, and expert products with 4-bit integer weights.
 Torch plumbing around the C ABI (include/mok.h): tensors are checked, outputs
 allocated unless given, and the kernels enqueued on the tensors' device, on
 its current stream.  Inputs that are not contiguous (or not 16-byte aligned)
-are copied; an output given by the caller has to be both."""
+are copied; an output given by the caller has to be both.  Nothing is recorded
+for autograd: the gradients are the _backward functions'."""
 from __future__ import annotations
 
 from dataclasses import dataclass
@@ -59,7 +60,7 @@ def _call(f, ref, *args):
             f(*args, stream)
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class PairMap:
     """Where the T * k token-expert pairs sit in the expert-sorted rows
     (mok_sort_pairs): int32 counts [E], offsets [E + 1], row_of_pair [T, k]
@@ -84,7 +85,7 @@ class PairMap:
     def _of(cls, *fields):
         """A map whose arrays are known to fit."""
         m = object.__new__(cls)
-        (m.T, m.k, m.E, m.expert_begin, m.expert_end, m.counts, m.offsets, m.row_of_pair, m.pair_of_row) = fields
+        m.__dict__.update(zip(cls.__dataclass_fields__, fields))
         return m
 
 
@@ -174,7 +175,7 @@ def unpermute_rows_backward(dout: torch.Tensor, pmap: PairMap, gate: torch.Tenso
 
 
 # ------------------------------------------------------------------ 4-bit integer weights
-@dataclass(frozen=True)
+@dataclass(frozen=True, eq=False)
 class Int4Weights:
     """Matrices [E, N, K] in 4-bit integers: uint8 codes [E, N, K / 2] (two per
     byte, the lower element in the low nibble), scales [E, N, K / group] in the
@@ -185,21 +186,35 @@ class Int4Weights:
     zeros: torch.Tensor | None = None
 
     def __post_init__(self):
-        fn = "Int4Weights"
+        for name in ("codes", "scales", "zeros"):
+            object.__setattr__(self, name, _ready(getattr(self, name)))
+        self.view("Int4Weights")
+
+    def view(self, fn: str):
+        """(E, N, K, group, the C view): the arrays checked against each other,
+        again only after one of them was given other storage."""
         q, s, z = self.codes, self.scales, self.zeros
+        now = (q.data_ptr(), s.data_ptr(), 0 if z is None else z.data_ptr(), q.shape, s.shape)
+        seen = self.__dict__.get("_seen")
+        if seen is not None and seen[0] == now:
+            return seen[1]
         _need(q.dim() == 3 and q.dtype == torch.uint8 and s.dim() == 3 and s.shape[:2] == q.shape[:2], fn,
               "uint8 codes [E, N, K / 2] and scales [E, N, K / group] expected")
         _need(s.dtype in (torch.bfloat16, torch.float16), fn, "bf16 or fp16 scales expected")
-        E, N, K = q.shape[0], q.shape[1], 2 * q.shape[2]
-        group = K // max(s.shape[2], 1)
-        _need(group in (32, 64, 128) and group * s.shape[2] == K, fn, "groups of 32, 64 or 128 expected")
-        _need(z is None or (z.dtype == torch.uint8 and z.shape == s.shape), fn, "uint8 zeros like the scales")
+        E, N, K = q.shape
+        K, G = 2 * K, s.shape[2]
+        group = K // G if G else 0
+        _need(group in (32, 64, 128) and group * G == K, fn, "groups of 32, 64 or 128 expected")
+        _need(z is None or (z.dtype == torch.uint8 and z.shape == s.shape), fn, "uint8 zeros like the scales expected")
         _on(fn, q, s, z)
-        q, s, z = _ready(q), _ready(s), _ready(z)
-        # the arrays cannot be replaced, so the C view of them is made once
-        for name, v in (("codes", q), ("scales", s), ("zeros", z), ("E", E), ("N", N), ("K", K), ("group", group),
-                        ("_c", mok.int4_weights(q, s, z))):
-            object.__setattr__(self, name, v)
+        _need(all(t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0) for t in (q, s, z)), fn,
+              "contiguous, 16-byte aligned arrays expected")
+        v = (E, N, K, group, mok.int4_weights(q, s, z))
+        self.__dict__["_seen"] = (now, v)
+        return v
+
+    def __reduce__(self):
+        return Int4Weights, (self.codes, self.scales, self.zeros)
 
 
 def quantize_int4(w: torch.Tensor, group: int = 128, symmetric: bool = True) -> Int4Weights:
@@ -226,24 +241,27 @@ def expert_matvec_int4(x: torch.Tensor, w: Int4Weights, pmap: PairMap | None = N
     [T * k, N] (rows without a pair are left as they are).  Without one, w is
     one matrix and every row of x is its own."""
     fn = "expert_matvec_int4"
-    _need(x.dim() == 2 and x.dtype == w.scales.dtype and x.shape[1] == w.K,
-          fn, "x [rows, K] of the scales' type expected")
+    E_w, N, K, group, wc = w.view(fn)
+    uc = None
+    _need(x.dim() == 2 and x.dtype == w.scales.dtype and x.shape[1] == K, fn,
+          "x [rows, K] of the scales' type expected")
     _on(fn, x, w.codes, None if w_up is None else w_up.codes, None if pmap is None else pmap.offsets)
     if w_up is not None:
-        _need(w_up.codes.shape == w.codes.shape and w_up.scales.shape == w.scales.shape and
-              w_up.scales.dtype == w.scales.dtype and (w_up.zeros is None) == (w.zeros is None), fn,
-              "w and w_up of one shape, group and kind expected")
+        up = w_up.view(fn)
+        uc = up[4]
+        _need(up[:4] == (E_w, N, K, group) and w_up.scales.dtype == w.scales.dtype and
+              (w_up.zeros is None) == (w.zeros is None), fn, "w and w_up of one shape, group and kind expected")
     if pmap is None:
-        _need(w.E == 1 and not from_tokens, fn, "one matrix expected without a pair map")
+        _need(E_w == 1 and not from_tokens, fn, "one matrix expected without a pair map")
         rows, k, E, eb, ee = x.shape[0], 1, 1, 0, 1
     else:
         rows, k, E, eb, ee = pmap.T * pmap.k, pmap.k, pmap.E, pmap.expert_begin, pmap.expert_end
-        _need(w.E == ee - eb, fn, "weights of the map's local experts expected")
+        _need(E_w == ee - eb, fn, "weights of the map's local experts expected")
         _need(x.shape[0] == (pmap.T if from_tokens else rows), fn, "x of T token rows or T * k sorted rows expected")
-    out = _output(fn, out, (rows, w.N), x.dtype, x.device)
-    cfg = mok.mok_int4_config(rows, x.shape[0], k, E, eb, ee, w.N, w.K, w.group, _DTYPES[x.dtype])
+    out = _output(fn, out, (rows, N), x.dtype, x.device)
+    cfg = mok.mok_int4_config(rows, x.shape[0], k, E, eb, ee, N, K, group, _DTYPES[x.dtype])
     _call(mok.mok_expert_matvec_int4, x, _ready(x), _ready(pmap.pair_of_row) if from_tokens else None,
-          None if pmap is None else _ready(pmap.offsets), w._c, None if w_up is None else w_up._c, cfg, out)
+          None if pmap is None else _ready(pmap.offsets), wc, uc, cfg, out)
     return out
 
 

@@ -10,6 +10,9 @@ chain (elements of a thread, then the lanes' and waves' tree).  A 4-bit product
 accumulates 32 products and the running value per matrix instruction (33 steps
 of at most 2 u each, should it not round to nearest), then the group's
 correction and the sum over groups and waves."""
+import copy
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
@@ -262,8 +265,9 @@ def _unpack(w):
     """(W, s (16 + q) + s (16 + z)) in 64 bits: the weights, and the magnitudes
     that the two sums of a group run over."""
     q = torch.stack((w.codes & 15, w.codes >> 4), -1).flatten(-2).double()
-    s = w.scales.double().repeat_interleave(w.group, 2)
-    z = torch.full_like(q, 8.0) if w.zeros is None else w.zeros.double().repeat_interleave(w.group, 2)
+    group = w.view("test")[3]
+    s = w.scales.double().repeat_interleave(group, 2)
+    z = torch.full_like(q, 8.0) if w.zeros is None else w.zeros.double().repeat_interleave(group, 2)
     return (q - z) * s, (32 + q + z) * s
 
 
@@ -271,15 +275,16 @@ def _product_ref(xr, expert, w, w_up, dt):
     """Values and tolerances of rows xr (64 bits) with expert ids."""
     def one(m):
         W, mag = _unpack(m)
-        v = torch.zeros((xr.shape[0], m.N), dtype=torch.float64, device="cuda")
+        E, N, K, group = m.view("test")[:4]
+        v = torch.zeros((xr.shape[0], N), dtype=torch.float64, device="cuda")
         t = torch.zeros_like(v)
-        for e in range(m.E):
+        for e in range(E):
             r = torch.where(expert == e)[0]
             v[r] = xr[r] @ W[e].t()
             t[r] = xr[r].abs() @ mag[e].t()
         # per matrix instruction 33 steps, at most four in a chain; then the
         # correction, the sum over groups, eight waves
-        return v, t * (4 * 33 * 2 + m.K / m.group + 12) * U
+        return v, t * (4 * 33 * 2 + K / group + 12) * U
     a, ta = one(w)
     if w_up is None:
         return a, a.abs() * HALF[dt] + ta + TINY[dt]
@@ -386,6 +391,38 @@ def test_matvec_subnormal_inputs():
     ref = x.double() @ _unpack(w)[0][0].t()
     assert float(ref.abs().max()) > 0
     assert torch.equal(X.expert_matvec_int4(x, w), ref.half())
+
+
+@pytest.mark.parametrize("rows", [3, 16, 40])
+def test_matvec_nonfinite_rows_stay_apart(rows):
+    """A row with a NaN or an infinity spoils its own results only."""
+    w = _weights(_gen(5), 1, 96, 384, 128, True, "bf16")
+    x = _randn(_gen(6), (rows, 384), "bf16")
+    want = X.expert_matvec_int4(x, w)
+    x[1, 17], x[rows - 1, 300] = float("nan"), float("inf")
+    got = X.expert_matvec_int4(x, w)
+    keep = [r for r in range(rows) if r not in (1, rows - 1)]
+    assert torch.equal(got[keep], want[keep])
+    assert not torch.isfinite(got[[1, rows - 1]]).any()
+
+
+def test_weights_copied_and_replaced():
+    """Copies of the weights and of a map stand on their own; neither takes
+    other arrays in place; weights whose storage is swapped are read anew."""
+    idx, gate, x, w1, w3, w2 = _decode()
+    m = X.sort_pairs(idx, 8)
+    want = X.int4_experts(x, m, gate, w1, w3, w2)
+    c1, cm = copy.deepcopy(w1), copy.deepcopy(m)
+    assert c1.codes.data_ptr() != w1.codes.data_ptr()
+    spare = w1.codes.clone()
+    w1.codes.zero_()
+    assert torch.equal(X.int4_experts(x, cm, gate, c1, w3, w2), want)
+    w1.codes.data = spare
+    assert torch.equal(X.int4_experts(x, m, gate, w1, w3, w2), want)
+    with pytest.raises(dataclasses.FrozenInstanceError):
+        w1.codes = spare
+    with pytest.raises(dataclasses.FrozenInstanceError):
+        m.offsets = m.offsets[:3]
 
 
 def test_matvec_local_experts_and_bad_maps():
