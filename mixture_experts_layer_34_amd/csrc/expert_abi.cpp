@@ -138,7 +138,6 @@ mok_status mok_expert_matvec_int4(const void* x, const int32_t* pair_of_row, con
   a.N = c.N;
   a.K = c.K;
   a.group = c.group;
-  a.dtype = c.dtype;
   a.pair = w_up != nullptr;
   return result(c.dtype == MOK_DTYPE_BF16 ? launch_int4_matvec_bf16(a, (hipStream_t)stream)
                                           : launch_int4_matvec_f16(a, (hipStream_t)stream));

@@ -18,7 +18,6 @@ struct Int4Args {
   int rows, x_rows, k;
   int eb, E_loc;
   int N, K, group;
-  int dtype;                   // kBF16 or kF16
   int pair;                    // two matrices: out = silu(first) * second
 };
 // x below 2 GiB and an expert's codes below 4 GiB (32-bit buffer offsets).

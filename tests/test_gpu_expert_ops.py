@@ -393,6 +393,31 @@ def test_matvec_subnormal_inputs():
     assert torch.equal(X.expert_matvec_int4(x, w), ref.half())
 
 
+@pytest.mark.parametrize("T,k,E,N,K,group,pair", [
+    (512, 4, 1024, 3600, 32, 32, False),      # tiles of four rows
+    (1024, 4, 1024, 3700, 32, 32, True),      # of sixteen, a pair
+    (1024, 4, 1024, 7400, 128, 64, False),    # of sixteen, 32 columns a wave
+    (5000, 4, 3, 8210, 128, 128, True),       # of thirty-two
+])
+def test_more_units_than_workgroups(T, k, E, N, K, group, pair):
+    """Products whose units exceed the largest grid: workgroups take several,
+    one after the other.  A sample of rows, the first and last among them."""
+    g = _gen(T + N)
+    idx = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32).cuda()
+    m = X.sort_pairs(idx, E)
+    w = [_weights(g, E, N, K, group, True, "bf16") for _ in range(2)]
+    x = _randn(g, (T, K), "bf16")
+    got = X.expert_matvec_int4(x, w[0], m, w_up=w[1] if pair else None, from_tokens=True)
+    assert torch.isfinite(got).all()
+    rows = torch.cat([torch.arange(40), torch.randint(0, T * k, (120,), generator=g),
+                      torch.arange(T * k - 40, T * k)]).cuda()
+    expert = idx.reshape(-1)[m.pair_of_row[rows].long()].long()
+    used, inner = torch.unique(expert, return_inverse=True)
+    cut = [X.Int4Weights(v.codes[used], v.scales[used], v.zeros[used]) for v in w]
+    ref, tol = _product_ref(x.double()[m.pair_of_row[rows].long() // k], inner, cut[0], cut[1] if pair else None, "bf16")
+    _close(got[rows], ref, tol, "sampled rows")
+
+
 @pytest.mark.parametrize("rows", [3, 16, 40])
 def test_matvec_nonfinite_rows_stay_apart(rows):
     """A row with a NaN or an infinity spoils its own results only."""
