@@ -39,16 +39,15 @@
 // too few units, their fp32 sums then meeting in LDS, added in wave order: the
 // same bits on every run.
 //
-// Measured: gate / up of 128 experts (d 4096, F 1536) 177 us for 128 tokens
-// (groups of 128; 4.7 TB/s of codes and scales), 137 us for 16 tokens (82
-// experts, groups of 32 with zero points; 4.5 TB/s), 16.2 us for one (8
-// experts; 3.2 TB/s, 6 us of it the launch and the first loads).  A deeper
-// ring (eight chunks) changed nothing or lost up to 20 %, all of x in LDS at
-// once won 0.3 us at three rows and lost 10 % at sixteen tokens' down product,
-// group sums of x taken while staging in place of the products with ones lost
-// 2 to 25 %, non-temporal loads of the codes nothing.  With 64 rows on one
-// matrix (4096 x 8192: 23.6 us) the two thousand waves spend two thirds of
-// their issue slots taking the codes apart, once for each sixteen rows.
+// Measured: gate / up of 128 experts (d 4096, F 1536) 169 us for 128 tokens
+// (groups of 128; 4.9 TB/s of codes and scales), 128 us for 16 tokens (82
+// experts, groups of 32 with zero points; 4.8 TB/s), 16.3 us for one (8
+// experts; 3.2 TB/s, 6 us of it the launch and the first loads).  A ring of
+// eight chunks is level at best and loses up to 37 % (one token's down product
+// 11.3 -> 12.0, 8 experts' with 128 rows 46.8 -> 64 us); non-temporal loads of
+// the codes gave nothing.  Past sixteen rows the vector units taking the codes
+// apart are the bound, once for each tile of rows: 64 rows on one matrix (8192
+// x 4096) 18.4 us where four rows take 9.2.
 #pragma once
 #include "elem.h"
 #include "int4_matvec.h"
@@ -486,19 +485,22 @@ inline int64_t waves_of(const Int4Args& a, int rt, int ng) {
 
 // A wave by itself on its columns needs no sum and no more barriers than x's,
 // so K is split only as far as it takes to fill the device: gate / up of one
-// token (768 groups of 16 columns) 22.1 / 18.1 / 16.5 / 20.1 us for splits of
-// 1 / 2 / 4 / 8, a dense 4099 x 7168 product of three rows 23.8 / 15.2 / 11.9 /
-// 10.2 us; sixteen tokens' gate / up (7,900 groups) 137 / 132 / 164 / 262 us.
+// token (768 groups of 16 columns) 20.7 / 17.9 / 16.7 / 20.5 us for splits of
+// 1 / 2 / 4 / 8, a dense 4099 x 7168 product of three rows 22.9 / 14.9 / 11.8 /
+// 10.2 us; sixteen tokens' gate / up (7,900 groups) 134 / 129 / 165 / 199 us.
 // With sixteen rows a tile, x is the larger part, and the waves that split K
 // keep others beside them to share it (eight in a workgroup): 2048 x 4096 with
 // 64 rows 10.6 us by four waves, 9.6 by eight; 8192 x 4096 with 32 rows 14.9
 // and 13.6; where K is whole, four are better (128 experts' gate / up of 128
-// tokens 176 us, 197 by eight).
+// tokens 176 us, 197 by eight).  Eight waves' registers take a whole unit, so
+// their splits of four end earlier: 16 experts' 768 x 2048 pair with 128 rows
+// (960 groups) 18.2 us in four, 13.4 in two; 8192 x 4096 with 8 rows (512)
+// 11.2 and 13.5.
 template <int DT, int NM, int RT, int GS> hipError_t run(const Int4Args& a, hipStream_t s) {
   constexpr int kBeside = RT == 4 ? 1 : 2;
   const int64_t waves = waves_of(a, RT, 1);
   if (waves * 4 < kWanted) return run_cfg<DT, NM, 1, RT, GS, 8, 1, 8>(a, s);
-  if (waves * 2 < kWanted) return run_cfg<DT, NM, 1, RT, GS, 4, kBeside, 4>(a, s);
+  if (waves * (RT == 4 ? 2 : 3) < kWanted) return run_cfg<DT, NM, 1, RT, GS, 4, kBeside, 4>(a, s);
   if (waves < kWanted) return run_cfg<DT, NM, 1, RT, GS, 2, 2 * kBeside, 4>(a, s);
   return run_cfg<DT, NM, 1, RT, GS, 1, 4, 4>(a, s);
 }
@@ -506,13 +508,14 @@ template <int DT, int NM, int RT, int GS> hipError_t run(const Int4Args& a, hipS
 // Rows per tile, from an expert's rows on average: four up to two rows (x then
 // costs a quarter; experts with more take several tiles), sixteen, and
 // thirty-two past sixteen rows, where taking the codes apart bounds the
-// product, if that still fills half the device.  Gate / up of 128 experts: 16
-// tokens (a row an expert) 137 us in fours, 155 in sixteens; 128 tokens (eight
-// rows) 304 / 178 us; of 8 experts with 128 rows each 87 us in sixteens, 69 in
-// thirty-twos, their down product 70 and 47; 8192 x 4096 with 64 rows 22.4 and
-// 18.8.  A single matrix in sixteens takes 32 columns a wave where that fills
-// the device (128 experts' down product of 128 tokens 115 -> 108 us): x is
-// then read once for both.
+// product, if that still fills half the device.  Gate / up of 128 experts in
+// fours / sixteens / thirty-twos: one row each 108 / 112 / 158 us, two 142 /
+// 145 / 205, four 198 / 161 / 226, eight 333 / 174 / 238, 24 rows 796 / 317 /
+// 262; 8192 x 4096 with 64 rows 51 / 21.8 / 18.4, a single matrix with five to
+// eight rows 11.6 / 10.8 us, but 6.4 / 8.0 at 2048 x 4096, where fours leave
+// most of the device idle.  A single matrix in sixteens takes 32 columns a
+// wave where that fills the device (128 experts' down product of 128 tokens
+// 115 -> 108 us): x is then read once for both.
 template <int DT, int GS> hipError_t run_group(const Int4Args& a, hipStream_t s) {
   if constexpr (GS < kChunk) {
     // a last chunk that is not whole: scales and zeros one by one, in sixteens
@@ -523,7 +526,8 @@ template <int DT, int GS> hipError_t run_group(const Int4Args& a, hipStream_t s)
     }
   }
   const int64_t experts = a.offsets ? a.E_loc : 1;
-  if (a.rows <= (a.offsets ? 2 : 4) * experts) return a.pair ? run<DT, 2, 4, GS>(a, s) : run<DT, 1, 4, GS>(a, s);
+  const bool few = a.offsets ? a.rows <= 2 * experts : a.rows <= 4 || (a.rows <= 8 && waves_of(a, 4, 1) * 4 < kWanted);
+  if (few) return a.pair ? run<DT, 2, 4, GS>(a, s) : run<DT, 1, 4, GS>(a, s);
   if (a.rows > 16 * experts) {
     const int64_t waves = waves_of(a, 32, 1);
     if (waves >= kWanted)

@@ -366,6 +366,23 @@ def test_dense_matvec(rows, N, K, group, zeros, pair, dt):
     _close(got, ref, tol, "dense product")
 
 
+@pytest.mark.parametrize("rows,N", [
+    (4, 8000), (4, 9600), (4, 17600), (4, 33000),       # fours, K in eight, four, two and whole
+    (8, 4000), (8, 4200), (7, 16),                      # five to eight rows in fours and sixteens
+    (16, 8000), (16, 9600), (16, 12000), (16, 33000),   # sixteens
+    (32, 20000), (32, 33000), (31, 66000),              # thirty-twos
+])
+@pytest.mark.parametrize("pair", [False, True])
+def test_dense_sizes_of_each_split(rows, N, pair):
+    g = _gen(rows + N)
+    w = [_weights(g, 1, N, 384, 64, True, "bf16") for _ in range(2)]
+    x = _randn(g, (rows, 384), "bf16")
+    got = X.expert_matvec_int4(x, w[0], w_up=w[1] if pair else None)
+    ref, tol = _product_ref(x.double(), torch.zeros(rows, dtype=torch.long, device="cuda"), w[0],
+                            w[1] if pair else None, "bf16")
+    _close(got, ref, tol, "dense product")
+
+
 def test_matvec_exact_integers():
     """Small integer x, power-of-two scales: every sum is exact in fp32, so the
     result is the rounded exact value, whatever the order (bf16 and fp16, each
