@@ -640,8 +640,8 @@ typedef struct mok_int4_config {
  *                   every row (E = 1, no pair_of_row)
  *   out             dtype [rows, N]
  * Codes enter the matrix cores exactly and the scales multiply fp32 sums; one
- * rounding at the end.  x finite, below 2^100 in magnitude.  Results are the
- * same bits on every run.  Few rows per expert: each tile of rows reads its
+ * rounding at the end.  x finite, below 2^100 in magnitude.  out must not
+ * overlap an input.  Results are the same bits on every run.  Few rows per expert: each tile of rows reads its
  * expert's weights again.
  * rows and x_rows up to 2^24, rows * N < 2^36, x below 2 GiB, one expert's codes
  * below 2 GiB, all experts' below 256 GiB.

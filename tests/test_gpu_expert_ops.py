@@ -717,3 +717,38 @@ def test_empty_calls():
     X.expert_matvec_int4(torch.zeros((5, 64), dtype=torch.bfloat16, device="cuda"), w, m, from_tokens=True, out=out)
     assert (out == 3).all()
     assert mok.MOK_OK == 0
+
+
+def test_outputs_apart_from_inputs():
+    """An output that shares memory with an input is refused, a neighbour in
+    one buffer is not, nor is the source of a copy that the call makes."""
+    g = _gen(77)
+    T, d = 8, 64
+    m = X.sort_pairs(torch.randint(0, 4, (T, 1), generator=g, dtype=torch.int32).cuda(), 4)
+    both = _randn(g, (2 * T, d), "bf16")
+    x, out = both[:T], both[T:]
+    w = _weights(g, 4, d, d, 32, True, "bf16")
+    gate = torch.rand(T, 1, generator=g).cuda()
+    for f in (lambda o: X.permute_rows(x, m, out=o), lambda o: X.unpermute_rows(x, m, gate, out=o),
+              lambda o: X.unpermute_rows_backward(x, m, gate, out=o)[0],
+              lambda o: X.unpermute_rows_backward(x.clone(), m, gate, y=x, out=o)[0],
+              lambda o: X.expert_matvec_int4(x, w, m, out=o),
+              lambda o: X.expert_matvec_int4(x, w, m, from_tokens=True, out=o)):
+        for bad in (x, both[1:T + 1], both[T - 1:2 * T - 1]):
+            with pytest.raises(ValueError, match="overlap"):
+                f(bad)
+        want = f(None)
+        assert torch.equal(f(out), want)
+    wide = _randn(g, (T, 2 * d), "bf16")
+    want = X.permute_rows(wide[:, ::2].contiguous(), m)
+    o = wide.view(2 * T, d)[:T]
+    assert torch.equal(X.permute_rows(wide[:, ::2], m, out=o), want)
+
+
+def test_weights_turned_in_place_are_refused():
+    w = _weights(_gen(5), 1, 64, 128, 32, True, "bf16")
+    x = _randn(_gen(6), (2, 128), "bf16")
+    X.expert_matvec_int4(x, w)
+    w.codes.transpose_(1, 2)  # 64 x 64 codes: the same shape and address
+    with pytest.raises(ValueError, match="contiguous"):
+        X.expert_matvec_int4(x, w)
