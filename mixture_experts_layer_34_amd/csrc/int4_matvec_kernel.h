@@ -473,49 +473,72 @@ hipError_t run_cfg(const Int4Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-constexpr int64_t kWanted = 8 * kNumCUs;  // waves that fill the device
+constexpr int64_t kWanted = 8 * kNumCUs;  // waves that fill the device, eight a compute unit
 
-// Waves of a call whose waves do not split K: the tiles it can expect (every
-// expert with rows has a last tile half full on average) times N's columns.
+// Waves of a call whose waves do not split K: its row tiles times N's columns.
+// The rows of each expert are known on the device only: one tile, or rows / rt
+// and a part of one (half a tile far past rt rows, none up to them).
 inline int64_t waves_of(const Int4Args& a, int rt, int ng) {
   const int64_t experts = a.E_loc < a.rows ? a.E_loc : a.rows;
-  const int64_t tiles = a.offsets ? experts + a.rows / rt / 2 : (a.rows + rt - 1) / rt;
+  const int64_t some = (8 * (int64_t)a.rows / rt + 3 * experts) / 8;
+  const int64_t tiles = !a.offsets ? (a.rows + rt - 1) / rt : some > experts ? some : experts;
   return tiles * ((a.N + 16 * ng - 1) / (16 * ng));
 }
 
 // A wave by itself on its columns needs no sum and no more barriers than x's,
-// so K is split only as far as it takes to fill the device: gate / up of one
-// token (768 groups of 16 columns) 20.7 / 17.9 / 16.7 / 20.5 us for splits of
-// 1 / 2 / 4 / 8, a dense 4099 x 7168 product of three rows 22.9 / 14.9 / 11.8 /
-// 10.2 us; sixteen tokens' gate / up (7,900 groups) 134 / 129 / 165 / 199 us.
-// With sixteen rows a tile, x is the larger part, and the waves that split K
-// keep others beside them to share it (eight in a workgroup): 2048 x 4096 with
-// 64 rows 10.6 us by four waves, 9.6 by eight; 8192 x 4096 with 32 rows 14.9
-// and 13.6; where K is whole, four are better (128 experts' gate / up of 128
-// tokens 176 us, 197 by eight).  Eight waves' registers take a whole unit, so
-// their splits of four end earlier: 16 experts' 768 x 2048 pair with 128 rows
-// (960 groups) 18.2 us in four, 13.4 in two; 8192 x 4096 with 8 rows (512)
-// 11.2 and 13.5.
+// so K is split only as far as it takes to fill the device, and waves that
+// split K keep others beside them to share x, eight in a workgroup (in tiles of
+// four, where x is small, as few as give each its share): gate / up of one token
+// (768 groups of 16 columns) 20.7 / 17.9 / 16.7 / 20.5 us for splits of 1 / 2 /
+// 4 / 8, a dense 4099 x 7168 product of three rows 22.9 / 14.9 / 11.8 / 10.2 us;
+// sixteen tokens' gate / up (7,900 groups) 134 / 129 / 165 / 199 us.
+//
+// From sixteen rows a tile a compute unit holds one workgroup of eight waves of
+// a pair (or of thirty-two rows), so one workgroup more than there are compute
+// units costs a whole second round, and the split is the largest that needs no
+// second one.  A pair of matrices with K 4096 and 16 rows, for splits of 8 / 4 /
+// 2 / 1 in eight waves each: N 6144 (384 groups) 19.6 / 14.3 /
+// 18.1 / 27.9 us, 10240 (640) 28.0 / 25.7 / 19.1 / 28.5, 18432 (1152) 45.2 /
+// 37.5 / 35.7 / 31.2; with 64 rows in thirty-twos 8192 (1024) - / - / 25.7 /
+// 36.7, 10240 (1280) - / - / 45.5 / 37.3.  A single matrix in sixteens shares
+// its compute unit: a split of two up to a whole device (18432 columns 19.6 us,
+// 19.9 whole); in thirty-twos sixteen waves of a split of two take the second
+// half device (12288 columns, 64 rows 23.9 us, 25.4 whole, 31.1 in eight
+// waves).  Past a device's waves a pair's workgroups are of four waves (128
+// experts' gate / up of 128 tokens 176 us, 197 by eight).
 template <int DT, int NM, int RT, int GS> hipError_t run(const Int4Args& a, hipStream_t s) {
-  constexpr int kBeside = RT == 4 ? 1 : 2;
   const int64_t waves = waves_of(a, RT, 1);
-  if (waves * 4 < kWanted) return run_cfg<DT, NM, 1, RT, GS, 8, 1, 8>(a, s);
-  if (waves * (RT == 4 ? 2 : 3) < kWanted) return run_cfg<DT, NM, 1, RT, GS, 4, kBeside, 4>(a, s);
-  if (waves < kWanted) return run_cfg<DT, NM, 1, RT, GS, 2, 2 * kBeside, 4>(a, s);
-  return run_cfg<DT, NM, 1, RT, GS, 1, 4, 4>(a, s);
+  if constexpr (RT == 4) {
+    if (waves * 4 * NM <= kWanted) return run_cfg<DT, NM, 1, RT, GS, 8, 1, 8>(a, s);
+    if (waves * 8 <= 3 * kWanted) return run_cfg<DT, NM, 1, RT, GS, 4, 1, 4>(a, s);
+    if (waves <= kWanted) return run_cfg<DT, NM, 1, RT, GS, 2, 2, 4>(a, s);
+    return run_cfg<DT, NM, 1, RT, GS, 1, 4, 4>(a, s);
+  } else if constexpr (RT == 16) {
+    if (waves * 8 <= kWanted) return run_cfg<DT, NM, 1, RT, GS, 8, 1, 8>(a, s);
+    if (waves * 4 <= kWanted) return run_cfg<DT, NM, 1, RT, GS, 4, 2, 4>(a, s);
+    if (waves * NM <= kWanted) return run_cfg<DT, NM, 1, RT, GS, 2, 4, 4>(a, s);
+    if constexpr (NM == 2)
+      if (waves <= kWanted) return run_cfg<DT, NM, 1, RT, GS, 1, 8, 4>(a, s);
+    return run_cfg<DT, NM, 1, RT, GS, 1, 4, 4>(a, s);
+  } else {
+    if (waves * 2 <= kWanted) return run_cfg<DT, NM, 1, RT, GS, 2, 4, 4>(a, s);
+    if (waves <= kWanted) return run_cfg<DT, NM, 1, RT, GS, NM == 1 ? 2 : 1, 8, 4>(a, s);
+    return run_cfg<DT, NM, 1, RT, GS, 1, NM == 1 ? 8 : 4, 4>(a, s);
+  }
 }
 
 // Rows per tile, from an expert's rows on average: four up to two rows (x then
 // costs a quarter; experts with more take several tiles), sixteen, and
 // thirty-two past sixteen rows, where taking the codes apart bounds the
-// product, if that still fills half the device.  Gate / up of 128 experts in
-// fours / sixteens / thirty-twos: one row each 108 / 112 / 158 us, two 142 /
-// 145 / 205, four 198 / 161 / 226, eight 333 / 174 / 238, 24 rows 796 / 317 /
-// 262; 8192 x 4096 with 64 rows 51 / 21.8 / 18.4, a single matrix with five to
-// eight rows 11.6 / 10.8 us, but 6.4 / 8.0 at 2048 x 4096, where fours leave
-// most of the device idle.  A single matrix in sixteens takes 32 columns a
-// wave where that fills the device (128 experts' down product of 128 tokens
-// 115 -> 108 us): x is then read once for both.
+// product, if that leaves no more than three eighths of the device idle.  Gate /
+// up of 128 experts in fours / sixteens / thirty-twos: one row each 108 / 112 /
+// 158 us, two 142 / 145 / 205, four 198 / 161 / 226, eight 333 / 174 / 238, 24
+// rows 796 / 317 / 262; a single matrix with 64 rows 51 / 21.8 / 18.4 at 8192 x
+// 4096, 18.5 in sixteens and 16.8 in thirty-twos at 5120, 13.5 and 16.9 at 4096;
+// with five to eight rows 11.6 in fours and 10.8 in sixteens, but 6.4 and 8.0 at
+// 2048 x 4096, where fours leave most of the device idle.  A single matrix in
+// sixteens takes 32 columns a wave where that fills the device (128 experts'
+// down product of 128 tokens 115 -> 108 us): x is then read once for both.
 template <int DT, int GS> hipError_t run_group(const Int4Args& a, hipStream_t s) {
   if constexpr (GS < kChunk) {
     // a last chunk that is not whole: scales and zeros one by one, in sixteens
@@ -528,13 +551,8 @@ template <int DT, int GS> hipError_t run_group(const Int4Args& a, hipStream_t s)
   const int64_t experts = a.offsets ? a.E_loc : 1;
   const bool few = a.offsets ? a.rows <= 2 * experts : a.rows <= 4 || (a.rows <= 8 && waves_of(a, 4, 1) * 4 < kWanted);
   if (few) return a.pair ? run<DT, 2, 4, GS>(a, s) : run<DT, 1, 4, GS>(a, s);
-  if (a.rows > 16 * experts) {
-    const int64_t waves = waves_of(a, 32, 1);
-    if (waves >= kWanted)
-      return a.pair ? run_cfg<DT, 2, 1, 32, GS, 1, 4, 4>(a, s) : run_cfg<DT, 1, 1, 32, GS, 1, 8, 4>(a, s);
-    if (2 * waves >= kWanted)
-      return a.pair ? run_cfg<DT, 2, 1, 32, GS, 2, 4, 4>(a, s) : run_cfg<DT, 1, 1, 32, GS, 2, 4, 4>(a, s);
-  }
+  if (a.rows > 16 * experts && waves_of(a, 32, 1) * 16 >= 5 * kWanted)
+    return a.pair ? run<DT, 2, 32, GS>(a, s) : run<DT, 1, 32, GS>(a, s);
   if (!a.pair && waves_of(a, 16, 2) >= kWanted) return run_cfg<DT, 1, 2, 16, GS, 1, 4, 4>(a, s);
   return a.pair ? run<DT, 2, 16, GS>(a, s) : run<DT, 1, 16, GS>(a, s);
 }

@@ -367,10 +367,10 @@ def test_dense_matvec(rows, N, K, group, zeros, pair, dt):
 
 
 @pytest.mark.parametrize("rows,N", [
-    (4, 8000), (4, 9600), (4, 17600), (4, 33000),       # fours, K in eight, four, two and whole
+    (4, 4000), (4, 8000), (4, 9600), (4, 17600), (4, 33000),  # fours, K in eight, four, two and whole
     (8, 4000), (8, 4200), (7, 16),                      # five to eight rows in fours and sixteens
-    (16, 8000), (16, 9600), (16, 12000), (16, 33000),   # sixteens
-    (32, 20000), (32, 33000), (31, 66000),              # thirty-twos
+    (16, 4000), (16, 8000), (16, 12000), (16, 20000), (16, 33000),  # sixteens
+    (32, 12000), (32, 20000), (32, 33000), (31, 66000),  # thirty-twos
 ])
 @pytest.mark.parametrize("pair", [False, True])
 def test_dense_sizes_of_each_split(rows, N, pair):
