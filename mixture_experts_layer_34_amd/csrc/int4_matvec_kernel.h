@@ -138,8 +138,13 @@ __device__ __forceinline__ void spread_quarters(uint32_t v, uint32_t (&o)[4]) {
 // (a load that is not wanted is sent past its buffer's end): where a load may
 // or may not be outstanding, the compiler can no longer count those in flight
 // and waits for all of them, which empties the ring once a round.
+//
+// A single matrix in thirty-twos whose waves do not split K is held to 128
+// registers, two workgroups a compute unit (20480 x 4096, groups of 32, 64 rows
+// 57.5 -> 47.3 us, nothing spilled); the others either fit or spill for it (a
+// pair in sixteens loses 2 to 20 %).
 template <int DT, int NM, int NG, int RT, int GS, int KS, int NW, int SCH, bool WHOLE>
-__global__ __launch_bounds__(64 * KS * NW) void int4_matvec_kernel(Int4Args a, const int32_t* __restrict__ offsets,
+__global__ __launch_bounds__(64 * KS * NW, RT == 32 && NM == 1 && KS == 1 ? 4 : 1) void int4_matvec_kernel(Int4Args a, const int32_t* __restrict__ offsets,
                                                                    const int32_t* __restrict__ pair_of_row) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NB = NM * NG;
