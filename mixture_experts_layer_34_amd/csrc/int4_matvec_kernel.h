@@ -541,9 +541,12 @@ template <int DT, int NM, int RT, int GS> hipError_t run(const Int4Args& a, hipS
 // rows 796 / 317 / 262; a single matrix with 64 rows 51 / 21.8 / 18.4 at 8192 x
 // 4096, 18.5 in sixteens and 16.8 in thirty-twos at 5120, 13.5 and 16.9 at 4096;
 // with five to eight rows 11.6 in fours and 10.8 in sixteens, but 6.4 and 8.0 at
-// 2048 x 4096, where fours leave most of the device idle.  A single matrix in
-// sixteens takes 32 columns a wave where that fills the device (128 experts'
-// down product of 128 tokens 115 -> 108 us): x is then read once for both.
+// 2048 x 4096, where fours leave most of the device idle.  Where 32 columns
+// a wave fill the device, a single matrix in sixteens takes them: x is then read
+// once for both (128 experts' down product of 128 tokens 97 us, 108 by eight
+// waves of 16 columns).  With groups of 32 their scales cost a workgroup's place
+// on the compute unit, and eight waves of 16 columns are faster (32 experts,
+// 4096 x 1536, four rows each 38.3 -> 33.9 us, 128 experts 121 -> 118).
 template <int DT, int GS> hipError_t run_group(const Int4Args& a, hipStream_t s) {
   if constexpr (GS < kChunk) {
     // a last chunk that is not whole: scales and zeros one by one, in sixteens
@@ -558,7 +561,10 @@ template <int DT, int GS> hipError_t run_group(const Int4Args& a, hipStream_t s)
   if (few) return a.pair ? run<DT, 2, 4, GS>(a, s) : run<DT, 1, 4, GS>(a, s);
   if (a.rows > 16 * experts && waves_of(a, 32, 1) * 16 >= 5 * kWanted)
     return a.pair ? run<DT, 2, 32, GS>(a, s) : run<DT, 1, 32, GS>(a, s);
-  if (!a.pair && waves_of(a, 16, 2) >= kWanted) return run_cfg<DT, 1, 2, 16, GS, 1, 4, 4>(a, s);
+  if (!a.pair && waves_of(a, 16, 2) >= kWanted) {
+    if constexpr (GS == 32) return run_cfg<DT, 1, 1, 16, GS, 1, 8, 4>(a, s);
+    else return run_cfg<DT, 1, 2, 16, GS, 1, 4, 4>(a, s);
+  }
   return a.pair ? run<DT, 2, 16, GS>(a, s) : run<DT, 1, 16, GS>(a, s);
 }
 
