@@ -39,10 +39,10 @@
 // too few units, their fp32 sums then meeting in LDS, added in wave order: the
 // same bits on every run.
 //
-// Measured: gate / up of 128 experts (d 4096, F 1536) 169 us for 128 tokens
-// (groups of 128; 4.9 TB/s of codes and scales), 128 us for 16 tokens (82
-// experts, groups of 32 with zero points; 4.8 TB/s), 16.3 us for one (8
-// experts; 3.2 TB/s, 6 us of it the launch and the first loads).  A ring of
+// Measured: gate / up of 128 experts (d 4096, F 1536) 171 us for 128 tokens
+// (groups of 128; 4.9 TB/s of codes and scales), 129 us for 16 tokens (82
+// experts, groups of 32 with zero points; 4.8 TB/s), 16.5 us for one (8
+// experts; 3.1 TB/s, 6 us of it the launch and the first loads).  A ring of
 // eight chunks is level at best and loses up to 37 % (one token's down product
 // 11.3 -> 12.0, 8 experts' with 128 rows 46.8 -> 64 us); non-temporal loads of
 // the codes gave nothing.  Past sixteen rows the vector units taking the codes
