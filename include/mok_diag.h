@@ -1,6 +1,7 @@
 /*
- * mok_diag.h — diagnostics of the matrix cores the MoE layer runs on
- * (libmok_diag.so, separate from the layer's libmok.so).  Test support only.
+ * mok_diag.h — diagnostics of the matrix cores the MoE layer runs on, and host
+ * views of what the expert operators' launches decide (libmok_diag.so, separate
+ * from the layer's libmok.so).  Test support only.
  */
 #ifndef MOK_DIAG_H_
 #define MOK_DIAG_H_
@@ -57,6 +58,14 @@ int32_t mok_diag_mfma_scale_raw(const uint32_t* a, const uint32_t* b, const uint
  * failed launch.
  */
 int32_t mok_diag_e4m3_check(uint32_t n, uint32_t* count, uint32_t* first, int32_t blocks, void* stream);
+
+/*
+ * The rows that mok_expert_matvec_int4 gives an expert whose offsets are
+ * [begin, end) in a buffer of `rows` rows, by the kernel's own function, on the
+ * host: range[0] = first row, range[1] = one past the last.  Returns 0, 1 for a
+ * null pointer.
+ */
+int32_t mok_diag_expert_rows(int32_t begin, int32_t end, int32_t rows, int32_t* range);
 
 #ifdef __cplusplus
 }

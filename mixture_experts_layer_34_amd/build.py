@@ -20,6 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["route_sort.hip", "permute_combine.hip", "gemm_bf16.hip", "gemm_stream.hip", "quantize_rows.hip", "gemm_f32.hip", "gemm_mxfp8.hip", "router_gemm.hip",
            "sort_pairs.hip", "permute_rows.hip", "int4_matvec_bf16.hip", "int4_matvec_f16.hip", "quantize_int4.hip",
            "mok_abi.cpp", "expert_abi.cpp"]
+DIAG_SOURCES = ["diag_mfma.hip", "diag_expert.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17", "-Wall", "-Wno-unused-function",
          # packed fp32 arithmetic stays off: hipcc would otherwise emit packed
@@ -60,9 +61,9 @@ def build(verbose: bool = True) -> str:
     if r.returncode != 0:
         raise RuntimeError("profiling driver build failed:\n" + r.stderr)
     os.replace(drv + ".tmp", drv)
-    # matrix-core diagnostics (test support), a library of their own
-    dobj = _compile("diag_mfma.hip")
-    r = subprocess.run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", DIAG + ".tmp", dobj],
+    # diagnostics (test support), a library of their own
+    dobjs = [_compile(s) for s in DIAG_SOURCES]
+    r = subprocess.run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", DIAG + ".tmp", *dobjs],
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("diagnostics link failed:\n" + r.stderr)

@@ -7,6 +7,18 @@
 
 namespace mok {
 
+// An expert's rows [begin, end) as the offsets give them, cut to [0, rows) at
+// both ends before anything is subtracted: any two int32 leave 0 <= begin <=
+// end <= rows, and no rows where the end is not past the beginning.
+struct RowRange {
+  int begin, end;
+};
+__host__ __device__ inline RowRange cut_rows(int begin, int end, int rows) {
+  const int b = begin < 0 ? 0 : begin > rows ? rows : begin;
+  const int e = end < b ? b : end > rows ? rows : end;
+  return RowRange{b, e};
+}
+
 struct Int4Args {
   const void* x;               // [x_rows, K]
   const int32_t* pair_of_row;  // x row of row r is pair_of_row[r] / k; null: r

@@ -182,10 +182,10 @@ __global__ __launch_bounds__(64 * KS * NW, RT == 32 && NM == 1 && KS == 1 ? 4 : 
       const int e = e0 + tid;
       int n = 0;
       if (e < E_loc) {
-        const int lo = max(offsets[a.eb + e], 0), hi = min(offsets[a.eb + e + 1], a.rows);
-        n = (max(hi - lo, 0) + RT - 1) / RT;
-        s_row[e] = lo;
-        s_end[e] = hi;
+        const RowRange r = cut_rows(offsets[a.eb + e], offsets[a.eb + e + 1], a.rows);
+        n = (r.end - r.begin + RT - 1) / RT;
+        s_row[e] = r.begin;
+        s_end[e] = r.end;
       }
       const int s = wave_prefix(n);
       if (lane == 63) wsum[wave] = s;
