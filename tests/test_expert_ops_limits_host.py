@@ -31,3 +31,32 @@ def test_offsets_are_cut_at_both_ends(rows):
         want = (max(lo, 0), min(hi, rows))
         assert (begin, end) == want if want[0] < want[1] else begin == end, (lo, hi)
     assert f(0, 1, rows, None) == 1
+
+
+P = [0x10000 * (i + 1) for i in range(8)]
+WRAPS = [2 ** 32, -2 ** 32, 2 ** 31, 2 ** 40]   # added to a size that is taken: its low 32 bits may stay as they were
+
+
+@pytest.mark.parametrize("by", WRAPS)
+def test_sizes_past_32_bits_are_refused(by):
+    """Every int32 size of the separate operators, one at a time."""
+    sort = dict(T=300, k=8, E=16, expert_begin=0, expert_end=16)
+    rows = dict(T=8, k=2, d=64)
+    config = dict(rows=16, x_rows=8, k=2, E=4, expert_begin=0, expert_end=4, N=64, K=128, group=32, dtype=1)
+
+    def each(sizes, call):
+        for name in sizes:
+            with pytest.raises(mok.MokError) as ei:
+                call(**{**sizes, name: sizes[name] + by})
+            assert ei.value.status == mok.MOK_ERR_INVALID_ARG, name
+
+    each(dict(T=300, k=8, E=16), mok.mok_sort_pairs_workspace_query)
+    each(sort, lambda **c: mok.mok_sort_pairs(P[0], *c.values(), *P[1:6]))
+    for f in (mok.mok_permute_rows, mok.mok_unpermute_rows):
+        each(rows, lambda **c: f(P[0], None, P[1], *c.values(), mok.MOK_DTYPE_BF16, 16, P[2]))
+    for f in (mok.mok_permute_rows_backward, mok.mok_unpermute_rows_backward):
+        each(rows, lambda **c: f(P[0], None, None, P[1], *c.values(), mok.MOK_DTYPE_BF16, 16, P[2], None))
+    each(config, lambda **c: mok.mok_int4_config(*c.values()))
+    each(config, mok.mok_int4_config)
+    each(dict(group=32), lambda **c: mok.mok_quantize_int4(P[0], 4, 128, c["group"], mok.MOK_DTYPE_BF16, P[1], P[2],
+                                                           None))
