@@ -659,8 +659,9 @@ mok_status mok_expert_matvec_int4(const void* x, const int32_t* pair_of_row, con
  *   zeros NULL  s = amax / 7, q = clamp(rint(v / s) + 8, 0, 15)
  *   zeros       lo = min(v, 0), hi = max(v, 0), s = (hi - lo) / 15,
  *               z = clamp(rint(-lo / s), 0, 15), q = clamp(rint(v / s) + z, 0, 15)
- * s is rounded to dtype first (fp32 arithmetic, ties to even); with s = 0 every
- * weight of the group is 0.
+ * s is rounded to dtype first (fp32 arithmetic, ties to even; a spread past
+ * fp32's range is taken in halves, so the scale of a finite group is finite);
+ * with s = 0 every weight of the group is 0.
  *   src     dtype [rows, K], finite, K a multiple of group; rows * K <= 2^40
  *   codes, scales, zeros  as in mok_int4_weights, rows in place of E_loc, N
  * Errors: as for mok_expert_matvec_int4.

@@ -44,7 +44,10 @@ __global__ __launch_bounds__(256) void quantize_int4_kernel(const uint4* __restr
       lo = fminf(lo, __shfl_xor(lo, o, 64));
       hi = fmaxf(hi, __shfl_xor(hi, o, 64));
     }
-    const uint16_t sb = (uint16_t)Elem<DT>::pack(zeros ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f, 0.f);
+    // hi - lo, or half of it where finite values lie further apart than fp32 reaches
+    const float span = hi - lo, wide = 0.5f * hi - 0.5f * lo;
+    const float s15 = span <= 3.4028234e38f ? span / 15.0f : wide / 15.0f * 2.0f;
+    const uint16_t sb = (uint16_t)Elem<DT>::pack(zeros ? s15 : fmaxf(hi, -lo) / 7.0f, 0.f);
     const float s = Elem<DT>::lo(sb);
     const float z = zeros ? (s > 0.f ? fminf(fmaxf(rintf(-lo / s), 0.f), 15.f) : 0.f) : 8.f;
     uint32_t c = 0;

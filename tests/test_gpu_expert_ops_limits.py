@@ -29,3 +29,23 @@ def test_offsets_far_outside_the_rows():
     ref, tol = _product_ref(x.double()[pairs.long() // k], torch.ones(T * k, dtype=torch.long, device="cuda"), w, None,
                             "bf16")
     _close(out, ref, tol, "expert 1's rows")
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("symmetric", [False, True])
+def test_quantize_the_widest_finite_group(group, symmetric):
+    """Groups whose ends lie further apart than fp32 reaches, to the largest
+    bf16 values: finite scales, and the codes and zero points of the same
+    groups 2^-8 times as large, whose scales are 2^-8 times these, bit for bit
+    (a power of two moves no rounding)."""
+    big = torch.finfo(torch.bfloat16).max
+    v = (torch.rand((6, 2 * group), generator=_gen(group)) * 2 - 1) * big
+    v[0, 0], v[0, 1] = big, -big
+    v[1, 3], v[1, 9] = big, -1.0
+    v[2] = -v[2].abs()
+    v = v.clamp(-big, big).bfloat16()
+    assert float((v.double().amax(1) - v.double().amin(1)).max()) > torch.finfo(torch.float32).max
+    w, small = (X.quantize_int4(u.cuda(), group, symmetric) for u in (v, v * 2.0 ** -8))
+    assert torch.isfinite(w.scales).all()
+    assert torch.equal(w.codes, small.codes) and torch.equal(w.scales, small.scales * 2.0 ** 8)
+    assert symmetric or torch.equal(w.zeros, small.zeros)
