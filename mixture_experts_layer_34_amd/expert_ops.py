@@ -276,7 +276,7 @@ def expert_matvec_int4(x: torch.Tensor, w: Int4Weights, pmap: PairMap | None = N
         _need(x.shape[0] == (pmap.T if from_tokens else rows), fn, "x of T token rows or T * k sorted rows expected")
     x = _ready(x)
     out = _output(fn, out, (rows, N), x.dtype, x.device, x)
-    cfg = mok.mok_int4_config(rows, x.shape[0], k, E, eb, ee, N, K, group, _DTYPES[x.dtype])
+    cfg = mok.int4_config(rows, x.shape[0], k, E, eb, ee, N, K, group, _DTYPES[x.dtype])
     _call(mok.mok_expert_matvec_int4, x, x, _ready(pmap.pair_of_row) if from_tokens else None,
           None if pmap is None else _ready(pmap.offsets), wc, uc, cfg, out)
     return out

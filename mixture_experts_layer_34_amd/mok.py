@@ -59,10 +59,6 @@ class mok_int4_config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("rows", "x_rows", "k", "E", "expert_begin", "expert_end", "N", "K", "group", "dtype")]
 
-    def __init__(self, *sizes, **named):
-        _int32("mok_int4_config", 0, *sizes, *named.values())
-        super().__init__(*sizes, **named)
-
 
 MOK_CHECK_LOGITS, MOK_CHECK_INDEX = 0x1, 0x2
 
@@ -152,10 +148,10 @@ def _ptr(v):
     return v.data_ptr()
 
 
-def _int32(where: str, *sizes):
-    """Refuses sizes that an int32 argument does not hold: ctypes would cut
-    them to their low 32 bits, and the library check what is left."""
-    if max(sizes) > 0x7FFFFFFF or min(sizes) < -0x80000000:
+def _int32(where: str, sizes: int):
+    """Refuses sizes (or-ed together) of which one is negative or past an int32:
+    ctypes would cut it to its low 32 bits, and the library check what is left."""
+    if sizes >> 31:
         raise MokError(MOK_ERR_INVALID_ARG, where)
 
 
@@ -264,7 +260,7 @@ def mok_router_logits_backward(x, Wr, dlogits, T, d, E, dx, dWr, stream=0):
 
 
 def mok_sort_pairs_workspace_query(T, k, E) -> int:
-    _int32("mok_sort_pairs_workspace_query", T, k, E)
+    _int32("mok_sort_pairs_workspace_query", T | k | E)
     n = ctypes.c_size_t()
     _check(lib().mok_sort_pairs_workspace_query(T, k, E, ctypes.byref(n)), "mok_sort_pairs_workspace_query")
     return n.value
@@ -272,38 +268,43 @@ def mok_sort_pairs_workspace_query(T, k, E) -> int:
 
 def mok_sort_pairs(topk_idx, T, k, E, expert_begin, expert_end, expert_counts, expert_offsets, row_of_pair,
                    pair_of_row, workspace, stream=0):
-    _int32("mok_sort_pairs", T, k, E, expert_begin, expert_end)
+    _int32("mok_sort_pairs", T | k | E | expert_begin | expert_end)
     _check(lib().mok_sort_pairs(_ptr(topk_idx), T, k, E, expert_begin, expert_end, _ptr(expert_counts),
                                 _ptr(expert_offsets), _ptr(row_of_pair), _ptr(pair_of_row), _ptr(workspace),
                                 stream or None), "mok_sort_pairs")
 
 
 def mok_permute_rows(x, gate, row_of_pair, T, k, d, dtype, rows, xp, stream=0):
-    _int32("mok_permute_rows", T, k, d)
+    _int32("mok_permute_rows", T | k | d)
     _check(lib().mok_permute_rows(_ptr(x), _ptr(gate), _ptr(row_of_pair), T, k, d, dtype, rows, _ptr(xp),
                                   stream or None), "mok_permute_rows")
 
 
 def mok_permute_rows_backward(dxp, x, gate, row_of_pair, T, k, d, dtype, rows, dx, dgate, stream=0):
-    _int32("mok_permute_rows_backward", T, k, d)
+    _int32("mok_permute_rows_backward", T | k | d)
     _check(lib().mok_permute_rows_backward(_ptr(dxp), _ptr(x), _ptr(gate), _ptr(row_of_pair), T, k, d, dtype, rows,
                                            _ptr(dx), _ptr(dgate), stream or None), "mok_permute_rows_backward")
 
 
 def mok_unpermute_rows(y, gate, row_of_pair, T, k, d, dtype, rows, out, stream=0):
-    _int32("mok_unpermute_rows", T, k, d)
+    _int32("mok_unpermute_rows", T | k | d)
     _check(lib().mok_unpermute_rows(_ptr(y), _ptr(gate), _ptr(row_of_pair), T, k, d, dtype, rows, _ptr(out),
                                     stream or None), "mok_unpermute_rows")
 
 
 def mok_unpermute_rows_backward(dout, y, gate, row_of_pair, T, k, d, dtype, rows, dy, dgate, stream=0):
-    _int32("mok_unpermute_rows_backward", T, k, d)
+    _int32("mok_unpermute_rows_backward", T | k | d)
     _check(lib().mok_unpermute_rows_backward(_ptr(dout), _ptr(y), _ptr(gate), _ptr(row_of_pair), T, k, d, dtype, rows,
                                              _ptr(dy), _ptr(dgate), stream or None), "mok_unpermute_rows_backward")
 
 
 def int4_weights(codes, scales, zeros) -> mok_int4_weights:
     return mok_int4_weights(_ptr(codes), _ptr(scales), _ptr(zeros))
+
+
+def int4_config(rows, x_rows, k, E, expert_begin, expert_end, N, K, group, dtype) -> mok_int4_config:
+    _int32("mok_int4_config", rows | x_rows | k | E | expert_begin | expert_end | N | K | group | dtype)
+    return mok_int4_config(rows, x_rows, k, E, expert_begin, expert_end, N, K, group, dtype)
 
 
 def mok_expert_matvec_int4(x, pair_of_row, expert_offsets, w: mok_int4_weights, w_up: mok_int4_weights | None,

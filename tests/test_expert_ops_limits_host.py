@@ -56,7 +56,6 @@ def test_sizes_past_32_bits_are_refused(by):
         each(rows, lambda **c: f(P[0], None, P[1], *c.values(), mok.MOK_DTYPE_BF16, 16, P[2]))
     for f in (mok.mok_permute_rows_backward, mok.mok_unpermute_rows_backward):
         each(rows, lambda **c: f(P[0], None, None, P[1], *c.values(), mok.MOK_DTYPE_BF16, 16, P[2], None))
-    each(config, lambda **c: mok.mok_int4_config(*c.values()))
-    each(config, mok.mok_int4_config)
+    each(config, mok.int4_config)
     each(dict(group=32), lambda **c: mok.mok_quantize_int4(P[0], 4, 128, c["group"], mok.MOK_DTYPE_BF16, P[1], P[2],
                                                            None))
