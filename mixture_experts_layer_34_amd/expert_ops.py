@@ -5,8 +5,8 @@ with their gradients, and expert products with 4-bit integer weights.
 Torch plumbing around the C ABI (include/mok.h): tensors are checked, outputs
 allocated unless given, and the kernels enqueued on the tensors' device, on
 its current stream.  Inputs that are not contiguous (or not 16-byte aligned)
-are copied; an output given by the caller has to be both, and apart from the
-inputs.  Nothing is recorded for autograd: the gradients are the _backward
+are copied; an output given by the caller has to be both, and apart from every
+input (rows, gates, maps and weights).  Nothing is recorded for autograd: the gradients are the _backward
 functions'."""
 from __future__ import annotations
 
@@ -143,9 +143,9 @@ def permute_rows(x: torch.Tensor, pmap: PairMap, gate: torch.Tensor | None = Non
     fn = "permute_rows"
     d, dt = _rows_args(fn, pmap, gate, x, out)
     rows = pmap.T * pmap.k if out is None else out.shape[0]
-    x = _ready(x)
-    out = _output(fn, out, (rows, d), x.dtype, x.device, x)
-    _call(mok.mok_permute_rows, x, x, _ready(gate), _ready(pmap.row_of_pair), pmap.T, pmap.k, d, dt, rows, out)
+    x, gate, rop = _ready(x), _ready(gate), _ready(pmap.row_of_pair)
+    out = _output(fn, out, (rows, d), x.dtype, x.device, x, gate, rop)
+    _call(mok.mok_permute_rows, x, x, gate, rop, pmap.T, pmap.k, d, dt, rows, out)
     return out
 
 
@@ -166,10 +166,9 @@ def unpermute_rows(y: torch.Tensor, pmap: PairMap, gate: torch.Tensor | None = N
     """out[t] = sum_j gate[t, j] * y[row(t, j)], in fp32, rounded once."""
     fn = "unpermute_rows"
     d, dt = _rows_args(fn, pmap, gate, None, y)
-    y = _ready(y)
-    out = _output(fn, out, (pmap.T, d), y.dtype, y.device, y)
-    _call(mok.mok_unpermute_rows, y, y, _ready(gate), _ready(pmap.row_of_pair), pmap.T, pmap.k, d, dt, y.shape[0],
-          out)
+    y, gate, rop = _ready(y), _ready(gate), _ready(pmap.row_of_pair)
+    out = _output(fn, out, (pmap.T, d), y.dtype, y.device, y, gate, rop)
+    _call(mok.mok_unpermute_rows, y, y, gate, rop, pmap.T, pmap.k, d, dt, y.shape[0], out)
     return out
 
 
@@ -181,11 +180,10 @@ def unpermute_rows_backward(dout: torch.Tensor, pmap: PairMap, gate: torch.Tenso
     fn = "unpermute_rows_backward"
     d, dt = _rows_args(fn, pmap, gate, dout, y)
     rows = y.shape[0] if y is not None else pmap.T * pmap.k if out is None else out.shape[0]
-    dout, y = _ready(dout), _ready(y)
-    dy = _output(fn, out, (rows, d), dout.dtype, dout.device, dout, y)
+    dout, y, gate, rop = _ready(dout), _ready(y), _ready(gate), _ready(pmap.row_of_pair)
+    dy = _output(fn, out, (rows, d), dout.dtype, dout.device, dout, y, gate, rop)
     dgate = None if y is None else torch.empty((pmap.T, pmap.k), dtype=torch.float32, device=dout.device)
-    _call(mok.mok_unpermute_rows_backward, dout, dout, y, _ready(gate), _ready(pmap.row_of_pair), pmap.T, pmap.k, d,
-          dt, rows, dy, dgate)
+    _call(mok.mok_unpermute_rows_backward, dout, dout, y, gate, rop, pmap.T, pmap.k, d, dt, rows, dy, dgate)
     return dy, dgate
 
 
@@ -275,10 +273,12 @@ def expert_matvec_int4(x: torch.Tensor, w: Int4Weights, pmap: PairMap | None = N
         _need(E_w == ee - eb, fn, "weights of the map's local experts expected")
         _need(x.shape[0] == (pmap.T if from_tokens else rows), fn, "x of T token rows or T * k sorted rows expected")
     x = _ready(x)
-    out = _output(fn, out, (rows, N), x.dtype, x.device, x)
+    pair = _ready(pmap.pair_of_row) if from_tokens else None
+    offsets = None if pmap is None else _ready(pmap.offsets)
+    read = () if out is None else [x, pair, offsets] + [t for m in (w, w_up) if m for t in (m.codes, m.scales, m.zeros)]
+    out = _output(fn, out, (rows, N), x.dtype, x.device, *read)
     cfg = mok.int4_config(rows, x.shape[0], k, E, eb, ee, N, K, group, _DTYPES[x.dtype])
-    _call(mok.mok_expert_matvec_int4, x, x, _ready(pmap.pair_of_row) if from_tokens else None,
-          None if pmap is None else _ready(pmap.offsets), wc, uc, cfg, out)
+    _call(mok.mok_expert_matvec_int4, x, x, pair, offsets, wc, uc, cfg, out)
     return out
 
 

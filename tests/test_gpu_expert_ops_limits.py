@@ -49,3 +49,50 @@ def test_quantize_the_widest_finite_group(group, symmetric):
     assert torch.isfinite(w.scales).all()
     assert torch.equal(w.codes, small.codes) and torch.equal(w.scales, small.scales * 2.0 ** 8)
     assert symmetric or torch.equal(w.zeros, small.zeros)
+
+
+def test_outputs_apart_from_gates_maps_and_weights():
+    """An output over the gates, the map or the weights of its own call is
+    refused, one right behind them in the same buffer is not."""
+    T, k, E, d = 64, 2, 4, 32
+    g = _gen(31)
+    m = X.sort_pairs(torch.randint(0, E, (T, k), generator=g, dtype=torch.int32).cuda(), E)
+
+    def beside(t, shape, dtype):
+        """(t again in a buffer of its own, an output over its last 16 bytes, one right behind it)"""
+        n = -(-t.nbytes // 16) * 16
+        size = torch.empty(shape, dtype=dtype).nbytes
+        raw = torch.zeros(n + size, dtype=torch.uint8, device="cuda")
+        raw[:t.nbytes] = t.contiguous().reshape(-1).view(torch.uint8)
+        view = lambda at, like, s: raw[at:at + like].view(dtype if s is shape else t.dtype).view(s)
+        return view(0, t.nbytes, t.shape), view(n - 16, size, shape), view(n, size, shape)
+
+    def check(t, shape, dtype, call):
+        t2, over, behind = beside(t, shape, dtype)
+        with pytest.raises(ValueError, match="overlap"):
+            call(t2, over)
+        want = call(t2, None)
+        got = call(t2, behind)
+        assert got.data_ptr() == behind.data_ptr() and torch.equal(got, want)
+
+    f32 = torch.float32
+    x, y, gate = _randn(g, (T, d)), _randn(g, (T * k, d)), torch.rand((T, k), generator=g).cuda()
+    named = lambda **o: X.PairMap(m.T, m.k, m.E, 0, E, **{**dict(
+        counts=m.counts, offsets=m.offsets, row_of_pair=m.row_of_pair, pair_of_row=m.pair_of_row), **o})
+    for op, src, shape in ((X.permute_rows, x, (T * k, d)), (X.unpermute_rows, y, (T, d)),
+                           (lambda *a, **o: X.unpermute_rows_backward(*a, **o)[0], x, (T * k, d))):
+        check(gate, shape, f32, lambda t, o: op(src, m, gate=t, out=o))
+        check(m.row_of_pair, shape, f32, lambda t, o: op(src, named(row_of_pair=t), gate=gate, out=o))
+    bf = torch.bfloat16
+    w = [_weights(g, E, d, 64, 32, True, "bf16") for _ in range(2)]
+    xb, out = _randn(g, (T, 64), "bf16"), (T * k, d)
+    call = lambda o, a=w[0], b=w[1], mm=m: X.expert_matvec_int4(xb, a, mm, w_up=b, from_tokens=True, out=o)
+    check(m.pair_of_row, out, bf, lambda t, o: call(o, mm=named(pair_of_row=t)))
+    check(m.offsets, out, bf, lambda t, o: call(o, mm=named(offsets=t)))
+    for name in ("codes", "scales", "zeros"):
+        for i in range(2):
+            def with_array(t, o):
+                ws = list(w)
+                ws[i] = X.Int4Weights(**{**dict(codes=w[i].codes, scales=w[i].scales, zeros=w[i].zeros), name: t})
+                return call(o, *ws)
+            check(getattr(w[i], name), out, bf, with_array)
