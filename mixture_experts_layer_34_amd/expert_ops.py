@@ -83,10 +83,18 @@ class PairMap:
     pair_of_row: torch.Tensor
 
     def __post_init__(self):
-        shapes = ((self.E,), (self.E + 1,), (self.T, self.k), (self.T * self.k,))
-        for t, shape in zip((self.counts, self.offsets, self.row_of_pair, self.pair_of_row), shapes):
-            _need(t.dtype == torch.int32 and tuple(t.shape) == shape and t.device == self.counts.device,
-                  "PairMap", "int32 counts [E], offsets [E + 1], row_of_pair [T, k], pair_of_row [T * k] on one device")
+        for name, shape in zip(("counts", "offsets", "row_of_pair", "pair_of_row"),
+                               ((self.E,), (self.E + 1,), (self.T, self.k), (self.T * self.k,))):
+            self._array("PairMap", name, shape)
+            _need(getattr(self, name).device == self.counts.device, "PairMap", "arrays on one device expected")
+
+    def _array(self, fn: str, name: str, shape) -> torch.Tensor:
+        """An array by name, with the type and shape it has to have: checked at
+        every use, for a tensor can be resized or given other data in place."""
+        t = getattr(self, name)
+        if t.dtype != torch.int32 or t.shape != shape:
+            raise ValueError(f"{fn}: int32 {name} {list(shape)} of the pair map expected")
+        return t
 
     @classmethod
     def _of(cls, *fields):
@@ -129,9 +137,9 @@ def _rows_args(fn: str, pmap: PairMap, gate, tokens, rows):
     _need(tokens is None or tuple(tokens.shape) == (pmap.T, d), fn, "token rows [T, d] expected")
     _need(rows is None or (rows.dim() == 2 and rows.dtype == ref.dtype and rows.shape[1] == d),
           fn, "expert rows [rows, d] of the tokens' type expected")
-    _need(gate is None or (gate.dtype == torch.float32 and gate.shape == pmap.row_of_pair.shape),
-          fn, "fp32 gate [T, k] expected")
-    _on(fn, ref, tokens, rows, gate, pmap.row_of_pair)
+    rop = pmap._array(fn, "row_of_pair", (pmap.T, pmap.k))
+    _need(gate is None or (gate.dtype == torch.float32 and gate.shape == rop.shape), fn, "fp32 gate [T, k] expected")
+    _on(fn, ref, tokens, rows, gate, rop)
     return d, dt
 
 
@@ -259,7 +267,9 @@ def expert_matvec_int4(x: torch.Tensor, w: Int4Weights, pmap: PairMap | None = N
     uc = None
     _need(x.dim() == 2 and x.dtype == w.scales.dtype and x.shape[1] == K, fn,
           "x [rows, K] of the scales' type expected")
-    _on(fn, x, w.codes, None if w_up is None else w_up.codes, None if pmap is None else pmap.offsets)
+    pair = pmap._array(fn, "pair_of_row", (pmap.T * pmap.k,)) if from_tokens and pmap is not None else None
+    offsets = None if pmap is None else pmap._array(fn, "offsets", (pmap.E + 1,))
+    _on(fn, x, w.codes, None if w_up is None else w_up.codes, offsets, pair)
     if w_up is not None:
         up = w_up.view(fn)
         uc = up[4]
@@ -272,9 +282,7 @@ def expert_matvec_int4(x: torch.Tensor, w: Int4Weights, pmap: PairMap | None = N
         rows, k, E, eb, ee = pmap.T * pmap.k, pmap.k, pmap.E, pmap.expert_begin, pmap.expert_end
         _need(E_w == ee - eb, fn, "weights of the map's local experts expected")
         _need(x.shape[0] == (pmap.T if from_tokens else rows), fn, "x of T token rows or T * k sorted rows expected")
-    x = _ready(x)
-    pair = _ready(pmap.pair_of_row) if from_tokens else None
-    offsets = None if pmap is None else _ready(pmap.offsets)
+    x, pair, offsets = _ready(x), _ready(pair), _ready(offsets)
     read = () if out is None else [x, pair, offsets] + [t for m in (w, w_up) if m for t in (m.codes, m.scales, m.zeros)]
     out = _output(fn, out, (rows, N), x.dtype, x.device, *read)
     cfg = mok.int4_config(rows, x.shape[0], k, E, eb, ee, N, K, group, _DTYPES[x.dtype])

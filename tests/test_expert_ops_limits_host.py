@@ -6,7 +6,9 @@ import itertools
 import os
 
 import pytest
+import torch
 
+from mixture_experts_layer_34_amd import expert_ops as X
 from mixture_experts_layer_34_amd import mok
 
 MIN, MAX = -2 ** 31, 2 ** 31 - 1
@@ -59,3 +61,31 @@ def test_sizes_past_32_bits_are_refused(by):
     each(config, mok.int4_config)
     each(dict(group=32), lambda **c: mok.mok_quantize_int4(P[0], 4, 128, c["group"], mok.MOK_DTYPE_BF16, P[1], P[2],
                                                            None))
+
+
+def _map(T=4, k=2, E=3):
+    z = lambda *s: torch.zeros(s, dtype=torch.int32)
+    return X.PairMap(T, k, E, 0, E, z(E), z(E + 1), z(T, k), z(T * k))
+
+
+@pytest.mark.parametrize("change", ["data", "resize", "type"])
+def test_a_map_whose_array_was_changed_in_place_is_refused(change):
+    """A shorter array would be read past its end."""
+    def changed(name):
+        m = _map()
+        t = getattr(m, name)
+        if change == "data":
+            t.data = t[:1].clone()
+        elif change == "resize":
+            t.resize_(1, *t.shape[1:])
+        else:
+            t.data = t.to(torch.int16)
+        return m
+
+    x, y = torch.zeros(4, 8), torch.zeros(8, 8)
+    for call in (lambda m: X.permute_rows(x, m), lambda m: X.permute_rows_backward(y, m), lambda m: X.unpermute_rows(y, m),
+                 lambda m: X.unpermute_rows_backward(x, m)):
+        with pytest.raises(ValueError, match="row_of_pair"):
+            call(changed("row_of_pair"))
+        with pytest.raises(ValueError, match="GPU"):    # the other arrays are not read
+            call(changed("offsets"))

@@ -96,3 +96,19 @@ def test_outputs_apart_from_gates_maps_and_weights():
                 ws[i] = X.Int4Weights(**{**dict(codes=w[i].codes, scales=w[i].scales, zeros=w[i].zeros), name: t})
                 return call(o, *ws)
             check(getattr(w[i], name), out, bf, with_array)
+
+
+def test_a_map_whose_array_was_changed_in_place_is_refused():
+    """The 4-bit product reads offsets and, from token rows, pairs: neither is
+    followed once it is shorter than the map says."""
+    g = _gen(8)
+    idx = torch.randint(0, 4, (6, 2), generator=g, dtype=torch.int32).cuda()
+    w, x, rows = _weights(g, 4, 16, 64, 32, False, "bf16"), _randn(g, (6, 64), "bf16"), _randn(g, (12, 64), "bf16")
+    for name in ("offsets", "pair_of_row"):
+        m = X.sort_pairs(idx, 4)
+        want = X.expert_matvec_int4(rows, w, m)
+        getattr(m, name).data = getattr(m, name)[:3].clone()
+        with pytest.raises(ValueError, match=name):
+            X.expert_matvec_int4(x, w, m, from_tokens=True)
+        if name == "pair_of_row":   # not read where x holds the sorted rows
+            assert torch.equal(X.expert_matvec_int4(rows, w, m), want)
