@@ -6,8 +6,8 @@ Torch plumbing around the C ABI (include/mok.h): tensors are checked, outputs
 allocated unless given, and the kernels enqueued on the tensors' device, on
 its current stream.  Inputs that are not contiguous (or not 16-byte aligned)
 are copied; an output given by the caller has to be both, and apart from every
-input (rows, gates, maps and weights).  Nothing is recorded for autograd: the gradients are the _backward
-functions'."""
+input (rows, gates, maps and weights).  Nothing is recorded for autograd: the
+gradients are the _backward functions'."""
 from __future__ import annotations
 
 from dataclasses import dataclass
@@ -29,7 +29,8 @@ def _on(fn: str, ref: torch.Tensor, *tensors):
     _need(ref.is_cuda, fn, "tensors on a GPU expected")
     i = ref.get_device()
     for t in tensors:
-        _need(t is None or t.get_device() == i, fn, "tensors on different devices")
+        if t is not None and t.get_device() != i:
+            raise ValueError(f"{fn}: tensors on different devices")
 
 
 def _ready(t):
@@ -39,17 +40,25 @@ def _ready(t):
     return t.clone(memory_format=torch.contiguous_format)
 
 
+def _of_shape(fn: str, name: str, t: torch.Tensor, shape) -> torch.Tensor:
+    """An array of a pair map with the type and shape it has to have: checked
+    at every use, for a tensor can be resized or given other data in place."""
+    if t.dtype != torch.int32 or t.shape != shape:
+        raise ValueError(f"{fn}: int32 {name} {list(shape)} of the pair map expected")
+    return t
+
+
 def _output(fn: str, out, shape, dtype, device, *inputs):
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != shape or out.dtype != dtype or out.device != device:
+    if out.shape != shape or out.dtype != dtype or out.device != device:
         raise ValueError(f"{fn}: out must be {dtype} {shape} on {device}")
     _need(out.is_contiguous() and out.data_ptr() % 16 == 0, fn, "out must be contiguous and 16-byte aligned")
     o, end = out.data_ptr(), out.data_ptr() + out.nbytes
     for t in inputs:
         if t is not None:
             i = t.data_ptr()
-            if max(o, i) < min(end, i + t.nbytes):
+            if i < end and o < i + t.nbytes and t.nbytes and out.nbytes:
                 raise ValueError(f"{fn}: out must not overlap an input")
     return out
 
@@ -85,16 +94,8 @@ class PairMap:
     def __post_init__(self):
         for name, shape in zip(("counts", "offsets", "row_of_pair", "pair_of_row"),
                                ((self.E,), (self.E + 1,), (self.T, self.k), (self.T * self.k,))):
-            self._array("PairMap", name, shape)
-            _need(getattr(self, name).device == self.counts.device, "PairMap", "arrays on one device expected")
-
-    def _array(self, fn: str, name: str, shape) -> torch.Tensor:
-        """An array by name, with the type and shape it has to have: checked at
-        every use, for a tensor can be resized or given other data in place."""
-        t = getattr(self, name)
-        if t.dtype != torch.int32 or t.shape != shape:
-            raise ValueError(f"{fn}: int32 {name} {list(shape)} of the pair map expected")
-        return t
+            t = _of_shape("PairMap", name, getattr(self, name), shape)
+            _need(t.device == self.counts.device, "PairMap", "arrays on one device expected")
 
     @classmethod
     def _of(cls, *fields):
@@ -134,11 +135,12 @@ def _rows_args(fn: str, pmap: PairMap, gate, tokens, rows):
     dt = _DTYPES.get(ref.dtype)
     _need(dt is not None and ref.dim() == 2, fn, "fp32, bf16 or fp16 matrices expected")
     d = ref.shape[1]
-    _need(tokens is None or tuple(tokens.shape) == (pmap.T, d), fn, "token rows [T, d] expected")
+    _need(tokens is None or tokens.shape == (pmap.T, d), fn, "token rows [T, d] expected")
     _need(rows is None or (rows.dim() == 2 and rows.dtype == ref.dtype and rows.shape[1] == d),
           fn, "expert rows [rows, d] of the tokens' type expected")
-    rop = pmap._array(fn, "row_of_pair", (pmap.T, pmap.k))
-    _need(gate is None or (gate.dtype == torch.float32 and gate.shape == rop.shape), fn, "fp32 gate [T, k] expected")
+    pairs = pmap.T, pmap.k
+    rop = _of_shape(fn, "row_of_pair", pmap.row_of_pair, pairs)
+    _need(gate is None or (gate.dtype == torch.float32 and gate.shape == pairs), fn, "fp32 gate [T, k] expected")
     _on(fn, ref, tokens, rows, gate, rop)
     return d, dt
 
@@ -264,16 +266,13 @@ def expert_matvec_int4(x: torch.Tensor, w: Int4Weights, pmap: PairMap | None = N
     one matrix and every row of x is its own."""
     fn = "expert_matvec_int4"
     E_w, N, K, group, wc = w.view(fn)
-    uc = None
     _need(x.dim() == 2 and x.dtype == w.scales.dtype and x.shape[1] == K, fn,
           "x [rows, K] of the scales' type expected")
-    pair = pmap._array(fn, "pair_of_row", (pmap.T * pmap.k,)) if from_tokens and pmap is not None else None
-    offsets = None if pmap is None else pmap._array(fn, "offsets", (pmap.E + 1,))
-    _on(fn, x, w.codes, None if w_up is None else w_up.codes, offsets, pair)
+    uc = us = pair = offsets = None
     if w_up is not None:
-        up = w_up.view(fn)
+        up, us = w_up.view(fn), w_up.scales
         uc = up[4]
-        _need(up[:4] == (E_w, N, K, group) and w_up.scales.dtype == w.scales.dtype and
+        _need(up[:4] == (E_w, N, K, group) and us.dtype == w.scales.dtype and
               (w_up.zeros is None) == (w.zeros is None), fn, "w and w_up of one shape, group and kind expected")
     if pmap is None:
         _need(E_w == 1 and not from_tokens, fn, "one matrix expected without a pair map")
@@ -282,9 +281,16 @@ def expert_matvec_int4(x: torch.Tensor, w: Int4Weights, pmap: PairMap | None = N
         rows, k, E, eb, ee = pmap.T * pmap.k, pmap.k, pmap.E, pmap.expert_begin, pmap.expert_end
         _need(E_w == ee - eb, fn, "weights of the map's local experts expected")
         _need(x.shape[0] == (pmap.T if from_tokens else rows), fn, "x of T token rows or T * k sorted rows expected")
+        offsets = _of_shape(fn, "offsets", pmap.offsets, (E + 1,))
+        if from_tokens:
+            pair = _of_shape(fn, "pair_of_row", pmap.pair_of_row, (rows,))
+    _on(fn, x, w.codes, us, offsets, pair)
     x, pair, offsets = _ready(x), _ready(pair), _ready(offsets)
-    read = () if out is None else [x, pair, offsets] + [t for m in (w, w_up) if m for t in (m.codes, m.scales, m.zeros)]
-    out = _output(fn, out, (rows, N), x.dtype, x.device, *read)
+    if out is None:
+        out = torch.empty((rows, N), dtype=x.dtype, device=x.device)
+    else:
+        read = [t for m in (w, w_up) if m for t in (m.codes, m.scales, m.zeros)]
+        out = _output(fn, out, (rows, N), x.dtype, x.device, x, pair, offsets, *read)
     cfg = mok.int4_config(rows, x.shape[0], k, E, eb, ee, N, K, group, _DTYPES[x.dtype])
     _call(mok.mok_expert_matvec_int4, x, x, pair, offsets, wc, uc, cfg, out)
     return out
