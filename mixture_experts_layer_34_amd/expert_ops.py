@@ -7,7 +7,9 @@ allocated unless given, and the kernels enqueued on the tensors' device, on
 its current stream.  Inputs that are not contiguous (or not 16-byte aligned)
 are copied; an output given by the caller has to be both, and apart from every
 input (rows, gates, maps and weights).  Nothing is recorded for autograd: the
-gradients are the _backward functions'."""
+gradients are the _backward functions', and permute_rows, unpermute_rows and the
+4-bit products refuse rows, gates and scales that require one while gradients
+are recorded."""
 from __future__ import annotations
 
 from dataclasses import dataclass
@@ -31,6 +33,14 @@ def _on(fn: str, ref: torch.Tensor, *tensors):
     for t in tensors:
         if t is not None and t.get_device() != i:
             raise ValueError(f"{fn}: tensors on different devices")
+
+
+def _unrecorded(fn: str, rows, other=None, out=None, third=None):
+    """No gradient is lost without a word."""
+    if (rows.requires_grad or (other is not None and other.requires_grad) or (out is not None and out.requires_grad) or
+            (third is not None and third.requires_grad)) and torch.is_grad_enabled():
+        raise RuntimeError(f"{fn} is not recorded for autograd, but a tensor requires a gradient: call it on detached "
+                           "tensors or under torch.no_grad()")
 
 
 def _ready(t):
@@ -152,6 +162,7 @@ def permute_rows(x: torch.Tensor, pmap: PairMap, gate: torch.Tensor | None = Non
     tensor)."""
     fn = "permute_rows"
     d, dt = _rows_args(fn, pmap, gate, x, out)
+    _unrecorded(fn, x, gate, out)
     rows = pmap.T * pmap.k if out is None else out.shape[0]
     x, gate, rop = _ready(x), _ready(gate), _ready(pmap.row_of_pair)
     out = _output(fn, out, (rows, d), x.dtype, x.device, x, gate, rop)
@@ -176,6 +187,7 @@ def unpermute_rows(y: torch.Tensor, pmap: PairMap, gate: torch.Tensor | None = N
     """out[t] = sum_j gate[t, j] * y[row(t, j)], in fp32, rounded once."""
     fn = "unpermute_rows"
     d, dt = _rows_args(fn, pmap, gate, None, y)
+    _unrecorded(fn, y, gate, out)
     y, gate, rop = _ready(y), _ready(gate), _ready(pmap.row_of_pair)
     out = _output(fn, out, (pmap.T, d), y.dtype, y.device, y, gate, rop)
     _call(mok.mok_unpermute_rows, y, y, gate, rop, pmap.T, pmap.k, d, dt, y.shape[0], out)
@@ -285,6 +297,7 @@ def expert_matvec_int4(x: torch.Tensor, w: Int4Weights, pmap: PairMap | None = N
         if from_tokens:
             pair = _of_shape(fn, "pair_of_row", pmap.pair_of_row, (rows,))
     _on(fn, x, w.codes, us, offsets, pair)
+    _unrecorded(fn, x, w.scales, out, us)
     x, pair, offsets = _ready(x), _ready(pair), _ready(offsets)
     if out is None:
         out = torch.empty((rows, N), dtype=x.dtype, device=x.device)

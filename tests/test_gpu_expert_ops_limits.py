@@ -112,3 +112,33 @@ def test_a_map_whose_array_was_changed_in_place_is_refused():
             X.expert_matvec_int4(x, w, m, from_tokens=True)
         if name == "pair_of_row":   # not read where x holds the sorted rows
             assert torch.equal(X.expert_matvec_int4(rows, w, m), want)
+
+
+def test_lost_gradients_are_refused():
+    """Rows, gates, scales and outputs that require a gradient while gradients
+    are recorded; not under no_grad, detached, or in the _backward functions,
+    whose results are no one's to differentiate."""
+    T, k, E, d = 5, 2, 3, 32
+    g = _gen(9)
+    m = X.sort_pairs(torch.randint(0, E, (T, k), generator=g, dtype=torch.int32).cuda(), E)
+    x, y, gate = _randn(g, (T, d)), _randn(g, (T * k, d)), torch.rand((T, k), generator=g).cuda()
+    w, xb = _weights(g, E, 16, d, 32, False, "bf16"), _randn(g, (T, d), "bf16")
+    grad = lambda t: t.detach().clone().requires_grad_()
+    wg = X.Int4Weights(w.codes, grad(w.scales))
+    buf = lambda: torch.zeros(T * k, d, device="cuda")
+    for call in (lambda: X.permute_rows(grad(x), m, out=buf()), lambda: X.permute_rows(x, m, gate=grad(gate), out=buf()),
+                 lambda: X.permute_rows(x, m, out=grad(buf())),
+                 lambda: X.unpermute_rows(grad(y), m), lambda: X.unpermute_rows(y, m, gate=grad(gate)),
+                 lambda: X.expert_matvec_int4(grad(xb), w, m, from_tokens=True),
+                 lambda: X.expert_matvec_int4(xb, wg, m, from_tokens=True),
+                 lambda: X.expert_matvec_int4(xb, w, m, w_up=wg, from_tokens=True)):
+        with pytest.raises(RuntimeError, match="autograd"):
+            call()
+        with torch.no_grad():
+            call()
+    want = X.unpermute_rows(y, m, gate=gate)
+    assert torch.equal(X.unpermute_rows(grad(y).detach(), m, gate=grad(gate).detach()), want)
+    dx, dgate = X.permute_rows_backward(grad(y), m, gate=grad(gate), x=grad(x))
+    assert torch.equal(dx, want) and not dx.requires_grad and not dgate.requires_grad
+    X.unpermute_rows_backward(grad(x), m, gate=grad(gate), y=grad(y))
+    X.quantize_int4(grad(xb), 32)
