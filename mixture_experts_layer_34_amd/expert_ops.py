@@ -215,7 +215,8 @@ class Int4Weights:
     """Matrices [E, N, K] in 4-bit integers: uint8 codes [E, N, K / 2] (two per
     byte, the lower element in the low nibble), scales [E, N, K / group] in the
     activations' type, and uint8 zeros (0..15) like the scales (None: 8
-    everywhere)."""
+    everywhere).  They may be held on the CPU (read, pickled, moved by `to`);
+    the products take them on x's GPU."""
     codes: torch.Tensor
     scales: torch.Tensor
     zeros: torch.Tensor | None = None
@@ -242,12 +243,16 @@ class Int4Weights:
         group = K // G if G else 0
         _need(group in (32, 64, 128) and group * G == K, fn, "groups of 32, 64 or 128 expected")
         _need(z is None or (z.dtype == torch.uint8 and z.shape == s.shape), fn, "uint8 zeros like the scales expected")
-        _on(fn, q, s, z)
+        _need(s.device == q.device and (z is None or z.device == q.device), fn, "tensors on different devices")
         _need(all(t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0) for t in (q, s, z)), fn,
               "contiguous, 16-byte aligned arrays expected")
         v = (E, N, K, group, mok.int4_weights(q, s, z))
         self.__dict__["_seen"] = (now, v)
         return v
+
+    def to(self, device) -> Int4Weights:
+        return Int4Weights(self.codes.to(device), self.scales.to(device),
+                           None if self.zeros is None else self.zeros.to(device))
 
     def __reduce__(self):
         return Int4Weights, (self.codes, self.scales, self.zeros)

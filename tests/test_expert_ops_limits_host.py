@@ -2,6 +2,7 @@
 ranges: offsets, sizes and tensors that do not fit are cut or refused before a
 kernel sees them (no GPU needed)."""
 import ctypes
+import io
 import itertools
 import os
 
@@ -89,3 +90,24 @@ def test_a_map_whose_array_was_changed_in_place_is_refused(change):
             call(changed("row_of_pair"))
         with pytest.raises(ValueError, match="GPU"):    # the other arrays are not read
             call(changed("offsets"))
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+def test_weights_are_read_and_moved_on_the_cpu(zeros):
+    """Weights of a checkpoint exist on the CPU and come back from a file as
+    they were; the products refuse them there, and what does not fit is refused
+    as on a GPU."""
+    codes = torch.randint(0, 256, (2, 4, 64), dtype=torch.uint8)
+    scales = torch.rand(2, 4, 4).bfloat16()
+    w = X.Int4Weights(codes, scales, torch.randint(0, 16, (2, 4, 4), dtype=torch.uint8) if zeros else None)
+    f = io.BytesIO()
+    torch.save(w, f)
+    f.seek(0)
+    for v in (torch.load(f, map_location="cpu", weights_only=False), w.to("cpu")):
+        assert v.view("test")[:4] == (2, 4, 128, 32)
+        for a, b in ((v.codes, w.codes), (v.scales, w.scales), (v.zeros, w.zeros)):
+            assert a is None and b is None if b is None else torch.equal(a, b)
+    with pytest.raises(ValueError, match="GPU"):
+        X.expert_matvec_int4(torch.zeros(4, 128).bfloat16(), X.Int4Weights(codes[:1], scales[:1]))
+    with pytest.raises(ValueError, match="devices"):
+        X.Int4Weights(codes, scales.to("meta"))

@@ -142,3 +142,12 @@ def test_lost_gradients_are_refused():
     assert torch.equal(dx, want) and not dx.requires_grad and not dgate.requires_grad
     X.unpermute_rows_backward(grad(x), m, gate=grad(gate), y=grad(y))
     X.quantize_int4(grad(xb), 32)
+
+
+def test_weights_moved_from_the_cpu():
+    w = _weights(_gen(4), 1, 48, 128, 32, True, "bf16")
+    x = _randn(_gen(5), (3, 128), "bf16")
+    there = w.to("cpu")
+    with pytest.raises(ValueError, match="devices"):
+        X.expert_matvec_int4(x, there)
+    assert torch.equal(X.expert_matvec_int4(x, there.to("cuda")), X.expert_matvec_int4(x, w))
