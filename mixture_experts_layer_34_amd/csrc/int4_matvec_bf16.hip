@@ -2,5 +2,5 @@
 #include "int4_matvec_kernel.h"
 
 namespace mok {
-hipError_t launch_int4_matvec_bf16(const Int4Args& a, hipStream_t s) { return run_dtype<kBF16>(a, s); }
+hipError_t launch_int4_matvec_bf16(const Int4Args& a, hipStream_t s) { return launch_int4(a, Launch<kBF16>{s}); }
 }  // namespace mok

@@ -2,5 +2,5 @@
 #include "int4_matvec_kernel.h"
 
 namespace mok {
-hipError_t launch_int4_matvec_f16(const Int4Args& a, hipStream_t s) { return run_dtype<kF16>(a, s); }
+hipError_t launch_int4_matvec_f16(const Int4Args& a, hipStream_t s) { return launch_int4(a, Launch<kF16>{s}); }
 }  // namespace mok

@@ -50,8 +50,7 @@
 // x 4096) 18.4 us where four rows take 9.2.
 #pragma once
 #include "elem.h"
-#include "int4_matvec.h"
-#include "mok_internal.h"
+#include "int4_rules.h"
 #include "pair_ops.h"
 
 namespace mok {
@@ -59,7 +58,6 @@ namespace {
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
-constexpr int kChunk = 128;  // K per round: 16 bytes of codes a lane
 constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every buffer: reads as zero
 
 __device__ __forceinline__ rsrc_t buffer(const void* p, int64_t bytes) {
@@ -464,118 +462,23 @@ __global__ __launch_bounds__(64 * KS * NW, RT == 32 && NM == 1 && KS == 1 ? 4 : 
 #endif
 }
 
-template <int DT, int NM, int NG, int RT, int GS, int KS, int NW, int SCH, bool WHOLE = true>
-hipError_t run_cfg(const Int4Args& a, hipStream_t s) {
-  constexpr int64_t NU = 16 * NG * NW;
-  const int64_t ntn = (a.N + NU - 1) / NU;
-  const int64_t tiles = (a.rows + RT - 1) / RT + (a.offsets ? (a.E_loc < a.rows ? a.E_loc : a.rows) : 0);
-  const int64_t units = tiles * ntn;
-  if (units == 0) return hipSuccess;
-  const unsigned grid = (unsigned)(units < 65536 ? units : 65536);
-  hipLaunchKernelGGL((int4_matvec_kernel<DT, NM, NG, RT, GS, KS, NW, SCH, WHOLE>), dim3(grid), dim3(64 * KS * NW),
-                     (3 * a.E_loc + 1) * sizeof(int32_t), s, a,
-                     a.offsets, a.pair_of_row);
-  return hipGetLastError();
-}
-
-constexpr int64_t kWanted = 8 * kNumCUs;  // waves that fill the device, eight a compute unit
-
-// Waves of a call whose waves do not split K: its row tiles times N's columns.
-// The rows of each expert are known on the device only: one tile, or rows / rt
-// and a part of one (half a tile far past rt rows, none up to them).
-inline int64_t waves_of(const Int4Args& a, int rt, int ng) {
-  const int64_t experts = a.E_loc < a.rows ? a.E_loc : a.rows;
-  const int64_t some = (8 * (int64_t)a.rows / rt + 3 * experts) / 8;
-  const int64_t tiles = !a.offsets ? (a.rows + rt - 1) / rt : some > experts ? some : experts;
-  return tiles * ((a.N + 16 * ng - 1) / (16 * ng));
-}
-
-// A wave by itself on its columns needs no sum and no more barriers than x's,
-// so K is split only as far as it takes to fill the device, and waves that
-// split K keep others beside them to share x, eight in a workgroup (in tiles of
-// four, where x is small, as few as give each its share): gate / up of one token
-// (768 groups of 16 columns) 20.7 / 17.9 / 16.7 / 20.5 us for splits of 1 / 2 /
-// 4 / 8, a dense 4099 x 7168 product of three rows 22.9 / 14.9 / 11.8 / 10.2 us;
-// sixteen tokens' gate / up (7,900 groups) 134 / 129 / 165 / 199 us.
-//
-// From sixteen rows a tile a compute unit holds one workgroup of eight waves of
-// a pair (or of thirty-two rows), so one workgroup more than there are compute
-// units costs a whole second round, and the split is the largest that needs no
-// second one.  A pair of matrices with K 4096 and 16 rows, for splits of 8 / 4 /
-// 2 / 1 in eight waves each: N 6144 (384 groups) 19.6 / 14.3 /
-// 18.1 / 27.9 us, 10240 (640) 28.0 / 25.7 / 19.1 / 28.5, 18432 (1152) 45.2 /
-// 37.5 / 35.7 / 31.2; with 64 rows in thirty-twos 8192 (1024) - / - / 25.7 /
-// 36.7, 10240 (1280) - / - / 45.5 / 37.3.  A single matrix in sixteens shares
-// its compute unit: a split of two up to a whole device (18432 columns 19.6 us,
-// 19.9 whole); in thirty-twos sixteen waves of a split of two take the second
-// half device (12288 columns, 64 rows 23.9 us, 25.4 whole, 31.1 in eight
-// waves).  Past a device's waves a pair's workgroups are of four waves (128
-// experts' gate / up of 128 tokens 176 us, 197 by eight).
-template <int DT, int NM, int RT, int GS> hipError_t run(const Int4Args& a, hipStream_t s) {
-  const int64_t waves = waves_of(a, RT, 1);
-  if constexpr (RT == 4) {
-    if (waves * 4 * NM <= kWanted) return run_cfg<DT, NM, 1, RT, GS, 8, 1, 8>(a, s);
-    if (waves * 8 <= 3 * kWanted) return run_cfg<DT, NM, 1, RT, GS, 4, 1, 4>(a, s);
-    if (waves <= kWanted) return run_cfg<DT, NM, 1, RT, GS, 2, 2, 4>(a, s);
-    return run_cfg<DT, NM, 1, RT, GS, 1, 4, 4>(a, s);
-  } else if constexpr (RT == 16) {
-    if (waves * 8 <= kWanted) return run_cfg<DT, NM, 1, RT, GS, 8, 1, 8>(a, s);
-    if (waves * 4 <= kWanted) return run_cfg<DT, NM, 1, RT, GS, 4, 2, 4>(a, s);
-    if (waves * NM <= kWanted) return run_cfg<DT, NM, 1, RT, GS, 2, 4, 4>(a, s);
-    if constexpr (NM == 2)
-      if (waves <= kWanted) return run_cfg<DT, NM, 1, RT, GS, 1, 8, 4>(a, s);
-    return run_cfg<DT, NM, 1, RT, GS, 1, 4, 4>(a, s);
-  } else {
-    if (waves * 2 <= kWanted) return run_cfg<DT, NM, 1, RT, GS, 2, 4, 4>(a, s);
-    if (waves <= kWanted) return run_cfg<DT, NM, 1, RT, GS, NM == 1 ? 2 : 1, 8, 4>(a, s);
-    return run_cfg<DT, NM, 1, RT, GS, 1, NM == 1 ? 8 : 4, 4>(a, s);
+// One configuration's launch (int4_rules.h says which).
+template <int DT> struct Launch {
+  hipStream_t s;
+  template <int NM, int NG, int RT, int GS, int KS, int NW, int SCH, bool WHOLE>
+  hipError_t run(const Int4Args& a) const {
+    constexpr int64_t NU = 16 * NG * NW;
+    const int64_t ntn = (a.N + NU - 1) / NU;
+    const int64_t tiles = (a.rows + RT - 1) / RT + (a.offsets ? (a.E_loc < a.rows ? a.E_loc : a.rows) : 0);
+    const int64_t units = tiles * ntn;
+    if (units == 0) return hipSuccess;
+    const unsigned grid = (unsigned)(units < 65536 ? units : 65536);
+    hipLaunchKernelGGL((int4_matvec_kernel<DT, NM, NG, RT, GS, KS, NW, SCH, WHOLE>), dim3(grid), dim3(64 * KS * NW),
+                       (3 * a.E_loc + 1) * sizeof(int32_t), s, a,
+                       a.offsets, a.pair_of_row);
+    return hipGetLastError();
   }
-}
-
-// Rows per tile, from an expert's rows on average: four up to two rows (x then
-// costs a quarter; experts with more take several tiles), sixteen, and
-// thirty-two past sixteen rows, where taking the codes apart bounds the
-// product, if that leaves no more than three eighths of the device idle.  Gate /
-// up of 128 experts in fours / sixteens / thirty-twos: one row each 108 / 112 /
-// 158 us, two 142 / 145 / 205, four 198 / 161 / 226, eight 333 / 174 / 238, 24
-// rows 796 / 317 / 262; a single matrix with 64 rows 51 / 21.8 / 18.4 at 8192 x
-// 4096, 18.5 in sixteens and 16.8 in thirty-twos at 5120, 13.5 and 16.9 at 4096;
-// with five to eight rows 11.6 in fours and 10.8 in sixteens, but 6.4 and 8.0 at
-// 2048 x 4096, where fours leave most of the device idle.  Where 32 columns
-// a wave fill the device, a single matrix in sixteens takes them: x is then read
-// once for both (128 experts' down product of 128 tokens 97 us, 108 by eight
-// waves of 16 columns).  With groups of 32 their scales cost a workgroup's place
-// on the compute unit, and eight waves of 16 columns are faster (32 experts,
-// 4096 x 1536, four rows each 38.3 -> 33.9 us, 128 experts 121 -> 118).
-template <int DT, int GS> hipError_t run_group(const Int4Args& a, hipStream_t s) {
-  if constexpr (GS < kChunk) {
-    // a last chunk that is not whole: scales and zeros one by one, in sixteens
-    if (a.K % kChunk) {
-      const bool many = waves_of(a, 16, 1) >= kWanted;
-      if (a.pair) return many ? run_cfg<DT, 2, 1, 16, GS, 1, 4, 4, false>(a, s) : run_cfg<DT, 2, 1, 16, GS, 4, 2, 4, false>(a, s);
-      return many ? run_cfg<DT, 1, 1, 16, GS, 1, 4, 4, false>(a, s) : run_cfg<DT, 1, 1, 16, GS, 4, 2, 4, false>(a, s);
-    }
-  }
-  const int64_t experts = a.offsets ? a.E_loc : 1;
-  const bool few = a.offsets ? a.rows <= 2 * experts : a.rows <= 4 || (a.rows <= 8 && waves_of(a, 4, 1) * 4 < kWanted);
-  if (few) return a.pair ? run<DT, 2, 4, GS>(a, s) : run<DT, 1, 4, GS>(a, s);
-  if (a.rows > 16 * experts && waves_of(a, 32, 1) * 16 >= 5 * kWanted)
-    return a.pair ? run<DT, 2, 32, GS>(a, s) : run<DT, 1, 32, GS>(a, s);
-  if (!a.pair && waves_of(a, 16, 2) >= kWanted) {
-    if constexpr (GS == 32) return run_cfg<DT, 1, 1, 16, GS, 1, 8, 4>(a, s);
-    else return run_cfg<DT, 1, 2, 16, GS, 1, 4, 4>(a, s);
-  }
-  return a.pair ? run<DT, 2, 16, GS>(a, s) : run<DT, 1, 16, GS>(a, s);
-}
-
-template <int DT> hipError_t run_dtype(const Int4Args& a, hipStream_t s) {
-  switch (a.group) {
-    case 32: return run_group<DT, 32>(a, s);
-    case 64: return run_group<DT, 64>(a, s);
-    case 128: return run_group<DT, 128>(a, s);
-  }
-  return hipErrorInvalidValue;
-}
+};
 
 }  // namespace
 
