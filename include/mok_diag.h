@@ -73,7 +73,7 @@ int32_t mok_diag_expert_rows(int32_t begin, int32_t end, int32_t rows, int32_t* 
  * host: config = {matrices, column groups of 16 a wave, rows a tile, group,
  * waves along K, waves along N, chunks of x a stage, 1 if K is a whole number
  * of chunks}, left as it was where nothing is launched.  Returns 0, 1 for a null
- * pointer or a group that is not 32, 64 or 128.
+ * pointer, no experts or a group that is not 32, 64 or 128.
  */
 int32_t mok_diag_int4_config(int32_t rows, int32_t E, int32_t E_loc, int32_t routed, int32_t N, int32_t K,
                              int32_t group, int32_t pair, int32_t* config);

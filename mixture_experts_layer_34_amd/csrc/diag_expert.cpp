@@ -17,13 +17,14 @@ struct Report {
 
 }  // namespace
 
-extern "C" int32_t mok_diag_int4_config(int32_t rows, int32_t, int32_t E_loc, int32_t routed, int32_t N, int32_t K,
+extern "C" int32_t mok_diag_int4_config(int32_t rows, int32_t E, int32_t E_loc, int32_t routed, int32_t N, int32_t K,
                                         int32_t group, int32_t pair, int32_t* config) {
-  if (!config) return 1;
+  if (!config || E < 1) return 1;
   static const int32_t some[2] = {};
   mok::Int4Args a{};
   a.offsets = routed ? some : nullptr;  // only whether there are any is asked
   a.rows = rows;
+  a.E = E;
   a.E_loc = E_loc;
   a.N = N;
   a.K = K;

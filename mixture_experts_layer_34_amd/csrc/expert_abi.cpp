@@ -133,6 +133,7 @@ mok_status mok_expert_matvec_int4(const void* x, const int32_t* pair_of_row, con
   a.rows = c.rows;
   a.x_rows = c.x_rows;
   a.k = c.k;
+  a.E = c.E;
   a.eb = c.expert_begin;
   a.E_loc = E_loc;
   a.N = c.N;

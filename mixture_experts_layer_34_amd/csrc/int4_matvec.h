@@ -28,7 +28,7 @@ struct Int4Args {
   const uint8_t* zeros[2];     // like the scales, or null: 8
   void* out;                   // [rows, N]
   int rows, x_rows, k;
-  int eb, E_loc;
+  int E, eb, E_loc;            // experts of the offsets; the local ones [eb, eb + E_loc)
   int N, K, group;
   int pair;                    // two matrices: out = silu(first) * second
 };

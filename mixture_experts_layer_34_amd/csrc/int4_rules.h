@@ -11,13 +11,22 @@ namespace mok {
 constexpr int kChunk = 128;  // K per round: 16 bytes of codes a lane
 constexpr int64_t kWanted = 8 * kNumCUs;  // waves that fill the device, eight a compute unit
 
+// Rows that a call's experts can expect: a pair map's rows are those of all its
+// E experts, of which the call holds E_loc (how many each has is known on the
+// device only).  128 tokens, top 8, on 32 of 256 experts (gate / up 1536 x 4096):
+// 50 us in the sixteens of four rows an expert, 64 in the thirty-twos of all 32;
+// 16 tokens 26 us in fours, 32 in sixteens.
+inline int64_t local_rows(const Int4Args& a) {
+  return a.offsets ? ((int64_t)a.rows * a.E_loc + a.E - 1) / a.E : a.rows;
+}
+
 // Waves of a call whose waves do not split K: its row tiles times N's columns.
-// The rows of each expert are known on the device only: one tile, or rows / rt
-// and a part of one (half a tile far past rt rows, none up to them).
+// An expert has one tile, or its rows / rt and a part of one (half a tile far
+// past rt rows, none up to them).
 inline int64_t waves_of(const Int4Args& a, int rt, int ng) {
-  const int64_t experts = a.E_loc < a.rows ? a.E_loc : a.rows;
-  const int64_t some = (8 * (int64_t)a.rows / rt + 3 * experts) / 8;
-  const int64_t tiles = !a.offsets ? (a.rows + rt - 1) / rt : some > experts ? some : experts;
+  const int64_t rows = local_rows(a), experts = a.E_loc < rows ? a.E_loc : rows;
+  const int64_t some = (8 * rows / rt + 3 * experts) / 8;
+  const int64_t tiles = !a.offsets ? (rows + rt - 1) / rt : some > experts ? some : experts;
   return tiles * ((a.N + 16 * ng - 1) / (16 * ng));
 }
 
@@ -87,10 +96,10 @@ template <int GS, class L> hipError_t launch_group(const Int4Args& a, const L& l
       return many ? l.template run<1, 1, 16, GS, 1, 4, 4, false>(a) : l.template run<1, 1, 16, GS, 4, 2, 4, false>(a);
     }
   }
-  const int64_t experts = a.offsets ? a.E_loc : 1;
-  const bool few = a.offsets ? a.rows <= 2 * experts : a.rows <= 4 || (a.rows <= 8 && waves_of(a, 4, 1) * 4 < kWanted);
+  const int64_t rows = local_rows(a), experts = a.offsets ? a.E_loc : 1;
+  const bool few = a.offsets ? rows <= 2 * experts : rows <= 4 || (rows <= 8 && waves_of(a, 4, 1) * 4 < kWanted);
   if (few) return a.pair ? launch_tiles<2, 4, GS>(a, l) : launch_tiles<1, 4, GS>(a, l);
-  if (a.rows > 16 * experts && waves_of(a, 32, 1) * 16 >= 5 * kWanted)
+  if (rows > 16 * experts && waves_of(a, 32, 1) * 16 >= 5 * kWanted)
     return a.pair ? launch_tiles<2, 32, GS>(a, l) : launch_tiles<1, 32, GS>(a, l);
   if (!a.pair && waves_of(a, 16, 2) >= kWanted) {
     if constexpr (GS == 32) return l.template run<1, 1, 16, GS, 1, 8, 4, true>(a);

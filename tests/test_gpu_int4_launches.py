@@ -54,3 +54,34 @@ def test_dense(rows, N, K, group, zeros, pair, dt):
     ref, tol = _product_ref(x.double(), torch.zeros(rows, dtype=torch.long, device="cuda"), w[0], up, dt)
     _close(got, ref, tol, "one matrix")
     assert torch.equal(X.expert_matvec_int4(x, w[0], w_up=up), got)
+
+
+@pytest.mark.parametrize("T,k,E,eb,ee,N,K,group,pair", [
+    (128, 8, 256, 32, 64, 528, 640, 128, True),     # four rows an expert: in sixteens
+    (128, 8, 256, 224, 256, 1040, 384, 32, False),
+    (16, 8, 128, 0, 16, 272, 1152, 64, True),       # one row: in fours
+    (256, 4, 64, 60, 64, 2000, 640, 64, False),     # sixteen rows
+    (300, 8, 16, 3, 4, 4100, 384, 128, False),      # 150 rows: thirty-twos; skewed, workgroups loop
+    (1, 8, 128, 0, 16, 144, 640, 32, True),         # one row for all of them
+])
+@pytest.mark.parametrize("skewed", [False, True])
+def test_expert_parallel_share(T, k, E, eb, ee, N, K, group, pair, skewed):
+    """Weights of the local experts only, with as many rows as fall to them, or
+    every pair on one of them."""
+    note(f"{config(T * k, E, ee - eb, True, N, K, group, pair)} skewed={skewed}")
+    g = _gen(T + N)
+    idx = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)
+    if skewed:
+        idx[:] = ee - 1
+    idx = idx.cuda()
+    m = X.sort_pairs(idx, E, eb, ee)
+    P = int(m.offsets[E])
+    w = [_weights(g, ee - eb, N, K, group, True, "bf16") for _ in range(2 if pair else 1)]
+    up = w[1] if pair else None
+    x = _randn(g, (T, K), "bf16")
+    out = torch.full((T * k, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    got = X.expert_matvec_int4(x, w[0], m, w_up=up, from_tokens=True, out=out)
+    assert torch.isnan(got[P:]).all()
+    pr = m.pair_of_row[:P].long()
+    ref, tol = _product_ref(x.double()[pr // k], idx.reshape(-1)[pr].long() - eb, w[0], up, "bf16")
+    _close(got[:P], ref, tol, "local rows")

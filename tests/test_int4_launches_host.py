@@ -22,3 +22,13 @@ def test_every_configuration_has_a_case(group, pair):
     assert routed == {config(T * k, E, E, True, N, K, g, p) for T, k, E, N, K, g, _, p in ROUTED
                       if (g, p) == (group, pair)}
     assert dense == {config(rows, 1, 1, False, N, K, g, p) for rows, N, K, g, _, p in DENSE if (g, p) == (group, pair)}
+
+
+@pytest.mark.parametrize("rows,E,E_loc", [(1024, 256, 32), (128, 128, 16), (4096, 128, 4), (512, 1024, 128), (96, 24, 8)])
+@pytest.mark.parametrize("pair", [False, True])
+def test_a_share_is_taken_for_its_own_rows(rows, E, E_loc, pair):
+    """A map over part of the experts launches what a map over those experts
+    alone does, with the rows that fall to them."""
+    for N, group in itertools.product((64, 1500, 4096, 20000), (32, 64, 128)):
+        assert config(rows, E, E_loc, True, N, 1536, group, pair) == \
+            config(rows * E_loc // E, E_loc, E_loc, True, N, 1536, group, pair)
