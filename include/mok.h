@@ -640,9 +640,11 @@ typedef struct mok_int4_config {
  *                   every row (E = 1, no pair_of_row)
  *   out             dtype [rows, N]
  * Codes enter the matrix cores exactly and the scales multiply fp32 sums; one
- * rounding at the end.  x finite, below 2^100 in magnitude.  out must not
- * overlap an input.  Results are the same bits on every run.  Few rows per expert: each tile of rows reads its
- * expert's weights again.
+ * rounding at the end.  The fp32 error is of the order of 2^-24 times the sum of
+ * scale |x_i| (32 + q_i + z_i), which an x far above a row's others raises also
+ * where its weight is 0.  x finite, below 2^100 in magnitude.  out must not
+ * overlap an input.  Results are the same bits on every run.  Few rows per
+ * expert: each tile of rows reads its expert's weights again.
  * rows and x_rows up to 2^24, rows * N < 2^36, x below 2 GiB, one expert's codes
  * below 2 GiB, all experts' below 256 GiB.
  * Errors: MOK_ERR_UNSUPPORTED for MOK_DTYPE_F32; MOK_ERR_INVALID_ARG for a

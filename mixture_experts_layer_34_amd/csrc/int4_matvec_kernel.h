@@ -13,8 +13,13 @@
 //   sum_k x_k W[n, k] = s (sum_k x_k (16 + q) - (16 + z) sum_k x_k),
 // where both sums are fp32 MFMA accumulations (the second against a matrix of
 // ones, once for all n) and the scale is applied to the fp32 result: no weight
-// is rounded.  The offset 16 costs at most log2(32 / |q - z|) bits of the
-// fp32 sum, far below the rounding of the 16-bit result.
+// is rounded.  The two sums cancel in 16 + z, so the fp32 error goes with
+// s sum_k |x_k| (32 + q + z) 2^-24 and not with the weights: a code equal to its
+// zero point leaves some too.  For x of one magnitude that is log2(32 / |q - z|)
+// bits of 24, far below the rounding of the 16-bit result; an x far above the
+// others shows in fp16 (6e4 on weights of 0 among x of 1, K 4096: the mean error
+// 0.066 -> 0.10 to 0.15 scales, results of 380 scales; with 1000, and in bf16 with
+// either, unchanged).
 //
 // v_mfma_f32_16x16x32: A = the tile's rows of x (lane: row lane % 16, K
 // 8 (lane / 16) + i), B = weight rows (lane: n = lane % 16, same K), result:

@@ -151,3 +151,23 @@ def test_weights_moved_from_the_cpu():
     with pytest.raises(ValueError, match="devices"):
         X.expert_matvec_int4(x, there)
     assert torch.equal(X.expert_matvec_int4(x, there.to("cuda")), X.expert_matvec_int4(x, w))
+
+
+@pytest.mark.parametrize("rows", [1, 8, 32])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_an_outlier_on_weights_of_zero(rows, dt):
+    """An x of 6e4 among x of 1, on weights whose code is their zero point,
+    adds nothing to the result and leaves no more than the bound of the two
+    sums that cancel, 2^-24 s |x| (32 + q + z) a step."""
+    N, K, G, at = 96, 1024, 128, 777
+    w = _weights(_gen(21), 1, N, K, G, True, dt)
+    zero, byte = w.zeros[0, :, at // G], w.codes[0, :, at // 2]
+    byte.copy_((byte & 15) | (zero << 4))           # element 777 lies in the high nibble
+    x = _randn(_gen(22), (rows, K), dt)
+    x[:, at] = 6e4
+    ref, tol = _product_ref(x.double(), torch.zeros(rows, dtype=torch.long, device="cuda"), w, None, dt)
+    without = x.clone()
+    without[:, at] = 0
+    assert torch.equal(ref, _product_ref(without.double(), torch.zeros(rows, dtype=torch.long, device="cuda"), w, None,
+                                         dt)[0])
+    _close(X.expert_matvec_int4(x, w), ref, tol, "with the outlier")
