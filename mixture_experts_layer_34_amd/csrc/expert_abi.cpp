@@ -98,7 +98,8 @@ mok_status mok_expert_matvec_int4(const void* x, const int32_t* pair_of_row, con
                                   const mok_int4_config* cfg, void* out, void* stream) {
   if (!cfg || !w) return MOK_ERR_INVALID_ARG;
   const mok_int4_config& c = *cfg;
-  if (c.rows < 0 || c.rows > (1 << 24) || c.x_rows < 0 || c.x_rows > (1 << 24) || c.k < 1 || c.N < 1 || c.K < 1) return MOK_ERR_INVALID_ARG;
+  if (c.rows < 0 || c.rows > (1 << 24) || c.x_rows < 0 || c.x_rows > (1 << 24)) return MOK_ERR_INVALID_ARG;
+  if (c.k < 1 || c.N < 1 || c.K < 1) return MOK_ERR_INVALID_ARG;
   if (bad_experts(c.E, c.expert_begin, c.expert_end)) return MOK_ERR_INVALID_ARG;
   if (c.group != 32 && c.group != 64 && c.group != 128) return MOK_ERR_INVALID_ARG;
   if (c.K % c.group || c.K > (1 << 20)) return MOK_ERR_INVALID_ARG;

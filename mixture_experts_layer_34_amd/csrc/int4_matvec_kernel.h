@@ -147,8 +147,8 @@ __device__ __forceinline__ void spread_quarters(uint32_t v, uint32_t (&o)[4]) {
 // 57.5 -> 47.3 us, nothing spilled); the others either fit or spill for it (a
 // pair in sixteens loses 2 to 20 %).
 template <int DT, int NM, int NG, int RT, int GS, int KS, int NW, int SCH, bool WHOLE>
-__global__ __launch_bounds__(64 * KS * NW, RT == 32 && NM == 1 && KS == 1 ? 4 : 1) void int4_matvec_kernel(Int4Args a, const int32_t* __restrict__ offsets,
-                                                                   const int32_t* __restrict__ pair_of_row) {
+__global__ __launch_bounds__(64 * KS * NW, RT == 32 && NM == 1 && KS == 1 ? 4 : 1)
+void int4_matvec_kernel(Int4Args a, const int32_t* __restrict__ offsets, const int32_t* __restrict__ pair_of_row) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NB = NM * NG;
   constexpr int NSC = kChunk / GS;          // groups in a chunk
@@ -252,7 +252,8 @@ __global__ __launch_bounds__(64 * KS * NW, RT == 32 && NM == 1 && KS == 1 ? 4 : 
       const int k = chunk_of(i) * kChunk + 32 * g4;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
-        wv[buf][b] = load16(rw[b / NG], i < nloc && k < K ? (uint32_t)((16 * (b % NG) + n16) * (K / 2) + k / 2) : kNowhere);
+        wv[buf][b] = load16(rw[b / NG],
+                            i < nloc && k < K ? (uint32_t)((16 * (b % NG) + n16) * (K / 2) + k / 2) : kNowhere);
     };
     auto load_scales = [&](int i0) {
       const int c = chunk_of(i0 + g4);
@@ -286,7 +287,8 @@ __global__ __launch_bounds__(64 * KS * NW, RT == 32 && NM == 1 && KS == 1 ? 4 : 
             const bool in = in_c && gi < G;
             const uint32_t v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, in ? 2 * (row + gi) : kNowhere, 0, 0);
             sv[b][i / 2] |= v << (16 * (i % 2));
-            zv[b] |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(z, in ? row + gi : kNowhere, 0, 0) << (8 * i);
+            const uint8_t zi = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(z, in ? row + gi : kNowhere, 0, 0);
+            zv[b] |= (uint32_t)zi << (8 * i);
           }
         }
       }

@@ -90,9 +90,12 @@ template <int NM, int RT, int GS, class L> hipError_t launch_tiles(const Int4Arg
 template <int GS, class L> hipError_t launch_group(const Int4Args& a, const L& l) {
   if constexpr (GS < kChunk) {
     // a last chunk that is not whole: scales and zeros one by one, in sixteens
+    // (gate / up of 128 experts, 1536 x 2880 in groups of 64, 1 / 16 / 128 tokens
+    // 24.7 / 111 / 167 us; 1536 x 2944, whole, 16.1 / 92 / 158)
     if (a.K % kChunk) {
       const bool many = waves_of(a, 16, 1) >= kWanted;
-      if (a.pair) return many ? l.template run<2, 1, 16, GS, 1, 4, 4, false>(a) : l.template run<2, 1, 16, GS, 4, 2, 4, false>(a);
+      if (a.pair && many) return l.template run<2, 1, 16, GS, 1, 4, 4, false>(a);
+      if (a.pair) return l.template run<2, 1, 16, GS, 4, 2, 4, false>(a);
       return many ? l.template run<1, 1, 16, GS, 1, 4, 4, false>(a) : l.template run<1, 1, 16, GS, 4, 2, 4, false>(a);
     }
   }

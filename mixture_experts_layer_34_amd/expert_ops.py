@@ -265,7 +265,8 @@ def quantize_int4(w: torch.Tensor, group: int = 128, symmetric: bool = True) -> 
     _on("quantize_int4", w)
     w = _ready(w if w.dim() == 3 else w[None])
     E, N, K = w.shape
-    _need(group in (32, 64, 128) and K > 0 and K % group == 0, "quantize_int4", "K a multiple of a group of 32, 64 or 128")
+    _need(group in (32, 64, 128) and K > 0 and K % group == 0, "quantize_int4",
+          "K a multiple of a group of 32, 64 or 128")
     codes = torch.empty((E, N, K // 2), dtype=torch.uint8, device=w.device)
     scales = torch.empty((E, N, K // group), dtype=w.dtype, device=w.device)
     zeros = None if symmetric else torch.empty(scales.shape, dtype=torch.uint8, device=w.device)

@@ -84,8 +84,8 @@ def test_a_map_whose_array_was_changed_in_place_is_refused(change):
         return m
 
     x, y = torch.zeros(4, 8), torch.zeros(8, 8)
-    for call in (lambda m: X.permute_rows(x, m), lambda m: X.permute_rows_backward(y, m), lambda m: X.unpermute_rows(y, m),
-                 lambda m: X.unpermute_rows_backward(x, m)):
+    for call in (lambda m: X.permute_rows(x, m), lambda m: X.permute_rows_backward(y, m),
+                 lambda m: X.unpermute_rows(y, m), lambda m: X.unpermute_rows_backward(x, m)):
         with pytest.raises(ValueError, match="row_of_pair"):
             call(changed("row_of_pair"))
         with pytest.raises(ValueError, match="GPU"):    # the other arrays are not read

@@ -126,8 +126,8 @@ def test_lost_gradients_are_refused():
     grad = lambda t: t.detach().clone().requires_grad_()
     wg = X.Int4Weights(w.codes, grad(w.scales))
     buf = lambda: torch.zeros(T * k, d, device="cuda")
-    for call in (lambda: X.permute_rows(grad(x), m, out=buf()), lambda: X.permute_rows(x, m, gate=grad(gate), out=buf()),
-                 lambda: X.permute_rows(x, m, out=grad(buf())),
+    for call in (lambda: X.permute_rows(grad(x), m, out=buf()),
+                 lambda: X.permute_rows(x, m, gate=grad(gate), out=buf()), lambda: X.permute_rows(x, m, out=grad(buf())),
                  lambda: X.unpermute_rows(grad(y), m), lambda: X.unpermute_rows(y, m, gate=grad(gate)),
                  lambda: X.expert_matvec_int4(grad(xb), w, m, from_tokens=True),
                  lambda: X.expert_matvec_int4(xb, wg, m, from_tokens=True),

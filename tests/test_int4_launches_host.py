@@ -24,7 +24,8 @@ def test_every_configuration_has_a_case(group, pair):
     assert dense == {config(rows, 1, 1, False, N, K, g, p) for rows, N, K, g, _, p in DENSE if (g, p) == (group, pair)}
 
 
-@pytest.mark.parametrize("rows,E,E_loc", [(1024, 256, 32), (128, 128, 16), (4096, 128, 4), (512, 1024, 128), (96, 24, 8)])
+@pytest.mark.parametrize("rows,E,E_loc", [(1024, 256, 32), (128, 128, 16), (4096, 128, 4), (512, 1024, 128),
+                                            (96, 24, 8)])
 @pytest.mark.parametrize("pair", [False, True])
 def test_a_share_is_taken_for_its_own_rows(rows, E, E_loc, pair):
     """A map over part of the experts launches what a map over those experts
