@@ -246,6 +246,7 @@ class Int4Weights:
         _need(s.device == q.device and (z is None or z.device == q.device), fn, "tensors on different devices")
         _need(all(t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0) for t in (q, s, z)), fn,
               "contiguous, 16-byte aligned arrays expected")
+        _need(all(t is None or t.data_ptr() or not t.numel() for t in (q, s, z)), fn, "arrays without memory")
         v = (E, N, K, group, mok.int4_weights(q, s, z))
         self.__dict__["_seen"] = (now, v)
         return v

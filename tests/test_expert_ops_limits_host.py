@@ -111,3 +111,13 @@ def test_weights_are_read_and_moved_on_the_cpu(zeros):
         X.expert_matvec_int4(torch.zeros(4, 128).bfloat16(), X.Int4Weights(codes[:1], scales[:1]))
     with pytest.raises(ValueError, match="devices"):
         X.Int4Weights(codes, scales.to("meta"))
+
+
+@pytest.mark.parametrize("name", ["codes", "scales", "zeros"])
+def test_weights_whose_memory_was_given_up_are_refused(name):
+    """Zero points without memory are not weights without zero points."""
+    w = X.Int4Weights(torch.zeros(1, 4, 64, dtype=torch.uint8), torch.ones(1, 4, 4).bfloat16(),
+                      torch.zeros(1, 4, 4, dtype=torch.uint8))
+    getattr(w, name).untyped_storage().resize_(0)
+    with pytest.raises(ValueError, match="without memory"):
+        w.view("test")
