@@ -230,8 +230,8 @@ class Int4Weights:
         """(E, N, K, group, the C view): the arrays checked against each other,
         again only after one of them was given other storage or strides."""
         q, s, z = self.codes, self.scales, self.zeros
-        now = (q.data_ptr(), s.data_ptr(), 0 if z is None else z.data_ptr(), q.shape, s.shape,
-               q.is_contiguous() and s.is_contiguous() and (z is None or z.is_contiguous()))
+        now = (q.data_ptr(), s.data_ptr(), q.shape, s.shape, q.is_contiguous() and s.is_contiguous(),
+               None if z is None else (z.data_ptr(), z.shape, z.is_contiguous()))
         seen = self.__dict__.get("_seen")
         if seen is not None and seen[0] == now:
             return seen[1]

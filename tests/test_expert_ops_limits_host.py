@@ -121,3 +121,14 @@ def test_weights_whose_memory_was_given_up_are_refused(name):
     getattr(w, name).untyped_storage().resize_(0)
     with pytest.raises(ValueError, match="without memory"):
         w.view("test")
+
+
+def test_zero_points_resized_in_place_are_refused():
+    """The same address with fewer zero points than scales."""
+    w = X.Int4Weights(torch.zeros(1, 4, 64, dtype=torch.uint8), torch.ones(1, 4, 4).bfloat16(),
+                      torch.zeros(1, 4, 4, dtype=torch.uint8))
+    address = w.zeros.data_ptr()
+    w.zeros.resize_(1, 2, 4)
+    assert w.zeros.data_ptr() == address
+    with pytest.raises(ValueError, match="zeros like the scales"):
+        w.view("test")
