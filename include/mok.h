@@ -644,7 +644,9 @@ typedef struct mok_int4_config {
  * scale |x_i| (32 + q_i + z_i), which an x far above a row's others raises also
  * where its weight is 0.  x finite, below 2^100 in magnitude.  out must not
  * overlap an input.  Results are the same bits on every run.  Few rows per
- * expert: each tile of rows reads its expert's weights again.
+ * expert: each tile of rows reads its expert's weights again.  The launch is
+ * chosen for rows * (local experts) / E rows; where all pairs of a map are
+ * local, a map over those experts alone (E their number) is the faster one.
  * rows and x_rows up to 2^24, rows * N < 2^36, x below 2 GiB, one expert's codes
  * below 2 GiB, all experts' below 256 GiB.
  * Errors: MOK_ERR_UNSUPPORTED for MOK_DTYPE_F32; MOK_ERR_INVALID_ARG for a

@@ -86,7 +86,10 @@ template <int NM, int RT, int GS, class L> hipError_t launch_tiles(const Int4Arg
 // once for both (128 experts' down product of 128 tokens 97 us, 108 by eight
 // waves of 16 columns).  With groups of 32 their scales cost a workgroup's place
 // on the compute unit, and eight waves of 16 columns are faster (32 experts,
-// 4096 x 1536, four rows each 38.3 -> 33.9 us, 128 experts 121 -> 118).
+// 4096 x 1536, four rows each 38.3 -> 33.9 us, 128 experts 121 -> 118).  A share
+// takes fours only where all rows of the map on it would be no more than eight an
+// expert: one that holds only its own pairs has them all (512 on 32 of 256
+// experts, gate / up 135 us in fours, 53 in sixteens).
 template <int GS, class L> hipError_t launch_group(const Int4Args& a, const L& l) {
   if constexpr (GS < kChunk) {
     // a last chunk that is not whole: scales and zeros one by one, in sixteens
@@ -100,7 +103,8 @@ template <int GS, class L> hipError_t launch_group(const Int4Args& a, const L& l
     }
   }
   const int64_t rows = local_rows(a), experts = a.offsets ? a.E_loc : 1;
-  const bool few = a.offsets ? rows <= 2 * experts : rows <= 4 || (rows <= 8 && waves_of(a, 4, 1) * 4 < kWanted);
+  const bool few = a.offsets ? rows <= 2 * experts && a.rows <= 8 * experts
+                             : rows <= 4 || (rows <= 8 && waves_of(a, 4, 1) * 4 < kWanted);
   if (few) return a.pair ? launch_tiles<2, 4, GS>(a, l) : launch_tiles<1, 4, GS>(a, l);
   if (rows > 16 * experts && waves_of(a, 32, 1) * 16 >= 5 * kWanted)
     return a.pair ? launch_tiles<2, 32, GS>(a, l) : launch_tiles<1, 32, GS>(a, l);

@@ -282,7 +282,9 @@ def expert_matvec_int4(x: torch.Tensor, w: Int4Weights, pmap: PairMap | None = N
     With a pair map x holds the expert-sorted rows [T * k, K], or with
     from_tokens the token rows [T, K], and the result the sorted rows
     [T * k, N] (rows without a pair are left as they are).  Without one, w is
-    one matrix and every row of x is its own."""
+    one matrix and every row of x is its own.  A map over part of its experts is
+    expected to have that part of its pairs local; where all of them are, sort
+    over those experts alone (E their number)."""
     fn = "expert_matvec_int4"
     E_w, N, K, group, wc = w.view(fn)
     _need(x.dim() == 2 and x.dtype == w.scales.dtype and x.shape[1] == K, fn,

@@ -61,17 +61,19 @@ def test_dense(rows, N, K, group, zeros, pair, dt):
     (128, 8, 256, 224, 256, 1040, 384, 32, False),
     (16, 8, 128, 0, 16, 272, 1152, 64, True),       # one row: in fours
     (256, 4, 64, 60, 64, 2000, 640, 64, False),     # sixteen rows
-    (300, 8, 16, 3, 4, 4100, 384, 128, False),      # 150 rows: thirty-twos; skewed, workgroups loop
+    (300, 8, 16, 3, 4, 4100, 384, 128, False),      # 150 rows: thirty-twos; local, workgroups loop
     (1, 8, 128, 0, 16, 144, 640, 32, True),         # one row for all of them
 ])
-@pytest.mark.parametrize("skewed", [False, True])
-def test_expert_parallel_share(T, k, E, eb, ee, N, K, group, pair, skewed):
-    """Weights of the local experts only, with as many rows as fall to them, or
-    every pair on one of them."""
-    note(f"{config(T * k, E, ee - eb, True, N, K, group, pair)} skewed={skewed}")
+@pytest.mark.parametrize("pairs", ["anywhere", "local", "one expert"])
+def test_expert_parallel_share(T, k, E, eb, ee, N, K, group, pair, pairs):
+    """Weights of the local experts only, with as many rows as fall to them,
+    every pair on them, or every pair on one of them."""
+    note(f"{config(T * k, E, ee - eb, True, N, K, group, pair)} pairs={pairs}")
     g = _gen(T + N)
     idx = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)
-    if skewed:
+    if pairs == "local":
+        idx = eb + idx % (ee - eb)
+    elif pairs == "one expert":
         idx[:] = ee - 1
     idx = idx.cuda()
     m = X.sort_pairs(idx, E, eb, ee)

@@ -33,3 +33,10 @@ def test_a_share_is_taken_for_its_own_rows(rows, E, E_loc, pair):
     for N, group in itertools.product((64, 1500, 4096, 20000), (32, 64, 128)):
         assert config(rows, E, E_loc, True, N, 1536, group, pair) == \
             config(rows * E_loc // E, E_loc, E_loc, True, N, 1536, group, pair)
+
+
+@pytest.mark.parametrize("pair", [False, True])
+def test_a_share_that_may_hold_every_row_is_not_taken_in_fours(pair):
+    """A map of pairs that are all local, over part of the experts."""
+    assert config(512, 256, 32, True, 1536, 4096, 128, pair)[2] == 16
+    assert config(256, 256, 32, True, 1536, 4096, 128, pair)[2] == 4
