@@ -673,6 +673,121 @@ mok_status mok_expert_matvec_int4(const void* x, const int32_t* pair_of_row, con
 mok_status mok_quantize_int4(const void* src, int64_t rows, int64_t K, int32_t group, mok_dtype dtype, uint8_t* codes,
                              void* scales, uint8_t* zeros, void* stream);
 
+/*
+ * The whole layer for a few tokens (a decode step; an MoE decode kernel is
+ * named as earlier work in [fluid], section "Quand la communication devient le
+ * vrai problème") in two launches, four with adapters, for fp32, bf16 and fp16
+ * weights of any width:
+ *   out[t] = sum_j gate[t,j] W2_e (silu(W1_e x[t]) * (W3_e x[t])),  e = topk_idx[t,j]
+ * over the local experts, with mok_moe_forward's routing (the same order of
+ * ties, gates and flags, bit for bit).
+ *   x               dtype [T, d]
+ *   router_logits   float [T, E]
+ *   W1, W3          dtype [E_loc, F, d]     W2  dtype [E_loc, d, F]
+ *   out             dtype [T, d]; 0 for a token without a local expert
+ *   topk_idx        int32 [T, k]
+ *   topk_gate       float [T, k]
+ *   workspace       mok_few_token_workspace_query bytes of scratch, one for each
+ *                   call in flight
+ * Sums are fp32 in a fixed order (the same bits on every run); the gate is
+ * applied to the first product's result in fp32, which is rounded once to dtype,
+ * and out once.
+ *
+ * Adapters (`adapter` and `lora` both NULL: none): token t with l = adapter[t] in
+ * [0, L) has W + scale[l] B_{l,e} A_{l,e} in place of each of its experts'
+ * matrices that lora[0] (W1), lora[1] (W3), lora[2] (W2) names; any other value
+ * of adapter[t] is no adapter.
+ *   adapter         int32 [T]
+ *   lora[m]         groups = L * E_loc, the adapter major: A dtype [L, E_loc, r,
+ *                   K], B dtype [L, E_loc, N, r] for that matrix [N, K], scale
+ *                   float [L], its own r each; A and B both NULL: none
+ * 0 <= T <= 16, 1 <= k <= min(E, 64), E <= 1024, 1 <= d, F <= 65536, L >= 1 with
+ * adapters.  Finite values: a NaN logit ranks below every number, and an
+ * infinity or NaN in W2 of an expert that any token chose reaches every token.
+ * T = 0 does nothing.
+ * Errors: MOK_ERR_INVALID_ARG for a null or misaligned pointer or a shape or flag
+ * outside these bounds; MOK_ERR_HIP for a failed launch.
+ */
+typedef struct mok_few_token_config {
+  int32_t T;                 /* tokens                                          */
+  int32_t d;                 /* hidden size                                     */
+  int32_t E;                 /* experts routed over                             */
+  int32_t k;                 /* experts a token                                 */
+  int32_t ffn;               /* expert width F                                  */
+  int32_t expert_begin;      /* first local expert                              */
+  int32_t expert_end;        /* one past the last local expert                  */
+  int32_t dtype;             /* mok_dtype of x, the weights and out             */
+  uint32_t flags;            /* MOK_FLAG_SIGMOID_GATES, MOK_FLAG_RENORM_GATES   */
+  int32_t L;                 /* adapters (read with `adapter` only)             */
+} mok_few_token_config;
+
+/* Low-rank adapters of one projection [N, K]: B_g A_g of each group g. */
+typedef struct mok_lora_weights {
+  const void* A;             /* dtype [groups, r, K]                            */
+  const void* B;             /* dtype [groups, N, r]                            */
+  const float* scale;        /* one each, NULL: 1                               */
+  int32_t r;                 /* rank, 1..128                                    */
+} mok_lora_weights;
+
+mok_status mok_few_token_workspace_query(const mok_few_token_config* cfg, const mok_lora_weights* lora,
+                                         size_t* workspace_bytes);
+mok_status mok_few_token_layer(const void* x, const float* router_logits, const void* W1, const void* W3,
+                               const void* W2, const int32_t* adapter, const mok_lora_weights* lora,
+                               const mok_few_token_config* cfg, void* out, int32_t* topk_idx, float* topk_gate,
+                               void* workspace, void* stream);
+
+/*
+ * Low-rank adapters beside a projection, and their gradients:
+ *   out_q = y_q + scale[g] B_g u_q,  u_q = A_g x_q
+ *   du_q = scale[g] B_g^T dout_q,    dx_q = base_q + A_g^T du_q,
+ *   dA_g = sum_q du_q x_q^T,         dB_g = scale[g] sum_q dout_q u_q^T
+ * for the rows q of group g, [offsets[g], offsets[g + 1]) of mok_sort_pairs.
+ *  - Many requests' adapters on one projection: the groups are the adapters,
+ *    sorted with k = 1 (an index outside the range: a row of no adapter), and x, y,
+ *    out in token order: row q is token pair_of_row[q] (outside [0, rows): no
+ *    row).  A token of no adapter (row_of_pair outside [0, rows)) gets out = y.
+ *  - One adapter on each expert's projection: pair_of_row and row_of_pair NULL, and
+ *    x, y, out in the experts' sorted rows; rows of no expert are left as they were.
+ *   x, dx, base     dtype [rows, K]         y, out, dout  dtype [rows, N]
+ *   y, base         NULL: 0; may be the same array as out (dx)
+ *   u               float [rows, r], sorted rows, not scaled; for the backward
+ *                   pass.  From the forward call NULL: not kept.  Rows of no
+ *                   group are left as they were.
+ *   w               groups = E_loc, group expert_begin first: A dtype [E_loc, r, K],
+ *                   B dtype [E_loc, N, r], scale float [E_loc]
+ *   offsets         int32 [E + 1]
+ *   dA, dB          float [E_loc, r, K], [E_loc, N, r]; 0 for a group without rows
+ *   workspace       mok_lora_workspace_query bytes of scratch (may be 0 bytes),
+ *                   one for each call in flight
+ * Sums are fp32 in a fixed order: the same bits on every run.  out and dx are
+ * rounded once; u and du enter their products with 16 bits of mantissa or more,
+ * the sums of dA and dB with all of theirs.
+ * 0 <= rows < 2^30, 1 <= r <= 128, 1 <= K, N <= 2^20, 1 <= E <= 1024.
+ * Errors: MOK_ERR_INVALID_ARG for a null or misaligned pointer, one of
+ * pair_of_row and row_of_pair without the other, or a shape outside these bounds;
+ * MOK_ERR_HIP for a failed launch.
+ */
+typedef struct mok_lora_config {
+  int32_t rows;              /* rows of x, y and out                            */
+  int32_t E;                 /* groups of the offsets                           */
+  int32_t expert_begin;      /* first group of w                                */
+  int32_t expert_end;        /* one past the last group of w                    */
+  int32_t K;                 /* input width                                     */
+  int32_t N;                 /* output width                                    */
+  int32_t dtype;             /* mok_dtype                                       */
+} mok_lora_config;
+
+/* Scratch of the forward call (with u given or not) and of the backward call. */
+mok_status mok_lora_workspace_query(const mok_lora_config* cfg, int32_t r, size_t* forward_bytes,
+                                    size_t* backward_bytes);
+mok_status mok_lora_rows(const void* x, const void* y, const int32_t* pair_of_row, const int32_t* row_of_pair,
+                         const int32_t* offsets, const mok_lora_weights* w, const mok_lora_config* cfg, void* out,
+                         float* u, void* workspace, void* stream);
+mok_status mok_lora_rows_backward(const void* dout, const void* x, const float* u, const void* base,
+                                  const int32_t* pair_of_row, const int32_t* row_of_pair, const int32_t* offsets,
+                                  const mok_lora_weights* w, const mok_lora_config* cfg, void* dx, float* dA,
+                                  float* dB, void* workspace, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* mok_status_string(mok_status s);
 

@@ -19,6 +19,7 @@ DIAG = os.path.join(PKG, "libmok_diag.so")
 BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["route_sort.hip", "permute_combine.hip", "gemm_bf16.hip", "gemm_stream.hip", "quantize_rows.hip", "gemm_f32.hip", "gemm_mxfp8.hip", "router_gemm.hip",
            "sort_pairs.hip", "permute_rows.hip", "int4_matvec_bf16.hip", "int4_matvec_f16.hip", "quantize_int4.hip",
+           "few_tokens.hip", "lora_rows.hip",
            "mok_abi.cpp", "expert_abi.cpp"]
 DIAG_SOURCES = ["diag_mfma.hip", "diag_expert.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -3,7 +3,9 @@
 #include <hip/hip_runtime.h>
 
 #include "../../include/mok.h"
+#include "few_tokens.h"
 #include "int4_matvec.h"
+#include "lora_rows.h"
 #include "pair_ops.h"
 
 using namespace mok;
@@ -27,6 +29,68 @@ mok_status pair_rows(const void* a, const void* in, void* out, float* dot, const
   if (dtype != MOK_DTYPE_F32 && dtype != MOK_DTYPE_BF16 && dtype != MOK_DTYPE_F16) return MOK_ERR_INVALID_ARG;
   if (!good(rop, T) || !aligned16(gate) || !aligned16(dot)) return MOK_ERR_INVALID_ARG;
   *p = PairRows{a, in, out, dot, gate, rop, T, k, d, (int)dtype, rows};
+  return MOK_OK;
+}
+
+// Parts of a workspace, one after the other on 256 bytes.
+struct Parts {
+  size_t total = 0;
+  size_t take(int64_t n) {
+    const size_t at = total;
+    total += ((size_t)n + 255) & ~(size_t)255;
+    return at;
+  }
+};
+
+bool bad_dtype(int32_t t) { return t != MOK_DTYPE_F32 && t != MOK_DTYPE_BF16 && t != MOK_DTYPE_F16; }
+int64_t elem_bytes(int32_t t) { return t == MOK_DTYPE_F32 ? 4 : 2; }
+bool bad_rank(int32_t r) { return r < 1 || r > kLoraMaxRank; }
+
+struct FewLayout {
+  size_t h, u[3], total;
+};
+mok_status few_layout(const mok_few_token_config* cfg, const mok_lora_weights* lora, FewLayout* o) {
+  if (!cfg) return MOK_ERR_INVALID_ARG;
+  const mok_few_token_config& c = *cfg;
+  if (c.T < 0 || c.T > kFewTokens || c.d < 1 || c.d > 65536 || c.ffn < 1 || c.ffn > 65536) return MOK_ERR_INVALID_ARG;
+  if (bad_experts(c.E, c.expert_begin, c.expert_end) || c.k < 1 || c.k > c.E || c.k > kFewSlots)
+    return MOK_ERR_INVALID_ARG;
+  if (bad_dtype(c.dtype) || (c.flags & ~(MOK_FLAG_SIGMOID_GATES | MOK_FLAG_RENORM_GATES))) return MOK_ERR_INVALID_ARG;
+  const int64_t P = (int64_t)c.T * c.k;
+  Parts p;
+  o->h = p.take(P * few_h_width(c.ffn) * elem_bytes(c.dtype));
+  for (int m = 0; m < 3; ++m) {
+    o->u[m] = p.total;
+    if (!lora) continue;
+    if ((lora[m].A != nullptr) != (lora[m].B != nullptr)) return MOK_ERR_INVALID_ARG;
+    if (!lora[m].A) continue;
+    if (bad_rank(lora[m].r) || c.L < 1) return MOK_ERR_INVALID_ARG;
+    o->u[m] = p.take(P * few_u_width(lora[m].r) * 4);
+  }
+  o->total = p.total;
+  return MOK_OK;
+}
+
+struct LoraLayout {
+  size_t part, At, Bt, du, total;
+  int splits;
+};
+mok_status lora_layout(const mok_lora_config* cfg, int32_t r, bool backward, LoraLayout* o) {
+  if (!cfg) return MOK_ERR_INVALID_ARG;
+  const mok_lora_config& c = *cfg;
+  if (c.rows < 0 || c.rows >= (1 << 30) || bad_experts(c.E, c.expert_begin, c.expert_end)) return MOK_ERR_INVALID_ARG;
+  if (c.K < 1 || c.K > (1 << 20) || c.N < 1 || c.N > (1 << 20) || bad_rank(r) || bad_dtype(c.dtype))
+    return MOK_ERR_INVALID_ARG;
+  const int G = c.expert_end - c.expert_begin;
+  Parts p;
+  o->splits = lora_splits(c.rows, G, backward ? c.N : c.K, c.dtype);
+  o->part = p.take((int64_t)o->splits * c.rows * r * 4);
+  if (backward) {
+    o->At = p.take((int64_t)G * r * c.K * elem_bytes(c.dtype));
+    o->Bt = p.take((int64_t)G * r * c.N * elem_bytes(c.dtype));
+    o->du = o->splits > 1 ? p.take((int64_t)c.rows * r * 4) : o->part;
+  }
+  o->total = p.total;
   return MOK_OK;
 }
 
@@ -153,6 +217,132 @@ mok_status mok_quantize_int4(const void* src, int64_t rows, int64_t K, int32_t g
   if (rows > (int64_t(1) << 40) / K) return MOK_ERR_INVALID_ARG;
   if (!good(src, rows) || !good(codes, rows) || !good(scales, rows) || !aligned16(zeros)) return MOK_ERR_INVALID_ARG;
   return result(launch_quantize_int4(src, rows, K, group, dtype, codes, scales, zeros, (hipStream_t)stream));
+}
+
+mok_status mok_few_token_workspace_query(const mok_few_token_config* cfg, const mok_lora_weights* lora,
+                                         size_t* workspace_bytes) {
+  FewLayout l;
+  const mok_status st = few_layout(cfg, lora, &l);
+  if (st != MOK_OK) return st;
+  if (!workspace_bytes) return MOK_ERR_INVALID_ARG;
+  *workspace_bytes = l.total;
+  return MOK_OK;
+}
+
+mok_status mok_few_token_layer(const void* x, const float* router_logits, const void* W1, const void* W3,
+                               const void* W2, const int32_t* adapter, const mok_lora_weights* lora,
+                               const mok_few_token_config* cfg, void* out, int32_t* topk_idx, float* topk_gate,
+                               void* workspace, void* stream) {
+  FewLayout l;
+  const mok_status st = few_layout(cfg, lora, &l);
+  if (st != MOK_OK) return st;
+  const mok_few_token_config& c = *cfg;
+  if (!good(x, c.T) || !good(router_logits, c.T) || !good(W1, 1) || !good(W3, 1) || !good(W2, 1) || !good(out, c.T) ||
+      !good(topk_idx, c.T) || !good(topk_gate, c.T) || !good(workspace, c.T))
+    return MOK_ERR_INVALID_ARG;
+  if ((lora != nullptr) != (adapter != nullptr) && c.T > 0) return MOK_ERR_INVALID_ARG;
+  if (!aligned16(adapter)) return MOK_ERR_INVALID_ARG;
+  if (c.T == 0) return MOK_OK;
+  FewTokens a{};
+  a.x = x;
+  a.logits = router_logits;
+  a.w[0] = W1;
+  a.w[1] = W3;
+  a.w[2] = W2;
+  a.out = out;
+  a.idx = topk_idx;
+  a.gate = topk_gate;
+  a.h = (char*)workspace + l.h;
+  bool any = false;
+  for (int m = 0; m < 3 && lora; ++m) {
+    if (!aligned16(lora[m].A) || !aligned16(lora[m].B) || !aligned16(lora[m].scale)) return MOK_ERR_INVALID_ARG;
+    a.lora[m] = FewLora{lora[m].A, lora[m].B, lora[m].scale, lora[m].r};
+    a.u[m] = (float*)((char*)workspace + l.u[m]);
+    any |= lora[m].A != nullptr;
+  }
+  a.adapter = any ? adapter : nullptr;
+  a.T = c.T;
+  a.d = c.d;
+  a.F = c.ffn;
+  a.Fp = few_h_width(c.ffn);
+  a.E = c.E;
+  a.eb = c.expert_begin;
+  a.E_loc = c.expert_end - c.expert_begin;
+  a.k = c.k;
+  a.L = c.L;
+  a.dtype = c.dtype;
+  a.gating = (c.flags & MOK_FLAG_SIGMOID_GATES ? kFewSigmoid : 0) | (c.flags & MOK_FLAG_RENORM_GATES ? kFewRenorm : 0);
+  return result(launch_few_tokens(a, (hipStream_t)stream));
+}
+
+mok_status mok_lora_workspace_query(const mok_lora_config* cfg, int32_t r, size_t* forward_bytes,
+                                    size_t* backward_bytes) {
+  LoraLayout f, b;
+  mok_status st = lora_layout(cfg, r, false, &f);
+  if (st == MOK_OK) st = lora_layout(cfg, r, true, &b);
+  if (st != MOK_OK) return st;
+  if (!forward_bytes || !backward_bytes) return MOK_ERR_INVALID_ARG;
+  *forward_bytes = f.total;
+  *backward_bytes = b.total;
+  return MOK_OK;
+}
+
+mok_status mok_lora_rows(const void* x, const void* y, const int32_t* pair_of_row, const int32_t* row_of_pair,
+                         const int32_t* offsets, const mok_lora_weights* w, const mok_lora_config* cfg, void* out,
+                         float* u, void* workspace, void* stream) {
+  if (!w) return MOK_ERR_INVALID_ARG;
+  LoraLayout l;
+  const mok_status st = lora_layout(cfg, w->r, false, &l);
+  if (st != MOK_OK) return st;
+  const mok_lora_config& c = *cfg;
+  if (!good(x, c.rows) || !aligned16(y) || !good(out, c.rows) || !good(w->A, 1) || !good(w->B, 1) ||
+      !aligned16(w->scale) || !good(offsets, 1) || !aligned16(u) || !good(workspace, c.rows))
+    return MOK_ERR_INVALID_ARG;
+  if (!aligned16(pair_of_row) || !aligned16(row_of_pair) || (pair_of_row != nullptr) != (row_of_pair != nullptr))
+    return MOK_ERR_INVALID_ARG;
+  if (c.rows == 0) return MOK_OK;
+  const LoraMap map{offsets + c.expert_begin, pair_of_row, row_of_pair, c.rows, c.expert_end - c.expert_begin};
+  // one share of K: its sum is u itself
+  float* part = l.splits == 1 && u ? u : (float*)((char*)workspace + l.part);
+  hipError_t e = launch_lora_rank(LoraRank{map, x, w->A, part, c.K, w->r, c.dtype, l.splits}, (hipStream_t)stream);
+  if (e == hipSuccess)
+    e = launch_lora_add(LoraAdd{map, part, w->B, w->scale, y, out, l.splits == 1 ? nullptr : u, c.N, w->r, c.dtype,
+                                l.splits}, (hipStream_t)stream);
+  return result(e);
+}
+
+mok_status mok_lora_rows_backward(const void* dout, const void* x, const float* u, const void* base,
+                                  const int32_t* pair_of_row, const int32_t* row_of_pair, const int32_t* offsets,
+                                  const mok_lora_weights* w, const mok_lora_config* cfg, void* dx, float* dA,
+                                  float* dB, void* workspace, void* stream) {
+  if (!w) return MOK_ERR_INVALID_ARG;
+  LoraLayout l;
+  const mok_status st = lora_layout(cfg, w->r, true, &l);
+  if (st != MOK_OK) return st;
+  const mok_lora_config& c = *cfg;
+  if (!good(dout, c.rows) || !good(x, c.rows) || !good(u, c.rows) || !aligned16(base) || !good(dx, c.rows) ||
+      !good(dA, 1) || !good(dB, 1) || !good(w->A, 1) || !good(w->B, 1) || !aligned16(w->scale) || !good(offsets, 1) ||
+      !good(workspace, 1))
+    return MOK_ERR_INVALID_ARG;
+  if (!aligned16(pair_of_row) || !aligned16(row_of_pair) ||
+      ((pair_of_row != nullptr) != (row_of_pair != nullptr) && c.rows > 0))
+    return MOK_ERR_INVALID_ARG;
+  const LoraMap map{offsets + c.expert_begin, pair_of_row, row_of_pair, c.rows, c.expert_end - c.expert_begin};
+  char* ws = (char*)workspace;
+  float *part = (float*)(ws + l.part), *du = (float*)(ws + l.du);
+  hipStream_t s = (hipStream_t)stream;
+  hipError_t e = hipSuccess;
+  if (c.rows > 0) {
+    e = launch_lora_transpose(w->A, w->B, map.G, w->r, c.K, c.N, c.dtype, ws + l.At, ws + l.Bt, s);
+    if (e == hipSuccess)
+      e = launch_lora_rank(LoraRank{map, dout, ws + l.Bt, part, c.N, w->r, c.dtype, l.splits}, s);
+    if (e == hipSuccess)
+      e = launch_lora_add(LoraAdd{map, part, ws + l.At, w->scale, base, dx, l.splits == 1 ? nullptr : du, c.K, w->r,
+                                  c.dtype, l.splits}, s);
+  }
+  if (e == hipSuccess)
+    e = launch_lora_grad(LoraGrad{map, {x, dout}, {du, u}, {dA, dB}, {c.K, c.N}, w->scale, w->r, c.dtype}, s);
+  return result(e);
 }
 
 }  // extern "C"

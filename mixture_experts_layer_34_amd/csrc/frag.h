@@ -1,0 +1,104 @@
+// Operand fragments of the 16x16 matrix instructions for rows of fp32, bf16 or
+// fp16: 16 bytes of one row a lane, of any width and alignment.
+//
+// With lane = 16 g + i, the lane holds KE consecutive elements (16 bytes) of
+// operand row i from element g KE of the K step on.  16-bit types: KE = 8, one
+// v_mfma_f32_16x16x32 a step.  fp32: KE = 4, four v_mfma_f32_16x16x4, the j-th
+// taking element j of every lane: the same order of K in both operands, so
+// every product is summed once.  The result holds, in lane 16 g + i, rows
+// 4 g + 0..3 (of the first operand) of column i (row i of the second).
+#pragma once
+#include "elem.h"
+
+namespace mok {
+
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+
+// A wave's number in its workgroup, in a scalar register: what depends on it
+// branches as a whole wave.  (A matrix instruction ignores the execution mask,
+// so none may stand under a condition that the compiler takes for one of lanes.)
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+template <int DT> constexpr int kFragElems = 16 / Elem<DT>::kBytes;  // KE
+template <int DT> constexpr int kFragStep = 4 * kFragElems<DT>;      // elements of a K step
+
+template <int DT> __device__ __forceinline__ f32x4_t mma(u32x4_t a, u32x4_t b, f32x4_t c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if constexpr (DT == 1) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                   0, 0, 0);
+  } else if constexpr (DT == 2) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
+                                                  0, 0);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[j]), __uint_as_float(b[j]), c, 0, 0, 0);
+    return c;
+  }
+#else
+  return c;
+#endif
+}
+
+// 16 bytes at p, which is aligned to an element only.
+typedef uint32_t u32x4_on2_t __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_on4_t __attribute__((ext_vector_type(4), aligned(4)));
+template <int DT> __device__ __forceinline__ u32x4_t load16(const char* p) {
+  if constexpr (Elem<DT>::kBytes == 4) return *reinterpret_cast<const u32x4_on4_t*>(p);
+  else return *reinterpret_cast<const u32x4_on2_t*>(p);
+}
+template <int DT> __device__ __forceinline__ void store16(char* p, u32x4_t v) {
+  if constexpr (Elem<DT>::kBytes == 4) *reinterpret_cast<u32x4_on4_t*>(p) = v;
+  else *reinterpret_cast<u32x4_on2_t*>(p) = v;
+}
+
+// The first n (0..KE) elements at p, zeros behind them.
+template <int DT> __device__ __forceinline__ u32x4_t load_part(const char* p, int n) {
+  constexpr int KE = kFragElems<DT>;
+  if (n >= KE) return load16<DT>(p);
+  u32x4_t v = {0, 0, 0, 0};
+  if constexpr (Elem<DT>::kBytes == 4) {
+#pragma unroll
+    for (int j = 0; j < KE; ++j)
+      if (j < n) v[j] = reinterpret_cast<const uint32_t*>(p)[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < KE; ++j)
+      if (j < n) v[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[j] << (16 * (j & 1));
+  }
+  return v;
+}
+template <int DT> __device__ __forceinline__ void store_part(char* p, u32x4_t v, int n) {
+  constexpr int KE = kFragElems<DT>;
+  if (n >= KE) {
+    store16<DT>(p, v);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < KE; ++j)
+    if (j < n) {
+      if constexpr (Elem<DT>::kBytes == 4) reinterpret_cast<uint32_t*>(p)[j] = v[j];
+      else reinterpret_cast<uint16_t*>(p)[j] = (uint16_t)(v[j / 2] >> (16 * (j & 1)));
+    }
+}
+
+// KE elements as fp32 and back (rounded to nearest even).
+template <int DT> __device__ __forceinline__ void widen(u32x4_t v, float* f) {
+  Vec<DT, kFragElems<DT>> e;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) e.w[j] = v[j];
+  e.widen(f);
+}
+template <int DT> __device__ __forceinline__ u32x4_t narrow(const float* f) {
+  const auto e = Vec<DT, kFragElems<DT>>::narrow(f);
+  return u32x4_t{e.w[0], e.w[1], e.w[2], e.w[3]};
+}
+
+// One element.
+template <int DT> __device__ __forceinline__ float elem_at(const void* p, int64_t i) {
+  if constexpr (DT == 0) return reinterpret_cast<const float*>(p)[i];
+  else return Elem<DT>::lo(reinterpret_cast<const uint16_t*>(p)[i]);
+}
+
+}  // namespace mok

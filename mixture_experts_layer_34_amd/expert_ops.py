@@ -1,15 +1,16 @@
 """The layer's steps as separate operators, for a routing or experts of the
 caller's own: pairs sorted by expert, token rows to the experts' rows and back
-with their gradients, and expert products with 4-bit integer weights.
+with their gradients, expert products with 4-bit integer weights, low-rank
+adapters beside a projection with their gradients, and the whole layer for a
+few tokens, with adapters or without.
 
 Torch plumbing around the C ABI (include/mok.h): tensors are checked, outputs
 allocated unless given, and the kernels enqueued on the tensors' device, on
 its current stream.  Inputs that are not contiguous (or not 16-byte aligned)
 are copied; an output given by the caller has to be both, and apart from every
 input (rows, gates, maps and weights).  Nothing is recorded for autograd: the
-gradients are the _backward functions', and permute_rows, unpermute_rows and the
-4-bit products refuse rows, gates and scales that require one while gradients
-are recorded."""
+gradients are the _backward functions', and the forward calls refuse rows, gates,
+scales, weights and adapters that require one while gradients are recorded."""
 from __future__ import annotations
 
 from dataclasses import dataclass
@@ -326,3 +327,180 @@ def int4_experts(x: torch.Tensor, pmap: PairMap, gate: torch.Tensor, w1: Int4Wei
     h = expert_matvec_int4(x, w1, pmap, w_up=w3, from_tokens=True)
     y = expert_matvec_int4(h, w2, pmap)
     return unpermute_rows(y, pmap, gate=gate)
+
+
+# ------------------------------------------------------------------ low-rank adapters
+@dataclass(frozen=True, eq=False)
+class LoraWeights:
+    """Low-rank adapters scale B A of a projection [N, K]: A [G, r, K] and B
+    [G, N, r] of one floating type, 1 <= r <= 128, scale fp32 [G] (None: 1), for
+    lora_rows; or A [L, E, r, K], B [L, E, N, r] and scale [L], adapter l of
+    expert e, for few_token_layer.  They may be held on the CPU and moved by
+    `to`; the operators take them on x's GPU."""
+    A: torch.Tensor
+    B: torch.Tensor
+    scale: torch.Tensor | None = None
+
+    def __post_init__(self):
+        for name in ("A", "B", "scale"):
+            object.__setattr__(self, name, _ready(getattr(self, name)))
+        self.view("LoraWeights")
+
+    def view(self, fn: str):
+        """(groups, N, K, the C view), the arrays checked against each other."""
+        a, b, s = self.A, self.B, self.scale
+        n = a.dim()
+        _need(n in (3, 4) and b.dim() == n and a.shape[:-2] == b.shape[:-2] and a.shape[-2] == b.shape[-1], fn,
+              "A [G, r, K] and B [G, N, r], or A [L, E, r, K] and B [L, E, N, r] expected")
+        r = a.shape[-2]
+        _need(a.dtype in _DTYPES and b.dtype == a.dtype, fn, "A and B of one type, fp32, bf16 or fp16, expected")
+        _need(1 <= r <= 128, fn, "a rank of 1 to 128 expected")
+        _need(s is None or (s.dtype == torch.float32 and s.shape == a.shape[:1]), fn,
+              "fp32 scale, one for each adapter, expected")
+        _need(b.device == a.device and (s is None or s.device == a.device), fn, "tensors on different devices")
+        _need(all(t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0) for t in (a, b, s)), fn,
+              "contiguous, 16-byte aligned arrays expected")
+        _need(all(t is None or t.data_ptr() or not t.numel() for t in (a, b, s)), fn, "arrays without memory")
+        return a.shape[:-2], b.shape[-2], a.shape[-1], mok.lora_weights(a, b, s, r)
+
+    def to(self, device) -> LoraWeights:
+        return LoraWeights(self.A.to(device), self.B.to(device), None if self.scale is None else self.scale.to(device))
+
+
+def _lora_args(fn: str, x, dout, amap: PairMap, w: LoraWeights, sorted_rows: bool):
+    """Checks rows [rows, K] and [rows, N] (either may be None) against a map
+    and its adapters; returns (rows, N, K, r, the C views of weights and config,
+    the map's arrays)."""
+    groups, N, K, wc = w.view(fn)
+    ref = x if x is not None else dout
+    dt = _DTYPES.get(ref.dtype)
+    rows = amap.T * amap.k
+    _need(len(groups) == 1 and groups[0] == amap.expert_end - amap.expert_begin, fn,
+          "adapters A [G, r, K] of the map's local groups expected")
+    _need(sorted_rows or amap.k == 1, fn, "a map of one group a row (k = 1) expected, or sorted rows")
+    _need(dt is not None and w.A.dtype == ref.dtype, fn, "rows of the adapters' type expected")
+    for t, width in ((x, K), (dout, N)):
+        _need(t is None or (t.shape == (rows, width) and t.dtype == ref.dtype), fn,
+              "x [rows, K] and y or dout [rows, N] of one type, a row for each of the map's, expected")
+    offsets = _of_shape(fn, "offsets", amap.offsets, (amap.E + 1,))
+    pair = rop = None
+    if not sorted_rows:
+        pair = _of_shape(fn, "pair_of_row", amap.pair_of_row, (rows,))
+        rop = _of_shape(fn, "row_of_pair", amap.row_of_pair, (amap.T, amap.k))
+    _on(fn, ref, x, dout, w.A, offsets, pair, rop)
+    cfg = mok.lora_config(rows, amap.E, amap.expert_begin, amap.expert_end, K, N, dt)
+    return rows, N, K, w.A.shape[1], wc, cfg, (_ready(pair), _ready(rop), _ready(offsets))
+
+
+def _added_to(fn: str, base, out, shape, like, *inputs):
+    """The base (contiguous) and the output of a sum, which may be one array."""
+    if base is not None:
+        _need(base.shape == shape and base.dtype == like.dtype, fn, f"rows to add to of {like.dtype} {list(shape)} expected")
+        _on(fn, like, base)
+    same = out is not None and base is not None and out.data_ptr() == base.data_ptr() and out.is_contiguous() and \
+        base.is_contiguous()
+    base = _ready(base)
+    out = _output(fn, out, shape, like.dtype, like.device, *inputs, None if same else base)
+    return base, out
+
+
+def lora_rows(x: torch.Tensor, amap: PairMap, w: LoraWeights, y: torch.Tensor | None = None,
+              sorted_rows: bool = False, out: torch.Tensor | None = None, save: bool = False):
+    """out_q = y_q + scale_g B_g (A_g x_q), g the group of row q (y None: 0).
+
+    Many requests' adapters beside one projection: amap =
+    sort_pairs(adapter[:, None], G), -1 for a row of the base model, and x
+    [T, K], y and out [T, N] in the tokens' order; a row of no adapter gets y.
+    One adapter on each expert's projection: the pairs' map with sorted_rows, and
+    all of them in the experts' sorted rows; rows of no expert are left as they
+    are.  `out` may be y itself.  With save the result is (out, u), u = A_g x_q
+    in fp32 [rows, r] and sorted rows, for lora_rows_backward."""
+    fn = "lora_rows"
+    rows, N, K, r, wc, cfg, (pair, rop, offsets) = _lora_args(fn, x, y, amap, w, sorted_rows)
+    _unrecorded(fn, x, y, out, w.scale)
+    _unrecorded(fn, w.A, w.B)
+    x = _ready(x)
+    y, out = _added_to(fn, y, out, (rows, N), x, x, pair, rop, offsets, w.A, w.B, w.scale)
+    u = torch.empty((rows, r), dtype=torch.float32, device=x.device) if save else None
+    ws = torch.empty(mok.mok_lora_workspace_query(cfg, r)[0], dtype=torch.uint8, device=x.device)
+    _call(mok.mok_lora_rows, x, x, y, pair, rop, offsets, wc, cfg, out, u, ws)
+    return (out, u) if save else out
+
+
+def lora_rows_backward(dout: torch.Tensor, x: torch.Tensor, u: torch.Tensor, amap: PairMap, w: LoraWeights,
+                       base: torch.Tensor | None = None, sorted_rows: bool = False, out: torch.Tensor | None = None):
+    """(dx, dA, dB) of lora_rows on x, whose u it kept: dx = base + the
+    adapters' share (base None: 0; `out` takes dx and may be base itself), dA
+    [G, r, K] and dB [G, N, r] in fp32, 0 for a group without rows.  y's
+    gradient is dout itself."""
+    fn = "lora_rows_backward"
+    rows, N, K, r, wc, cfg, (pair, rop, offsets) = _lora_args(fn, x, dout, amap, w, sorted_rows)
+    _need(u.dtype == torch.float32 and u.shape == (rows, r), fn, "fp32 u [rows, r] of the forward call expected")
+    _on(fn, x, u)
+    dout, x, u = _ready(dout), _ready(x), _ready(u)
+    base, dx = _added_to(fn, base, out, (rows, K), x, dout, x, u, pair, rop, offsets, w.A, w.B, w.scale)
+    dA = torch.empty(w.A.shape, dtype=torch.float32, device=x.device)
+    dB = torch.empty(w.B.shape, dtype=torch.float32, device=x.device)
+    ws = torch.empty(max(mok.mok_lora_workspace_query(cfg, r)[1], 16), dtype=torch.uint8, device=x.device)
+    _call(mok.mok_lora_rows_backward, x, dout, x, u, base, pair, rop, offsets, wc, cfg, dx, dA, dB, ws)
+    return dx, dA, dB
+
+
+# ------------------------------------------------------------------ the layer for a few tokens
+_GATING = {"softmax": 0, "sigmoid": mok.MOK_FLAG_SIGMOID_GATES}
+
+
+def few_token_layer(x: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor,
+                    k: int, expert_begin: int = 0, gating: str = "softmax", renorm: bool = False,
+                    adapter: torch.Tensor | None = None, lora=None, out: torch.Tensor | None = None):
+    """The layer for at most 16 tokens (a decode step), in two launches, four
+    with adapters: (out, topk_idx, topk_gate) with out[t] = sum_j gate[t, j]
+    W2_e (silu(W1_e x_t) * (W3_e x_t)), e = topk_idx[t, j].
+
+    x [T, d], w1 and w3 [E_loc, F, d], w2 [E_loc, d, F] of one type, fp32, bf16 or
+    fp16; logits fp32 [T, E]; the experts [expert_begin, expert_begin + E_loc) are
+    local and a token without one of them gets 0.  Routing as in the layer
+    (MoeShape.gating, renorm).  lora = (l1, l3, l2), LoraWeights [L, E_loc, ...]
+    of w1, w3 and w2 or None each, with int32 adapter [T]: token t's matrices are
+    W + scale B A of its adapter; an adapter outside [0, L) is none."""
+    fn = "few_token_layer"
+    dt = _DTYPES.get(x.dtype)
+    _need(x.dim() == 2 and dt is not None and x.shape[0] <= 16, fn, "fp32, bf16 or fp16 x [T, d], T <= 16, expected")
+    T, d = x.shape
+    _need(w1.dim() == 3 and w1.dtype == x.dtype and w1.shape[2] == d, fn, "w1 [E_loc, F, d] of x's type expected")
+    E_loc, F = w1.shape[:2]
+    _need(w3.shape == w1.shape and w3.dtype == x.dtype and w2.shape == (E_loc, d, F) and w2.dtype == x.dtype, fn,
+          "w3 [E_loc, F, d] and w2 [E_loc, d, F] of x's type expected")
+    _need(logits.dim() == 2 and logits.shape[0] == T and logits.dtype == torch.float32, fn,
+          "fp32 logits [T, E] expected")
+    E = logits.shape[1]
+    _need(gating in _GATING, fn, "gating 'softmax' or 'sigmoid' expected")
+    _on(fn, x, logits, w1, w3, w2, adapter)
+    _unrecorded(fn, x, logits, out, w1)
+    _unrecorded(fn, w3, w2)
+    L, lc, read = 0, None, []
+    _need((lora is None) == (adapter is None), fn, "lora and adapter expected together")
+    if lora is not None:
+        _need(adapter.dtype == torch.int32 and adapter.shape == (T,), fn, "int32 adapter [T] expected")
+        _need(len(lora) == 3, fn, "lora of w1, w3 and w2 expected")
+        lc = (mok.mok_lora_weights * 3)()
+        for m, (lw, N, K) in enumerate(zip(lora, (F, F, d), (d, d, F))):
+            if lw is None:
+                continue
+            groups, n, kk, c = lw.view(fn)
+            _need(len(groups) == 2 and groups[1] == E_loc and (n, kk) == (N, K) and lw.A.dtype == x.dtype and
+                  L in (0, groups[0]) and groups[0], fn, "adapters [L, E_loc, ...] of the weights' type and sizes expected")
+            _on(fn, x, lw.A)
+            _unrecorded(fn, lw.A, lw.B, lw.scale)
+            L = groups[0]
+            lc[m] = c
+            read += [lw.A, lw.B, lw.scale]
+    x, logits, w1, w3, w2, adapter = (_ready(t) for t in (x, logits, w1, w3, w2, adapter))
+    out = _output(fn, out, (T, d), x.dtype, x.device, x, logits, w1, w3, w2, adapter, *read)
+    idx = torch.empty((T, k), dtype=torch.int32, device=x.device)
+    gate = torch.empty((T, k), dtype=torch.float32, device=x.device)
+    cfg = mok.few_token_config(T, d, E, k, F, expert_begin, expert_begin + E_loc, dt,
+                               _GATING[gating] | (mok.MOK_FLAG_RENORM_GATES if renorm else 0), L)
+    ws = torch.empty(mok.mok_few_token_workspace_query(cfg, lc), dtype=torch.uint8, device=x.device)
+    _call(mok.mok_few_token_layer, x, x, logits, w1, w3, w2, adapter, lc, cfg, out, idx, gate, ws)
+    return out, idx, gate

@@ -60,6 +60,19 @@ class mok_int4_config(ctypes.Structure):
                 ("rows", "x_rows", "k", "E", "expert_begin", "expert_end", "N", "K", "group", "dtype")]
 
 
+class mok_few_token_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "d", "E", "k", "ffn", "expert_begin", "expert_end", "dtype")] + [
+        ("flags", ctypes.c_uint32), ("L", ctypes.c_int32)]
+
+
+class mok_lora_weights(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("r", ctypes.c_int32)]
+
+
+class mok_lora_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "E", "expert_begin", "expert_end", "K", "N", "dtype")]
+
+
 MOK_CHECK_LOGITS, MOK_CHECK_INDEX = 0x1, 0x2
 
 
@@ -136,6 +149,16 @@ def lib() -> ctypes.CDLL:
                                              _P]
         L.mok_quantize_int4.restype = ctypes.c_int
         L.mok_quantize_int4.argtypes = [_P, i64, i64, i32, ctypes.c_int, _P, _P, _P, _P]
+        few, lw, lc = (ctypes.POINTER(t) for t in (mok_few_token_config, mok_lora_weights, mok_lora_config))
+        size = ctypes.POINTER(ctypes.c_size_t)
+        L.mok_few_token_workspace_query.argtypes = [few, lw, size]
+        L.mok_few_token_layer.argtypes = [_P, _P, _P, _P, _P, _P, lw, few, _P, _P, _P, _P, _P]
+        L.mok_lora_workspace_query.argtypes = [lc, i32, size, size]
+        L.mok_lora_rows.argtypes = [_P, _P, _P, _P, _P, lw, lc, _P, _P, _P, _P]
+        L.mok_lora_rows_backward.argtypes = [_P, _P, _P, _P, _P, _P, _P, lw, lc, _P, _P, _P, _P, _P]
+        for f in (L.mok_few_token_workspace_query, L.mok_few_token_layer, L.mok_lora_workspace_query, L.mok_lora_rows,
+                  L.mok_lora_rows_backward):
+            f.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -318,3 +341,57 @@ def mok_quantize_int4(src, rows, K, group, dtype, codes, scales, zeros, stream=0
     _int32("mok_quantize_int4", group)
     _check(lib().mok_quantize_int4(_ptr(src), rows, K, group, dtype, _ptr(codes), _ptr(scales), _ptr(zeros),
                                    stream or None), "mok_quantize_int4")
+
+
+def few_token_config(T, d, E, k, ffn, expert_begin, expert_end, dtype, flags, L) -> mok_few_token_config:
+    _int32("mok_few_token_config", T | d | E | k | ffn | expert_begin | expert_end | dtype | flags | L)
+    return mok_few_token_config(T, d, E, k, ffn, expert_begin, expert_end, dtype, flags, L)
+
+
+def lora_weights(A, B, scale, r) -> mok_lora_weights:
+    _int32("mok_lora_weights", r)
+    return mok_lora_weights(_ptr(A), _ptr(B), _ptr(scale), r)
+
+
+def lora_config(rows, E, expert_begin, expert_end, K, N, dtype) -> mok_lora_config:
+    _int32("mok_lora_config", rows | E | expert_begin | expert_end | K | N | dtype)
+    return mok_lora_config(rows, E, expert_begin, expert_end, K, N, dtype)
+
+
+def mok_few_token_workspace_query(cfg: mok_few_token_config, lora=None) -> int:
+    """`lora`: None, or a ctypes array of three mok_lora_weights."""
+    n = ctypes.c_size_t()
+    _check(lib().mok_few_token_workspace_query(ctypes.byref(cfg), lora, ctypes.byref(n)),
+           "mok_few_token_workspace_query")
+    return n.value
+
+
+def mok_few_token_layer(x, router_logits, W1, W3, W2, adapter, lora, cfg, out, topk_idx, topk_gate, workspace,
+                        stream=0):
+    _check(lib().mok_few_token_layer(_ptr(x), _ptr(router_logits), _ptr(W1), _ptr(W3), _ptr(W2), _ptr(adapter), lora,
+                                     ctypes.byref(cfg), _ptr(out), _ptr(topk_idx), _ptr(topk_gate), _ptr(workspace),
+                                     stream or None), "mok_few_token_layer")
+
+
+def mok_lora_workspace_query(cfg: mok_lora_config, r: int):
+    """(bytes of the forward call's workspace, of the backward call's)."""
+    _int32("mok_lora_workspace_query", r)
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().mok_lora_workspace_query(ctypes.byref(cfg), r, ctypes.byref(f), ctypes.byref(b)),
+           "mok_lora_workspace_query")
+    return f.value, b.value
+
+
+def mok_lora_rows(x, y, pair_of_row, row_of_pair, offsets, w: mok_lora_weights, cfg: mok_lora_config, out, u,
+                  workspace, stream=0):
+    _check(lib().mok_lora_rows(_ptr(x), _ptr(y), _ptr(pair_of_row), _ptr(row_of_pair), _ptr(offsets), ctypes.byref(w),
+                               ctypes.byref(cfg), _ptr(out), _ptr(u), _ptr(workspace), stream or None),
+           "mok_lora_rows")
+
+
+def mok_lora_rows_backward(dout, x, u, base, pair_of_row, row_of_pair, offsets, w: mok_lora_weights,
+                           cfg: mok_lora_config, dx, dA, dB, workspace, stream=0):
+    _check(lib().mok_lora_rows_backward(_ptr(dout), _ptr(x), _ptr(u), _ptr(base), _ptr(pair_of_row),
+                                        _ptr(row_of_pair), _ptr(offsets), ctypes.byref(w), ctypes.byref(cfg),
+                                        _ptr(dx), _ptr(dA), _ptr(dB), _ptr(workspace), stream or None),
+           "mok_lora_rows_backward")

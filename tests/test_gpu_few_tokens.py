@@ -1,0 +1,268 @@
+"""The layer for a few tokens on the GPU, with adapters and without, against a
+plain implementation in 64 bits (tests/adapter_cases.py derives the bounds), and
+against the layer itself."""
+import pytest
+import torch
+
+import workloads as W
+from mixture_experts_layer_34_amd import expert_ops as X
+from mixture_experts_layer_34_amd.layer import MoeBuffers, MoeShape
+from tests.adapter_cases import DT, close, gen, layer64, randn, route64, rounded
+from tests.gpu_case import note
+
+pytestmark = pytest.mark.gpu
+
+
+def _case(T, d, F, E, n, dt, seed):
+    g = gen(seed)
+    return (randn(g, (T, d), dt), randn(g, (T, E)), randn(g, (n, F, d), dt, d ** -0.5),
+            randn(g, (n, F, d), dt, d ** -0.5), randn(g, (n, d, F), dt, F ** -0.5))
+
+
+def _lora(T, d, F, n, L, ranks, dt, seed, scaled=True):
+    g = gen(seed)
+    ws = [None if r is None else
+          X.LoraWeights(randn(g, (L, n, r, K), dt, K ** -0.5), randn(g, (L, n, N, r), dt, 0.5 * r ** -0.5),
+                        randn(g, (L,)) if scaled else None)
+          for r, N, K in zip(ranks, (F, F, d), (d, d, F))]
+    adapter = torch.randint(-1, L + 1, (T,), generator=g, dtype=torch.int32)  # L: past the last, none
+    return adapter.cuda(), ws
+
+
+def _check(args, k, dt, **kw):
+    got, idx, gate = X.few_token_layer(*args, k, **kw)
+    ref, err, ridx, rgate = layer64(*args, k, eb=kw.get("expert_begin", 0),
+                                    **{n: v for n, v in kw.items() if n != "expert_begin"})
+    assert torch.equal(idx.cpu().long(), ridx)
+    close(gate, rgate, 2.0 ** -18 * rgate, "gates")
+    close(got, ref, rounded(ref, err, dt), "out")
+    return got, idx, gate
+
+
+LAYERS = [(1, 64, 64, 4, 1, "bf16"), (1, 1, 1, 1, 1, "f32"), (2, 32, 16, 3, 3, "f16"), (3, 128, 256, 8, 2, "f32"),
+          (5, 130, 67, 17, 4, "bf16"), (7, 91, 33, 9, 2, "f16"), (16, 64, 48, 4, 2, "bf16"),
+          (16, 256, 320, 16, 8, "bf16"), (9, 257, 129, 64, 6, "f32"), (13, 512, 96, 130, 5, "bf16"),
+          (16, 100, 40, 300, 64, "bf16"), (4, 40, 200, 1024, 8, "f16"), (11, 1000, 72, 6, 6, "bf16"),
+          (16, 33, 31, 64, 64, "f32"), (6, 2048, 32, 8, 2, "bf16"), (8, 24, 2080, 8, 3, "f16")]
+
+
+@pytest.mark.parametrize("T,d,F,E,k,dt", LAYERS)
+@pytest.mark.parametrize("gating,renorm", [("softmax", False), ("sigmoid", True)])
+def test_layer(T, d, F, E, k, dt, gating, renorm):
+    note(f"few tokens T={T} d={d} F={F} E={E} k={k} {dt} {gating} {renorm}")
+    _check(_case(T, d, F, E, E, dt, T + d + F), k, dt, gating=gating, renorm=renorm)
+
+
+@pytest.mark.parametrize("gating,renorm", [("softmax", True), ("sigmoid", False)])
+@pytest.mark.parametrize("T,E,eb,n,k", [(5, 16, 4, 3, 2), (16, 64, 60, 4, 8), (1, 8, 7, 1, 1), (12, 128, 0, 16, 8)])
+def test_share_of_the_experts(T, E, eb, n, k, gating, renorm):
+    """Tokens without a local expert get 0."""
+    args = _case(T, 96, 80, E, n, "bf16", T + E)
+    got, idx, _ = _check(args, k, "bf16", expert_begin=eb, gating=gating, renorm=renorm)
+    none = ~((idx >= eb) & (idx < eb + n)).any(1)
+    assert not got[none].any()
+
+
+@pytest.mark.parametrize("T,d,F,E,k,dt", LAYERS[1:])
+@pytest.mark.parametrize("ranks", [(16, 16, 16), (3, None, 33), (None, 128, None)])
+def test_adapters(T, d, F, E, k, dt, ranks):
+    note(f"few tokens with adapters T={T} d={d} F={F} E={E} k={k} {dt} ranks={ranks}")
+    if E > 64 and max(r or 0 for r in ranks) > 64:
+        ranks = tuple(r and min(r, 20) for r in ranks)  # the stacks stay small
+    adapter, lora = _lora(T, d, F, E, 3, ranks, dt, T * 7 + d, scaled=dt != "f16")
+    _check(_case(T, d, F, E, E, dt, T + d), k, dt, adapter=adapter, lora=lora)
+
+
+def test_adapters_on_a_share_and_none_in_use():
+    T, d, F, E, eb, n, k, dt = 9, 96, 64, 16, 5, 6, 4, "bf16"
+    args = _case(T, d, F, E, n, dt, 3)
+    adapter, lora = _lora(T, d, F, n, 4, (8, 8, 8), dt, 5)
+    _check(args, k, dt, expert_begin=eb, adapter=adapter, lora=lora)
+    plain = X.few_token_layer(*args, k, expert_begin=eb)[0]
+    adapter.fill_(-1)
+    assert torch.equal(X.few_token_layer(*args, k, expert_begin=eb, adapter=adapter, lora=lora)[0], plain)
+    assert torch.equal(X.few_token_layer(*args, k, expert_begin=eb, adapter=adapter, lora=(None,) * 3)[0], plain)
+
+
+@pytest.mark.parametrize("gating,renorm", [("softmax", False), ("softmax", True), ("sigmoid", False),
+                                           ("sigmoid", True)])
+def test_routing_is_the_layers_own(gating, renorm):
+    """Indices and gates bit for bit those of the whole layer's call on the
+    same logits, ties among them; the outputs within the two calls' rounding."""
+    T, d, E, k, F = 16, 256, 32, 5, 128
+    args = list(_case(T, d, F, E, E, "bf16", 17))
+    args[1][2] = 0.25                       # a row of ties
+    args[1][3, ::2] = args[1][3, 1::2]
+    buf = MoeBuffers(MoeShape(T=T, d=d, E=E, k=k, F=F, gating=gating, renorm=renorm))
+    buf.forward(*args)
+    got, idx, gate = _check(args, k, "bf16", gating=gating, renorm=renorm)
+    assert torch.equal(idx, buf.topk_idx) and torch.equal(gate, buf.topk_gate)
+    # the layer rounds h, then each pair's y, before its weighted sum: two
+    # roundings of 2^-8 for each, of the pairs' magnitudes, beside this call's
+    _, err, ridx, rgate = layer64(*args, k, gating=gating, renorm=renorm)
+    mag = torch.zeros((T, d), dtype=torch.float64)
+    for t in range(T):
+        for j in range(k):
+            w1, w3, w2 = (w[ridx[t, j]].double().cpu() for w in args[2:])
+            z = w1 @ args[0][t].double().cpu()
+            mag[t] += rgate[t, j] * (w2.abs() @ (z * torch.sigmoid(z) * (w3 @ args[0][t].double().cpu())).abs())
+    close(got, buf.out, 2 * err + 2.0 ** -6 * mag, "the layer's out")
+
+
+def test_no_tokens_and_sixteen_at_most():
+    args = _case(0, 64, 32, 8, 8, "bf16", 1)
+    out, idx, gate = X.few_token_layer(*args, 2)
+    assert out.shape == (0, 64) and idx.shape == (0, 2) and gate.shape == (0, 2)
+    with pytest.raises(ValueError, match="T <= 16"):
+        X.few_token_layer(*_case(17, 64, 32, 8, 8, "bf16", 1), 2)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_tokens_non_finite_values_stay_its_own(bad):
+    for dt in DT:
+        args = _case(6, 96, 64, 8, 8, dt, 23)
+        clean = X.few_token_layer(*args, 3)[0]
+        args[0][2, 5] = bad
+        got = X.few_token_layer(*args, 3)[0]
+        keep = [0, 1, 3, 4, 5]
+        assert torch.equal(got[keep], clean[keep]) and not torch.isfinite(got[2]).all()
+
+
+def test_nan_logits_rank_last_and_stay_in_range():
+    args = _case(4, 64, 32, 8, 8, "bf16", 29)
+    args[1][1, :7] = float("nan")
+    args[1][2] = float("nan")
+    _, idx, _ = X.few_token_layer(*args, 3)
+    ref, _ = route64(args[1], 3, "softmax", False)
+    assert torch.equal(idx.cpu().long(), ref)
+
+
+def test_strides_other_memory_and_given_outputs():
+    args = _case(5, 96, 64, 8, 8, "bf16", 31)
+    want = X.few_token_layer(*args, 2)
+    x, logits, w1, w3, w2 = args
+    xs = torch.empty((96, 5), dtype=x.dtype, device="cuda").t()
+    xs.copy_(x)
+    ls = torch.empty((5, 9), device="cuda")[:, 1:]
+    ls.copy_(logits)
+    ws = w2.transpose(1, 2).contiguous().transpose(1, 2)
+    out = torch.empty_like(x)
+    got = X.few_token_layer(xs, ls, w1, w3, ws, 2, out=out)
+    assert got[0] is out and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_two_streams_and_captured_graphs():
+    T, d, F, E, k, dt = 12, 256, 192, 16, 4, "bf16"
+    args, args2 = _case(T, d, F, E, E, dt, 41), _case(T, d, F, E, E, dt, 42)
+    adapter, lora = _lora(T, d, F, E, 3, (16, 16, 16), dt, 43)
+
+    def step(a):
+        return X.few_token_layer(*a, k, adapter=adapter, lora=lora)
+
+    want, want2 = step(args), step(args2)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(s1):
+            a = step(args)
+        with torch.cuda.stream(s2):
+            b = step(args2)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(a, want)) and all(torch.equal(p, q) for p, q in zip(b, want2))
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        held = step(args)
+    with torch.cuda.graph(g2):
+        held2 = step(args)
+    for n in range(4):
+        for mine, other in zip(args[:2], args2[:2]):
+            mine.copy_(other if n % 2 else mine.flip(0))
+        ref = step(args)
+        for t in (*held, *held2):
+            t.fill_(7)
+        g1.replay()
+        g2.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(held, ref))
+        assert all(torch.equal(p, q) for p, q in zip(held2, ref))
+
+
+def test_the_training_shape_by_samples():
+    """d 4096, E 128, k 8, F 1536 (bf16): all of a token's output against 64
+    bits, one token and sixteen."""
+    w = W.WORKLOADS["bf16_train"]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+
+    def normal(shape, std):
+        return torch.empty(shape, dtype=torch.bfloat16, device="cuda").normal_(0, std, generator=g)
+
+    w1, w3 = normal((w.E, w.F, w.d), w.d ** -0.5), normal((w.E, w.F, w.d), w.d ** -0.5)
+    w2 = normal((w.E, w.d, w.F), w.F ** -0.5)
+    for T in (1, 16):
+        x, logits = normal((T, w.d), 1.0), torch.randn((T, w.E), generator=g, device="cuda")
+        got, idx, _ = X.few_token_layer(x, logits, w1, w3, w2, w.k)
+        at = [0, T - 1]
+        ref, err, ridx, _ = layer64(x[at], logits[at], w1, w3, w2, w.k)
+        assert torch.equal(idx[at].cpu().long(), ridx)
+        close(got[at], ref, rounded(ref, err, "bf16"), "out")
+
+
+def test_a_decode_step_with_requests_adapters():
+    """A shared projection in 4 bits with each request's adapter beside it, the
+    router, and the experts with the same requests' adapters."""
+    T, d, E, k, F, L, r, dt = 12, 256, 16, 4, 128, 3, 8, "bf16"
+    g = gen(51)
+    x = randn(g, (T, d), dt)
+    adapter = torch.randint(-1, L, (T,), generator=g, dtype=torch.int32).cuda()
+    proj = X.quantize_int4(randn(g, (d, d), dt, d ** -0.5), group=64)
+    shared = X.LoraWeights(randn(g, (L, r, d), dt, d ** -0.5), randn(g, (L, d, r), dt, 0.3), randn(g, (L,)))
+    wr = randn(g, (E, d), dt, d ** -0.5)
+    _, _, w1, w3, w2 = _case(T, d, F, E, E, dt, 52)
+    _, lora = _lora(T, d, F, E, L, (r, r, r), dt, 53)
+    amap = X.sort_pairs(adapter[:, None], L)
+
+    base = X.expert_matvec_int4(x, proj)
+    hidden = X.lora_rows(x, amap, shared, y=base)
+    from mixture_experts_layer_34_amd.layer import router_logits
+    logits = router_logits(hidden, wr)
+    out, idx, gate = X.few_token_layer(hidden, logits, w1, w3, w2, k, adapter=adapter, lora=lora)
+
+    from tests.adapter_cases import lora64
+    ref, err, _, _ = lora64(x, adapter.cpu().long(), shared.A, shared.B, shared.scale, base)
+    close(hidden, ref, rounded(ref, err, dt), "projection")
+    ref, err, ridx, _ = layer64(hidden, logits, w1, w3, w2, k, adapter=adapter, lora=lora)
+    assert torch.equal(idx.cpu().long(), ridx)
+    close(out, ref, rounded(ref, err, dt), "layer")
+
+
+def test_training_adapters_of_the_experts():
+    """Rows to the experts, an adapter beside each expert's product, back; its
+    gradients through the same steps against autograd in 64 bits."""
+    T, k, E, d, N, r = 30, 3, 6, 64, 48, 4
+    g = gen(61)
+    idx = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32).cuda()
+    gate = torch.rand((T, k), generator=g).cuda()
+    x, dout = randn(g, (T, d)), randn(g, (T, N))
+    w = X.LoraWeights(randn(g, (E, r, d), "f32", d ** -0.5), randn(g, (E, N, r), "f32", 0.5), randn(g, (E,)))
+    m = X.sort_pairs(idx, E)
+    xp = X.permute_rows(x, m)
+    yp, u = X.lora_rows(xp, m, w, sorted_rows=True, save=True)
+    out = X.unpermute_rows(yp, m, gate=gate)
+    dyp, _ = X.unpermute_rows_backward(dout, m, gate=gate, y=yp)
+    dxp, dA, dB = X.lora_rows_backward(dyp, xp, u, m, w, sorted_rows=True)
+    dx, _ = X.permute_rows_backward(dxp, m)
+    leaf = [t.double().cpu().requires_grad_() for t in (x, w.A, w.B)]
+    s, gd, ic = w.scale.double().cpu(), gate.double().cpu(), idx.cpu().long()
+    ref = torch.zeros((T, N), dtype=torch.float64)
+    for j in range(k):
+        e = ic[:, j]
+        ref = ref + gd[:, j, None] * s[e][:, None] * torch.einsum(
+            "tnr,trd,td->tn", leaf[2][e], leaf[1][e], leaf[0])
+    (ref * dout.double().cpu()).sum().backward()
+    for got, want, what in ((out, ref.detach(), "out"), (dx, leaf[0].grad, "dx"), (dA, leaf[1].grad, "dA"),
+                            (dB, leaf[2].grad, "dB")):
+        # fp32 throughout: chains of at most d + N + T k + 4 r steps of 2^-23, of
+        # magnitudes that stay within 64 times the largest result
+        close(got, want, torch.full_like(want, 64 * (d + N + T * k + 4 * r) * 2.0 ** -23 * float(want.abs().max())),
+              what)
