@@ -762,7 +762,8 @@ mok_status mok_few_token_layer(const void* x, const float* router_logits, const 
  * Sums are fp32 in a fixed order: the same bits on every run.  out and dx are
  * rounded once; u and du enter their products with 16 bits of mantissa or more,
  * the sums of dA and dB with all of theirs.
- * 0 <= rows < 2^30, 1 <= r <= 128, 1 <= K, N <= 2^20, 1 <= E <= 1024.
+ * 0 <= rows < 2^30, 1 <= r <= 128, 1 <= K, N <= 2^20, rows * K and rows * N < 2^40,
+ * 1 <= E <= 1024.
  * Errors: MOK_ERR_INVALID_ARG for a null or misaligned pointer, one of
  * pair_of_row and row_of_pair without the other, or a shape outside these bounds;
  * MOK_ERR_HIP for a failed launch.

@@ -72,8 +72,9 @@ mok_status few_layout(const mok_few_token_config* cfg, const mok_lora_weights* l
 }
 
 struct LoraLayout {
-  size_t part, At, Bt, du, total;
+  size_t part, At, Bt, du, sums, total;
   int splits;
+  LoraGradPlan grad;
 };
 mok_status lora_layout(const mok_lora_config* cfg, int32_t r, bool backward, LoraLayout* o) {
   if (!cfg) return MOK_ERR_INVALID_ARG;
@@ -81,14 +82,18 @@ mok_status lora_layout(const mok_lora_config* cfg, int32_t r, bool backward, Lor
   if (c.rows < 0 || c.rows >= (1 << 30) || bad_experts(c.E, c.expert_begin, c.expert_end)) return MOK_ERR_INVALID_ARG;
   if (c.K < 1 || c.K > (1 << 20) || c.N < 1 || c.N > (1 << 20) || bad_rank(r) || bad_dtype(c.dtype))
     return MOK_ERR_INVALID_ARG;
+  // the tiles of a launch are counted in 32 bits
+  if ((int64_t)c.rows * (c.K > c.N ? c.K : c.N) >= (int64_t(1) << 40)) return MOK_ERR_INVALID_ARG;
   const int G = c.expert_end - c.expert_begin;
   Parts p;
-  o->splits = lora_splits(c.rows, G, backward ? c.N : c.K, c.dtype);
-  o->part = p.take((int64_t)o->splits * c.rows * r * 4);
+  o->splits = lora_splits(c.rows, G, r, backward ? c.N : c.K, c.dtype);
+  o->part = p.take((int64_t)o->splits * c.rows * lora_width(r) * 4);
   if (backward) {
     o->At = p.take((int64_t)G * r * c.K * elem_bytes(c.dtype));
     o->Bt = p.take((int64_t)G * r * c.N * elem_bytes(c.dtype));
-    o->du = o->splits > 1 ? p.take((int64_t)c.rows * r * 4) : o->part;
+    o->du = o->splits > 1 ? p.take((int64_t)c.rows * lora_width(r) * 4) : o->part;
+    o->grad = lora_grad_plan(c.rows, G, r, c.K, c.N, c.dtype);
+    o->sums = p.take(o->grad.part_bytes);
   }
   o->total = p.total;
   return MOK_OK;
@@ -302,12 +307,10 @@ mok_status mok_lora_rows(const void* x, const void* y, const int32_t* pair_of_ro
     return MOK_ERR_INVALID_ARG;
   if (c.rows == 0) return MOK_OK;
   const LoraMap map{offsets + c.expert_begin, pair_of_row, row_of_pair, c.rows, c.expert_end - c.expert_begin};
-  // one share of K: its sum is u itself
-  float* part = l.splits == 1 && u ? u : (float*)((char*)workspace + l.part);
+  float* part = (float*)((char*)workspace + l.part);
   hipError_t e = launch_lora_rank(LoraRank{map, x, w->A, part, c.K, w->r, c.dtype, l.splits}, (hipStream_t)stream);
   if (e == hipSuccess)
-    e = launch_lora_add(LoraAdd{map, part, w->B, w->scale, y, out, l.splits == 1 ? nullptr : u, c.N, w->r, c.dtype,
-                                l.splits}, (hipStream_t)stream);
+    e = launch_lora_add(LoraAdd{map, part, w->B, w->scale, y, out, u, c.N, w->r, c.dtype, l.splits, w->r}, (hipStream_t)stream);
   return result(e);
 }
 
@@ -331,17 +334,18 @@ mok_status mok_lora_rows_backward(const void* dout, const void* x, const float* 
   char* ws = (char*)workspace;
   float *part = (float*)(ws + l.part), *du = (float*)(ws + l.du);
   hipStream_t s = (hipStream_t)stream;
-  hipError_t e = hipSuccess;
+  hipError_t e = launch_lora_prepare(LoraPrepare{map, w->A, w->B, ws + l.At, ws + l.Bt, dA, dB, w->r, c.K, c.N,
+                                                 c.dtype}, s);
   if (c.rows > 0) {
-    e = launch_lora_transpose(w->A, w->B, map.G, w->r, c.K, c.N, c.dtype, ws + l.At, ws + l.Bt, s);
     if (e == hipSuccess)
       e = launch_lora_rank(LoraRank{map, dout, ws + l.Bt, part, c.N, w->r, c.dtype, l.splits}, s);
     if (e == hipSuccess)
       e = launch_lora_add(LoraAdd{map, part, ws + l.At, w->scale, base, dx, l.splits == 1 ? nullptr : du, c.K, w->r,
-                                  c.dtype, l.splits}, s);
+                                  c.dtype, l.splits, lora_width(w->r)}, s);
+    if (e == hipSuccess)
+      e = launch_lora_grad(LoraGrad{map, {x, dout}, {du, u}, {dA, dB}, {c.K, c.N}, w->scale, w->r, c.dtype,
+                                    l.grad.tile_rows, l.grad.part_bytes ? (float*)(ws + l.sums) : nullptr}, s);
   }
-  if (e == hipSuccess)
-    e = launch_lora_grad(LoraGrad{map, {x, dout}, {du, u}, {dA, dB}, {c.K, c.N}, w->scale, w->r, c.dtype}, s);
   return result(e);
 }
 

@@ -148,9 +148,9 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
   build_slots(a, s, bits, base, 64 * kUpWaves);
 
   const int ntn = a.Fp / 16, total = s.nslots * ntn;
-  const int full = a.d / STEP, steps = (a.d + STEP - 1) / STEP;  // whole K steps, and all of them
-  const int s0 = steps * w / kUpWaves, s1 = steps * (w + 1) / kUpWaves;
-  const int e1 = s1 < full ? s1 : full;  // whole steps of this wave
+  const int full = a.d / STEP;                                    // whole K steps
+  const int all = full / U;                                      // whole chunks: the waves take them in turn
+  const int chunks = all > w ? (all - w + kUpWaves - 1) / kUpWaves : 0;
   const int64_t row_bytes = (int64_t)a.d * S;
   int flip = 0;
   for (int un = blockIdx.x; un < total; un += gridDim.x, flip ^= 1) {
@@ -160,10 +160,10 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
     const uint64_t has = __ballot(pair >= 0);
     const int tx = pair >= 0 ? i16 : __ffsll((unsigned long long)has) - 1;  // a token that has the expert
     const int n = n0 + i16 < a.F ? n0 + i16 : a.F - 1;
-    const int64_t at = ((int64_t)e * a.F + n) * row_bytes + (int64_t)(s0 * STEP + g * KE) * S;
+    const int64_t at = ((int64_t)e * a.F + n) * row_bytes + (int64_t)(g * KE) * S;
     const char* p1 = (const char*)a.w[0] + at;
     const char* p3 = (const char*)a.w[1] + at;
-    const char* px = (const char*)a.x + tx * row_bytes + (int64_t)(s0 * STEP + g * KE) * S;
+    const char* px = (const char*)a.x + tx * row_bytes + (int64_t)(g * KE) * S;
     f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     u32x4_t q1[2][U], q3[2][U], qx[2][U];
     auto load = [&](int buf, int c) {
@@ -174,6 +174,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
         q3[buf][j] = load16<DT>(p3 + o);
         qx[buf][j] = load16<DT>(px + o);
       }
+      __builtin_amdgcn_sched_barrier(0);
     };
     auto mul = [&](int buf) {
 #pragma unroll
@@ -181,35 +182,33 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
         acc[0] = mma<DT>(q1[buf][j], qx[buf][j], acc[0]);
         acc[1] = mma<DT>(q3[buf][j], qx[buf][j], acc[1]);
       }
+      __builtin_amdgcn_sched_barrier(0);
     };
-    const int ns = e1 > s0 ? e1 - s0 : 0, nc = ns / U * U;
-    if (nc) load(0, 0);
-    for (int c = 0; c < nc; c += 2 * U) {
-      if (c + U < nc) load(1, c + U);
-      mul(0);
-      if (c + U < nc) {
-        if (c + 2 * U < nc) load(0, c + 2 * U);
+    // Chunk c + 1 is in flight while chunk c is multiplied.  No load stands under
+    // a condition (the last one is asked for again): behind a branch the compiler
+    // can only wait for every load, and the ring would run empty at each turn.
+    // And it may not move loads to their uses, where they save it registers.
+    if (chunks) {
+      load(0, w * U);
+      int c = 0;
+      for (; c + 2 <= chunks; c += 2) {
+        load(1, ((c + 1) * kUpWaves + w) * U);
+        mul(0);
+        load(0, ((c + 2 < chunks ? c + 2 : chunks - 1) * kUpWaves + w) * U);
         mul(1);
       }
+      if (c < chunks) mul(0);
     }
-    if (nc < ns) {  // the steps that fill no chunk
-#pragma unroll
-      for (int j = 0; j < U - 1; ++j)
-        if (nc + j < ns) {
-          const int o = (nc + j) * STEP * S;
-          q1[0][j] = load16<DT>(p1 + o);
-          q3[0][j] = load16<DT>(p3 + o);
-          qx[0][j] = load16<DT>(px + o);
-        }
-#pragma unroll
-      for (int j = 0; j < U - 1; ++j)
-        if (nc + j < ns) {
-          acc[0] = mma<DT>(q1[0][j], qx[0][j], acc[0]);
-          acc[1] = mma<DT>(q3[0][j], qx[0][j], acc[1]);
-        }
-    }
-    if (s1 > full) {  // the step that d ends in
-      const int left = a.d - full * STEP - g * KE, o = (full - s0) * STEP * S;
+    // the steps that fill no chunk, a wave each, and the step that d ends in
+    for (int i = all * U; i < full; ++i)
+      if (i % kUpWaves == w) {
+        const int o = i * STEP * S;
+        const u32x4_t vx = load16<DT>(px + o);
+        acc[0] = mma<DT>(load16<DT>(p1 + o), vx, acc[0]);
+        acc[1] = mma<DT>(load16<DT>(p3 + o), vx, acc[1]);
+      }
+    if (full * STEP < a.d && w == 0) {
+      const int left = a.d - full * STEP - g * KE, o = full * STEP * S;
       const u32x4_t vx = load_part<DT>(px + o, left);
       acc[0] = mma<DT>(load_part<DT>(p1 + o, left), vx, acc[0]);
       acc[1] = mma<DT>(load_part<DT>(p3 + o, left), vx, acc[1]);
@@ -261,7 +260,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
 #endif
 }
 
-template <int DT, int NW>
+template <int DT, int NW, bool WHOLE>
 __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewTokens a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int KE = kFragElems<DT>, STEP = kFragStep<DT>, S = Elem<DT>::kBytes, U = kUnroll;
@@ -283,59 +282,52 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewTokens a) {
   const int n0 = blockIdx.x * 16;
   const int n = n0 + i16 < a.d ? n0 + i16 : a.d - 1;
   const int64_t row_bytes = (int64_t)a.F * S;
-  const int full = a.F / STEP, steps = a.Fp / STEP;  // of one expert: whole K steps of W2, and all of them
-  const int chunks = (steps + U - 1) / U;
-  const int64_t all = (int64_t)s.nslots * chunks;
-  const int c0 = (int)(all * w / NW), c1 = (int)(all * (w + 1) / NW);
+  const int chunks = (a.F + STEP * U - 1) / (STEP * U);  // of one expert
+  const int all = s.nslots * chunks;  // the waves take them in turn: what they read at a time is neighbouring
+  const int mine = all > w ? (all - w + NW - 1) / NW : 0;
   const auto hrs = __builtin_amdgcn_make_buffer_rsrc(a.h, (short)0, (int)((int64_t)P * a.Fp * S), 0x00020000);
-  // cursor of the next chunk to load
-  int slot = chunks ? c0 / chunks : 0, ch = c0 - slot * chunks, e = 0;
-  uint32_t hoff = 0;
-  const char* wp = nullptr;
-  auto open = [&]() {
-    if (slot < s.nslots) {
-      e = __builtin_amdgcn_readfirstlane(s.expert[slot]);
-      const int pair = s.pair[slot * 16 + i16];
-      // a pair that is not: an offset past the buffer, which loads zeros
-      hoff = pair >= 0 ? (uint32_t)(pair * a.Fp + g * KE) * S : 0xC0000000u;
-      wp = (const char*)a.w[2] + ((int64_t)e * a.d + n) * row_bytes + g * KE * S;
-    }
-  };
+  // cursor of the next chunk to load; past the last one it stays on it
+  const int skip_slots = NW / chunks, skip = NW - skip_slots * chunks;
+  int slot = w / chunks, ch = w - slot * chunks;
   f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
   u32x4_t qw[2][U], qh[2][U];
+  // WHOLE: F is a multiple of KE, a lane's 16 bytes lie in F or past it; a
+  // lane past it reads the row's first bytes and zeros of h.
   auto load = [&](int buf) {
+    const int e = __builtin_amdgcn_readfirstlane(s.expert[slot]);
+    const int pair = s.pair[slot * 16 + i16];
+    // a pair that is not: an offset past the buffer, which loads zeros
+    const uint32_t hoff = pair >= 0 ? (uint32_t)(pair * a.Fp) * S : 0xC0000000u;
+    const char* wp = (const char*)a.w[2] + ((int64_t)e * a.d + n) * row_bytes;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const int st = ch * U + j;
-      const int o = st * STEP * S;
-      if (st < full) {
-        qw[buf][j] = load16<DT>(wp + o);
-      } else {
-        const int left = a.F - st * STEP - g * KE;
-        qw[buf][j] = load_part<DT>(wp + o, left < 0 ? 0 : left);
-      }
-      const auto v = __builtin_amdgcn_raw_buffer_load_b128(hrs, st < steps ? hoff + o : 0xC0000000u, 0, 0);
+      const int k = (ch * U + j) * STEP + g * KE;
+      if constexpr (WHOLE) qw[buf][j] = load16<DT>(wp + (k < a.F ? k : 0) * S);
+      else qw[buf][j] = load_part<DT>(wp + k * S, k < a.F ? a.F - k : 0);
+      const auto v = __builtin_amdgcn_raw_buffer_load_b128(hrs, k < a.F ? hoff + k * S : 0xC0000000u, 0, 0);
       qh[buf][j] = u32x4_t{(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
     }
-    if (++ch == chunks) {
-      ch = 0;
-      ++slot;
-      open();
-    }
+    const bool wrap = ch + skip >= chunks;
+    const int next = slot + skip_slots + wrap;
+    ch = next < s.nslots ? ch + skip - (wrap ? chunks : 0) : ch;
+    slot = next < s.nslots ? next : slot;
+    __builtin_amdgcn_sched_barrier(0);
   };
   auto mul = [&](int buf) {
 #pragma unroll
     for (int j = 0; j < U; ++j) acc = mma<DT>(qw[buf][j], qh[buf][j], acc);
+    __builtin_amdgcn_sched_barrier(0);
   };
-  open();
-  if (c0 < c1) load(0);
-  for (int c = c0; c < c1; c += 2) {
-    if (c + 1 < c1) load(1);
-    mul(0);
-    if (c + 1 < c1) {
-      if (c + 2 < c1) load(0);
+  if (mine) {  // no load under a condition, as in UP
+    load(0);
+    int c = 0;
+    for (; c + 2 <= mine; c += 2) {
+      load(1);
+      mul(0);
+      load(0);
       mul(1);
     }
+    if (c < mine) mul(0);
   }
   // the adapters: wave w takes slots w, w + NW, ... of every token
   if (a.adapter && a.lora[2].A && i16 < a.T) {
@@ -437,8 +429,11 @@ template <int DT, int EPL> hipError_t run(const FewTokens& a, hipStream_t s) {
                      up_lds(P, slots), s, a);
   if (a.adapter && a.lora[2].A)
     hipLaunchKernelGGL((few_rank_kernel<DT, EPL, true>), dim3(P, few_u_width(a.lora[2].r) / 4), dim3(256), 0, s, a);
-  hipLaunchKernelGGL((few_down_kernel<DT, 16>), dim3((a.d + 15) / 16), dim3(1024),
-                     (size_t)P * 4 + (size_t)slots * 34 + 64, s, a);
+  const size_t lds = (size_t)P * 4 + (size_t)slots * 34 + 64;
+  if (a.F % kFragElems<DT> == 0)
+    hipLaunchKernelGGL((few_down_kernel<DT, 16, true>), dim3((a.d + 15) / 16), dim3(1024), lds, s, a);
+  else
+    hipLaunchKernelGGL((few_down_kernel<DT, 16, false>), dim3((a.d + 15) / 16), dim3(1024), lds, s, a);
   return hipGetLastError();
 }
 

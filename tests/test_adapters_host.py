@@ -107,7 +107,7 @@ def _lora(cfg_over=None, backward=False, **over):
 @pytest.mark.parametrize("cfg", [
     dict(rows=-1), dict(rows=1 << 30), dict(E=0), dict(E=1025), dict(expert_begin=-1), dict(expert_begin=4),
     dict(expert_end=5), dict(K=0), dict(K=(1 << 20) + 1), dict(N=0), dict(N=(1 << 20) + 1), dict(dtype=3),
-    dict(dtype=-1),
+    dict(dtype=-1), dict(rows=1 << 22, K=1 << 18), dict(rows=1 << 22, N=1 << 18),
 ])
 def test_lora_refuses_shapes(cfg, backward):
     assert _lora(cfg, backward) == BAD
