@@ -47,7 +47,7 @@ int64_t elem_bytes(int32_t t) { return t == MOK_DTYPE_F32 ? 4 : 2; }
 bool bad_rank(int32_t r) { return r < 1 || r > kLoraMaxRank; }
 
 struct FewLayout {
-  size_t h, u[3], total;
+  size_t h, table, u[3], total;
 };
 mok_status few_layout(const mok_few_token_config* cfg, const mok_lora_weights* lora, FewLayout* o) {
   if (!cfg) return MOK_ERR_INVALID_ARG;
@@ -59,6 +59,7 @@ mok_status few_layout(const mok_few_token_config* cfg, const mok_lora_weights* l
   const int64_t P = (int64_t)c.T * c.k;
   Parts p;
   o->h = p.take(P * few_h_width(c.ffn) * elem_bytes(c.dtype));
+  o->table = p.take(P ? few_table_size(c.T, c.k, c.expert_end - c.expert_begin) : 0);
   for (int m = 0; m < 3; ++m) {
     o->u[m] = p.total;
     if (!lora) continue;
@@ -258,6 +259,7 @@ mok_status mok_few_token_layer(const void* x, const float* router_logits, const 
   a.idx = topk_idx;
   a.gate = topk_gate;
   a.h = (char*)workspace + l.h;
+  a.table = (char*)workspace + l.table;
   bool any = false;
   for (int m = 0; m < 3 && lora; ++m) {
     if (!aligned16(lora[m].A) || !aligned16(lora[m].B) || !aligned16(lora[m].scale)) return MOK_ERR_INVALID_ARG;

@@ -26,18 +26,20 @@ struct FewTokens {
   void* out;
   int32_t* idx;
   float* gate;
-  void* h;      // [T k, Fp] gate * silu(a) * b, zeros in columns [F, Fp)
+  void* h;      // [T k, Fp] gate * silu(a) * b, in columns [0, F)
+  void* table;  // few_table_size bytes: the chosen experts and their pairs
   float* u[3];  // [T k, rp] scale * A v of each pair, zeros past r
   FewLora lora[3];
   const int32_t* adapter;  // [T], NULL: no adapters
   int T, d, F, Fp, E, eb, E_loc, k, L, dtype, gating;
 };
 
-// Width of an h row: whole K steps of the matrix instruction.
+// Width of an h row: whole 16-byte loads.
 inline int few_h_width(int F) { return (F + 31) / 32 * 32; }
 // Width of a u row: whole 16-byte loads.
 __host__ __device__ inline int few_u_width(int r) { return (r + 7) / 8 * 8; }
 
+size_t few_table_size(int T, int k, int E_loc);
 hipError_t launch_few_tokens(const FewTokens& a, hipStream_t s);
 
 }  // namespace mok

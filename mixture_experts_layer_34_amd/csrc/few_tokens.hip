@@ -1,6 +1,6 @@
 // The whole expert layer for a few tokens (a decode step of up to sixteen
 // sequences) in two launches, four with adapters:
-//   route   e_1..e_k of token t: its k largest logits, gates g_j (route_token)
+//   route   e_1..e_k of token t: its k largest logits, gates g_j
 //   UP      h_p = g_j silu(W1_e x_t) * (W3_e x_t)      of each pair p = (t, j)
 //   DOWN    out_t = sum_j W2_e h_p
 // and, where adapter l of token t stands beside the expert's matrices, W + s_l
@@ -25,7 +25,6 @@
 #include "few_tokens.h"
 #include "frag.h"
 #include "mok_internal.h"
-#include "route_token.h"
 
 namespace mok {
 namespace {
@@ -74,20 +73,99 @@ __device__ __forceinline__ void build_slots(const FewTokens& a, FewTables& s, ui
   s.nslots = __builtin_amdgcn_readfirstlane(base[32]);
 }
 
-// Routing of tokens t0, t0 + step, ... by the calling wave, into LDS.
+// The tables as UP leaves them for DOWN: a word for their number, then the experts
+// and the pairs of all `most` slots.
+__host__ __device__ inline size_t few_table_bytes(int most) { return 16 + (size_t)(most + 1) / 2 * 4 + (size_t)most * 32; }
+__device__ __forceinline__ int16_t* table_pairs(void* table, int most) {
+  return reinterpret_cast<int16_t*>((char*)table + 16 + (size_t)(most + 1) / 2 * 4);
+}
+
+// Maximum of an unsigned word over a wave, in a scalar register.
+template <int CTRL> __device__ __forceinline__ uint32_t dpp_max_u32(uint32_t v) {
+  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
+  return o > v ? o : v;
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = dpp_max_u32<0xb1>(v);   // quad_perm [1,0,3,2]
+  v = dpp_max_u32<0x4e>(v);   // quad_perm [2,3,0,1]
+  v = dpp_max_u32<0x124>(v);  // row_ror 4
+  v = dpp_max_u32<0x128>(v);  // row_ror 8
+  v = dpp_max_u32<0x142>(v);  // row_bcast 15
+  v = dpp_max_u32<0x143>(v);  // row_bcast 31
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// Routing of tokens t0, t0 + step, ... below t1 by the calling wave: the layer's own
+// (route_token.h), bit for bit, in fewer steps, for every workgroup does it
+// before it can ask for a weight (one token of 128 experts, k 8: 3.4 -> 1.3 us).
+// A round takes the largest word of the order-preserving code, six lane moves,
+// and the lowest expert that holds it by ballots; the gates are computed once, by
+// lane j for the j-th choice.
 template <int EPL>
-__device__ __forceinline__ void route_few(const FewTokens& a, int t0, int t1, int step, int32_t* idx, float* gate,
-                                          int32_t* idx2, float* gate2, float* lse, float* graw) {
+__device__ __forceinline__ void route_few(const FewTokens& a, int t0, int t1, int step, int32_t* idx, float* gate) {
+  const int lane = lane_id(), E = a.E, k = a.k;
+  float next[EPL];
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = lane + 64 * i;
+      next[i] = t < t1 && e < E ? a.logits[(int64_t)t * E + e] : -INFINITY;
+    }
+  };
+  fetch(t0);
   for (int t = t0; t < t1; t += step) {
-    const float* row = a.logits + (int64_t)t * a.E;
-    if (a.gating == 0)
-      route_token<EPL, false, false>(row, t, a.E, a.k, idx, gate, idx2, gate2, lse, nullptr, graw);
-    else if (a.gating == kFewSigmoid)
-      route_token<EPL, true, false>(row, t, a.E, a.k, idx, gate, idx2, gate2, lse, nullptr, graw);
-    else if (a.gating == kFewRenorm)
-      route_token<EPL, false, true>(row, t, a.E, a.k, idx, gate, idx2, gate2, lse, nullptr, graw);
-    else
-      route_token<EPL, true, true>(row, t, a.E, a.k, idx, gate, idx2, gate2, lse, nullptr, graw);
+    float v[EPL];
+    uint32_t code[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      v[i] = next[i] != next[i] ? -INFINITY : next[i];  // a NaN ranks as -inf
+      uint32_t u = __float_as_uint(v[i]);
+      if ((u << 1) == 0) u = 0;  // -0 ties with +0
+      code[i] = lane + 64 * i < E ? ((u & 0x80000000u) ? ~u : (u | 0x80000000u)) : 0u;
+    }
+    fetch(t + step);
+    int mine = 0;        // lane j: the j-th choice and its logit
+    float logit = 0.f, m = 0.f;
+    for (int j = 0; j < k; ++j) {
+      uint32_t best = code[0];
+#pragma unroll
+      for (int i = 1; i < EPL; ++i) best = code[i] > best ? code[i] : best;
+      best = wave_max_u32(best);
+      int e = 0;
+#pragma unroll
+      for (int i = EPL - 1; i >= 0; --i) {  // the lowest index is looked for last, and stays
+        const uint64_t at = __ballot(code[i] == best);
+        e = at ? 64 * i + __ffsll((unsigned long long)at) - 1 : e;
+      }
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (lane + 64 * i == e) code[i] = 0u;
+      const float bv = __uint_as_float((best & 0x80000000u) ? (best & 0x7FFFFFFFu) : ~best);
+      if (j == 0) m = bv;
+      mine = lane == j ? e : mine;
+      logit = lane == j ? bv : logit;
+    }
+    // a choice's gate is top * inv; the products enter the sum of a renormalised
+    // row unrounded, as they do in the layer's router
+    float top = 1.0f / (1.0f + expf(-logit)), inv = 1.0f;
+    if (!(a.gating & kFewSigmoid)) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (lane + 64 * i < E) s += expf(v[i] - m);
+      top = expf(logit - m);
+      inv = 1.0f / wave_sum(s);
+    }
+    float g = top * inv;
+    if (a.gating & kFewRenorm) {
+      float sum = 0.f;
+      for (int j = 0; j < k; ++j) sum = fmaf(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(top), j)), inv, sum);
+      g /= sum;
+    }
+    if (lane < k) {
+      idx[t * k + lane] = mine;
+      gate[t * k + lane] = g;
+    }
   }
 }
 
@@ -113,11 +191,8 @@ template <int DT> __device__ __forceinline__ float rank_dot(const char* b, const
   return s;
 }
 
-// LDS of UP: idx, gate and the copies route_token writes [P] each, the waves'
-// raw gates, then the tables.
-__host__ __device__ inline size_t up_lds(int P, int slots) {
-  return (size_t)P * 16 + kUpWaves * kFewSlots * 4 + (size_t)slots * 34 + 64;
-}
+// LDS of UP: idx and gate [P] each, then the tables.
+__host__ __device__ inline size_t up_lds(int P, int slots) { return (size_t)P * 8 + (size_t)slots * 34 + 64; }
 
 template <int DT, int EPL>
 __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
@@ -127,18 +202,15 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
   __shared__ f32x4_t red[2][kUpWaves - 1][2][64];
   __shared__ uint32_t bits[32];
   __shared__ int base[33];
-  __shared__ float lse[16];
   const int tid = threadIdx.x, lane = tid & 63, w = wave_id();
   const int i16 = lane & 15, g = lane >> 4;
   const int P = a.T * a.k, most = few_slots(P, a.E_loc);
   FewTables s;
   s.idx = reinterpret_cast<int32_t*>(lds);
   s.gate = reinterpret_cast<float*>(lds + 4 * P);
-  float* graw = reinterpret_cast<float*>(lds + 16 * P) + w * kFewSlots;
-  s.pair = reinterpret_cast<int16_t*>(lds + 16 * P + kUpWaves * kFewSlots * 4);
+  s.pair = reinterpret_cast<int16_t*>(lds + 8 * P);
   s.expert = s.pair + 16 * most;
-  route_few<EPL>(a, w, a.T, kUpWaves, s.idx, s.gate, reinterpret_cast<int32_t*>(lds + 8 * P),
-                 reinterpret_cast<float*>(lds + 12 * P), lse, graw);
+  route_few<EPL>(a, w, a.T, kUpWaves, s.idx, s.gate);
   __syncthreads();
   if (blockIdx.x == 0)
     for (int p = tid; p < P; p += 64 * kUpWaves) {
@@ -146,36 +218,81 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
       a.gate[p] = s.gate[p];
     }
   build_slots(a, s, bits, base, 64 * kUpWaves);
+  if (blockIdx.x == 0) {
+    if (tid == 0) *reinterpret_cast<int32_t*>(a.table) = s.nslots;
+    for (int i = tid; i < s.nslots; i += 64 * kUpWaves) reinterpret_cast<int16_t*>((char*)a.table + 16)[i] = s.expert[i];
+    for (int i = tid; i < s.nslots * 8; i += 64 * kUpWaves)
+      reinterpret_cast<uint32_t*>(table_pairs(a.table, most))[i] = reinterpret_cast<const uint32_t*>(s.pair)[i];
+  }
 
-  const int ntn = a.Fp / 16, total = s.nslots * ntn;
+  // Columns of h: those of all slots one after the other, in tiles of up to
+  // sixteen that the workgroups take in turn.  A compute unit with more to read
+  // than another ends later by as much (they get even shares of the memory's rate),
+  // so the tiles are as wide as makes every workgroup take the same number of them.
+  const int64_t total = (int64_t)s.nslots * a.F;
+  int64_t n = (total + 15) / 16;
+  n = (n + kNumCUs - 1) / kNumCUs * kNumCUs;
+  if (n > gridDim.x) n = gridDim.x;
+  if (blockIdx.x >= n || total == 0) return;
+  const int64_t tiles = ((total + 15) / 16 + n - 1) / n * n;
+  int64_t tile = blockIdx.x, pos = total * tile / tiles, end = total * (tile + 1) / tiles;
   const int full = a.d / STEP;                                    // whole K steps
   const int all = full / U;                                      // whole chunks: the waves take them in turn
   const int chunks = all > w ? (all - w + kUpWaves - 1) / kUpWaves : 0;
   const int64_t row_bytes = (int64_t)a.d * S;
-  int flip = 0;
-  for (int un = blockIdx.x; un < total; un += gridDim.x, flip ^= 1) {
-    const int slot = un / ntn, n0 = (un - slot * ntn) * 16;
-    const int e = __builtin_amdgcn_readfirstlane(s.expert[slot]);
-    const int pair = s.pair[slot * 16 + i16];
-    const uint64_t has = __ballot(pair >= 0);
-    const int tx = pair >= 0 ? i16 : __ffsll((unsigned long long)has) - 1;  // a token that has the expert
-    const int n = n0 + i16 < a.F ? n0 + i16 : a.F - 1;
-    const int64_t at = ((int64_t)e * a.F + n) * row_bytes + (int64_t)(g * KE) * S;
-    const char* p1 = (const char*)a.w[0] + at;
-    const char* p3 = (const char*)a.w[1] + at;
-    const char* px = (const char*)a.x + tx * row_bytes + (int64_t)(g * KE) * S;
-    f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    u32x4_t q1[2][U], q3[2][U], qx[2][U];
-    auto load = [&](int buf, int c) {
+  // A tile, or its part of one expert.  A lane's row of W1 and W3, and
+  // its token's row of x (of a token that has the expert, for those that have not).
+  struct Tile {
+    int n0, cols, e, pair;
+    const char *p1, *p3, *px;
+  };
+  auto open = [&](int64_t at) {
+    Tile t;
+    const int slot = (int)(at / a.F);
+    t.n0 = (int)(at - (int64_t)slot * a.F);
+    t.cols = a.F - t.n0 < 16 ? a.F - t.n0 : 16;
+    t.cols = end - at < t.cols ? (int)(end - at) : t.cols;
+    t.e = __builtin_amdgcn_readfirstlane(s.expert[slot]);
+    t.pair = s.pair[slot * 16 + i16];
+    const uint64_t has = __ballot(t.pair >= 0);
+    const int tx = t.pair >= 0 ? i16 : __ffsll((unsigned long long)has) - 1;
+    const int n = t.n0 + (i16 < t.cols ? i16 : t.cols - 1);
+    const int64_t row = ((int64_t)t.e * a.F + n) * row_bytes + (int64_t)(g * KE) * S;
+    t.p1 = (const char*)a.w[0] + row;
+    t.p3 = (const char*)a.w[1] + row;
+    t.px = (const char*)a.x + tx * row_bytes + (int64_t)(g * KE) * S;
+    return t;
+  };
+  u32x4_t q1[2][U], q3[2][U], qx[2][U];
+  auto load = [&](int buf, const char* p1, const char* p3, const char* px, int c) {
 #pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int o = (c + j) * STEP * S;
-        q1[buf][j] = load16<DT>(p1 + o);
-        q3[buf][j] = load16<DT>(p3 + o);
-        qx[buf][j] = load16<DT>(px + o);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    };
+    for (int j = 0; j < U; ++j) {
+      const int o = ((c * kUpWaves + w) * U + j) * STEP * S;
+      q1[buf][j] = load16<DT>(p1 + o);
+      q3[buf][j] = load16<DT>(p3 + o);
+      qx[buf][j] = load16<DT>(px + o);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // the columns behind: of the same tile, or of the next that has any
+  auto step = [&](int by) {
+    pos += by;
+    while (pos >= end && (tile += n) < tiles) {
+      pos = total * tile / tiles;
+      end = total * (tile + 1) / tiles;
+    }
+    return pos < end;
+  };
+  if (!step(0)) return;
+  Tile t = open(pos);
+  if (chunks) load(0, t.p1, t.p3, t.px, 0);
+  bool more = true;
+  for (int flip = 0; more; flip ^= 1) {
+    more = step(t.cols);
+    const Tile next = more ? open(pos) : t;
+    const int n0 = t.n0, cols = t.cols, e = t.e, pair = t.pair;
+    const char *p1 = t.p1, *p3 = t.p3, *px = t.px;
+    f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     auto mul = [&](int buf) {
 #pragma unroll
       for (int j = 0; j < U; ++j) {
@@ -184,20 +301,18 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
       }
       __builtin_amdgcn_sched_barrier(0);
     };
-    // Chunk c + 1 is in flight while chunk c is multiplied.  No load stands under
-    // a condition (the last one is asked for again): behind a branch the compiler
-    // can only wait for every load, and the ring would run empty at each turn.
-    // And it may not move loads to their uses, where they save it registers.
-    if (chunks) {
-      load(0, w * U);
-      int c = 0;
-      for (; c + 2 <= chunks; c += 2) {
-        load(1, ((c + 1) * kUpWaves + w) * U);
-        mul(0);
-        load(0, ((c + 2 < chunks ? c + 2 : chunks - 1) * kUpWaves + w) * U);
-        mul(1);
-      }
-      if (c < chunks) mul(0);
+    // Chunk c + 1 is in flight while chunk c is multiplied, and the next tile's
+    // first chunk while this one's last is, and through what ends the tile.  No
+    // load stands under a condition (where there is none to ask for, one is asked
+    // for again): behind a branch the compiler can only wait for every load, and
+    // the ring would run empty at each turn.  And it may not move loads to their
+    // uses, where they save it registers.
+    for (int c = 0; c < chunks; c += 2) {
+      load(1, p1, p3, px, c + 1 < chunks ? c + 1 : c);
+      mul(0);
+      const bool here = c + 2 < chunks;
+      load(0, here ? p1 : next.p1, here ? p3 : next.p3, here ? px : next.px, here ? c + 2 : 0);
+      if (c + 1 < chunks) mul(1);
     }
     // the steps that fill no chunk, a wave each, and the step that d ends in
     for (int i = all * U; i < full; ++i)
@@ -216,7 +331,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
     const int l = a.adapter && pair >= 0 ? adapter_of(a, i16) : -1;
     if (l >= 0) {  // wave w adds the adapter's share of row 4 g + w of the tile
       const int nr = n0 + 4 * g + w;
-      if (nr < a.F)
+      if (4 * g + w < cols)
 #pragma unroll
         for (int m = 0; m < 2; ++m)
           if (a.lora[m].A) {
@@ -243,79 +358,94 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
       }
       if (pair >= 0) {
         const float gt = s.gate[pair];
-        float hv[4];
+        const int64_t ho = (int64_t)pair * a.Fp + n0 + 4 * g;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float va = acc[0][i];
-          hv[i] = n0 + 4 * g + i < a.F ? va * sigmoidf_(va) * acc[1][i] * gt : 0.f;
+          const float va = acc[0][i], hv = va * sigmoidf_(va) * acc[1][i] * gt;
+          if (4 * g + i < cols) {
+            if constexpr (DT == 0) reinterpret_cast<float*>(a.h)[ho + i] = hv;
+            else reinterpret_cast<uint16_t*>(a.h)[ho + i] = (uint16_t)Elem<DT>::pack(hv, 0.f);
+          }
         }
-        char* hp = (char*)a.h + ((int64_t)pair * a.Fp + n0 + 4 * g) * S;
-        if constexpr (DT == 0)
-          *reinterpret_cast<f32x4_t*>(hp) = f32x4_t{hv[0], hv[1], hv[2], hv[3]};
-        else
-          *reinterpret_cast<u32x2_t*>(hp) = u32x2_t{Elem<DT>::pack(hv[0], hv[1]), Elem<DT>::pack(hv[2], hv[3])};
       }
     }
+    t = next;
   }
 #endif
 }
 
-template <int DT, int NW, bool WHOLE>
-__global__ __launch_bounds__(64 * NW) void few_down_kernel(FewTokens a) {
+// A workgroup owns `cols` columns of out, up to 16 NT: as many as give every
+// compute unit the same share.
+constexpr int kDownWaves = 16;
+template <int DT, int NT, bool WHOLE>
+__global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, int cols) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int KE = kFragElems<DT>, STEP = kFragStep<DT>, S = Elem<DT>::kBytes, U = kUnroll;
+  constexpr int KE = kFragElems<DT>, STEP = kFragStep<DT>, S = Elem<DT>::kBytes, U = kUnroll, NW = kDownWaves;
   extern __shared__ __align__(16) char lds[];
-  __shared__ f32x4_t red[NW][64];
-  __shared__ uint32_t bits[32];
-  __shared__ int base[33];
+  __shared__ f32x4_t red[NW][NT][64];
   const int tid = threadIdx.x, lane = tid & 63, w = wave_id();
   const int i16 = lane & 15, g = lane >> 4;
   const int P = a.T * a.k, most = few_slots(P, a.E_loc);
-  FewTables s;
-  s.idx = reinterpret_cast<int32_t*>(lds);
-  s.pair = reinterpret_cast<int16_t*>(lds + 4 * P);
-  s.expert = s.pair + 16 * most;
-  for (int p = tid; p < P; p += 64 * NW) s.idx[p] = a.idx[p];
+  int16_t *s_pair = reinterpret_cast<int16_t*>(lds), *s_expert = s_pair + 16 * most;
+  const int nslots = *reinterpret_cast<const int32_t*>(a.table);
+  for (int i = tid; i < most * 8; i += 64 * NW)
+    reinterpret_cast<uint32_t*>(s_pair)[i] = reinterpret_cast<const uint32_t*>(table_pairs(a.table, most))[i];
+  for (int i = tid; i < most; i += 64 * NW) s_expert[i] = reinterpret_cast<const int16_t*>((const char*)a.table + 16)[i];
   __syncthreads();
-  build_slots(a, s, bits, base, 64 * NW);
 
-  const int n0 = blockIdx.x * 16;
-  const int n = n0 + i16 < a.d ? n0 + i16 : a.d - 1;
+  const int n0 = blockIdx.x * cols, n1 = n0 + cols < a.d ? n0 + cols : a.d;
   const int64_t row_bytes = (int64_t)a.F * S;
+  int64_t wrow[NT];  // the lane's rows of W2, in bytes from the expert's first
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    const int n = n0 + 16 * q + i16;
+    wrow[q] = (n < n1 ? n : n1 - 1) * row_bytes;
+  }
   const int chunks = (a.F + STEP * U - 1) / (STEP * U);  // of one expert
-  const int all = s.nslots * chunks;  // the waves take them in turn: what they read at a time is neighbouring
+  const int all = nslots * chunks;  // the waves take them in turn: what they read at a time is neighbouring
   const int mine = all > w ? (all - w + NW - 1) / NW : 0;
   const auto hrs = __builtin_amdgcn_make_buffer_rsrc(a.h, (short)0, (int)((int64_t)P * a.Fp * S), 0x00020000);
   // cursor of the next chunk to load; past the last one it stays on it
   const int skip_slots = NW / chunks, skip = NW - skip_slots * chunks;
   int slot = w / chunks, ch = w - slot * chunks;
-  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  u32x4_t qw[2][U], qh[2][U];
+  f32x4_t acc[NT];
+#pragma unroll
+  for (int q = 0; q < NT; ++q) acc[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  u32x4_t qw[2][U][NT], qh[2][U];
+  int left[2];  // !WHOLE: elements of F from the lane's first of the chunk
   // WHOLE: F is a multiple of KE, a lane's 16 bytes lie in F or past it; a
   // lane past it reads the row's first bytes and zeros of h.
   auto load = [&](int buf) {
-    const int e = __builtin_amdgcn_readfirstlane(s.expert[slot]);
-    const int pair = s.pair[slot * 16 + i16];
+    const int e = __builtin_amdgcn_readfirstlane(s_expert[slot]);
+    const int pair = s_pair[slot * 16 + i16];
     // a pair that is not: an offset past the buffer, which loads zeros
     const uint32_t hoff = pair >= 0 ? (uint32_t)(pair * a.Fp) * S : 0xC0000000u;
-    const char* wp = (const char*)a.w[2] + ((int64_t)e * a.d + n) * row_bytes;
+    const char* wp = (const char*)a.w[2] + (int64_t)e * a.d * row_bytes;
+    left[buf] = a.F - ch * U * STEP - g * KE;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int k = (ch * U + j) * STEP + g * KE;
-      if constexpr (WHOLE) qw[buf][j] = load16<DT>(wp + (k < a.F ? k : 0) * S);
-      else qw[buf][j] = load_part<DT>(wp + k * S, k < a.F ? a.F - k : 0);
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+        if constexpr (WHOLE) qw[buf][j][q] = load16<DT>(wp + wrow[q] + (k < a.F ? k : 0) * S);
+        else qw[buf][j][q] = load_part<DT>(wp + wrow[q] + k * S, k < a.F ? a.F - k : 0);
+      }
       const auto v = __builtin_amdgcn_raw_buffer_load_b128(hrs, k < a.F ? hoff + k * S : 0xC0000000u, 0, 0);
       qh[buf][j] = u32x4_t{(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
     }
     const bool wrap = ch + skip >= chunks;
     const int next = slot + skip_slots + wrap;
-    ch = next < s.nslots ? ch + skip - (wrap ? chunks : 0) : ch;
-    slot = next < s.nslots ? next : slot;
+    ch = next < nslots ? ch + skip - (wrap ? chunks : 0) : ch;
+    slot = next < nslots ? next : slot;
     __builtin_amdgcn_sched_barrier(0);
   };
   auto mul = [&](int buf) {
 #pragma unroll
-    for (int j = 0; j < U; ++j) acc = mma<DT>(qw[buf][j], qh[buf][j], acc);
+    for (int j = 0; j < U; ++j) {
+      if constexpr (!WHOLE) qh[buf][j] = first_elems<DT>(qh[buf][j], left[buf] - j * STEP);  // past F nothing was written
+#pragma unroll
+      for (int q = 0; q < NT; ++q) acc[q] = mma<DT>(qw[buf][j][q], qh[buf][j], acc[q]);
+    }
     __builtin_amdgcn_sched_barrier(0);
   };
   if (mine) {  // no load under a condition, as in UP
@@ -334,26 +464,31 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewTokens a) {
     const int l = adapter_of(a, i16), r = a.lora[2].r;
     if (l >= 0)
       for (int j = w; j < a.k; j += NW) {
-        const int p = i16 * a.k + j, el = s.idx[p] - a.eb;
+        const int p = i16 * a.k + j, el = a.idx[p] - a.eb;
         if (el < 0 || el >= a.E_loc) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n0 + 4 * g + i < a.d)
-            acc[i] += rank_dot<DT>((const char*)a.lora[2].B +
-                                       (((int64_t)l * a.E_loc + el) * a.d + n0 + 4 * g + i) * r * S,
-                                   a.u[2] + (int64_t)p * few_u_width(r), r);
+        for (int q = 0; q < NT; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int n = n0 + 16 * q + 4 * g + i;
+            if (n < n1)
+              acc[q][i] += rank_dot<DT>((const char*)a.lora[2].B + (((int64_t)l * a.E_loc + el) * a.d + n) * r * S,
+                                        a.u[2] + (int64_t)p * few_u_width(r), r);
+          }
       }
   }
-  red[w][lane] = acc;
-  __syncthreads();
-  if (w == 0 && i16 < a.T) {
-    f32x4_t v = red[0][lane];
 #pragma unroll
-    for (int q = 1; q < NW; ++q) v += red[q][lane];
-    const int64_t o = (int64_t)i16 * a.d + n0 + 4 * g;
+  for (int q = 0; q < NT; ++q) red[w][q][lane] = acc[q];
+  __syncthreads();
+  if (w < NT && i16 < a.T) {  // a wave for each sixteen columns
+    f32x4_t v = red[0][w][lane];
+#pragma unroll
+    for (int k = 1; k < NW; ++k) v += red[k][w][lane];
+    const int n = n0 + 16 * w + 4 * g;
+    const int64_t o = (int64_t)i16 * a.d + n;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (n0 + 4 * g + i < a.d) {
+      if (n + i < n1) {
         if constexpr (DT == 0) reinterpret_cast<float*>(a.out)[o + i] = v[i];
         else reinterpret_cast<uint16_t*>(a.out)[o + i] = (uint16_t)Elem<DT>::pack(v[i], 0.f);
       }
@@ -367,8 +502,8 @@ __global__ __launch_bounds__(64 * NW) void few_down_kernel(FewTokens a) {
 template <int DT, int EPL, bool DOWN> __global__ __launch_bounds__(256) void few_rank_kernel(FewTokens a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int KE = kFragElems<DT>, S = Elem<DT>::kBytes;
-  __shared__ int32_t idx[2][kFewSlots];
-  __shared__ float gate[2][kFewSlots], graw[kFewSlots], lse[1];
+  __shared__ int32_t idx[kFewSlots];
+  __shared__ float gate[kFewSlots];
   const int lane = lane_id(), w = wave_id();
   const int p = blockIdx.x, t = p / a.k, j = p - t * a.k;
   const int l = adapter_of(a, t);
@@ -383,10 +518,10 @@ template <int DT, int EPL, bool DOWN> __global__ __launch_bounds__(256) void few
     if (w == 0) {  // token t alone, as token 0 of its own row
       FewTokens one = a;
       one.logits = a.logits + (int64_t)t * a.E;
-      route_few<EPL>(one, 0, 1, 1, idx[0], gate[0], idx[1], gate[1], lse, graw);
+      route_few<EPL>(one, 0, 1, 1, idx, gate);
     }
     __syncthreads();
-    e = idx[0][j];
+    e = idx[j];
   }
   e -= a.eb;
   if (e < 0 || e >= a.E_loc) return;
@@ -410,6 +545,11 @@ template <int DT, int EPL, bool DOWN> __global__ __launch_bounds__(256) void few
 #endif
 }
 
+template <int DT, int NT, bool WHOLE> void down(const FewTokens& a, int cols, int slots, hipStream_t s) {
+  hipLaunchKernelGGL((few_down_kernel<DT, NT, WHOLE>), dim3((a.d + cols - 1) / cols), dim3(64 * kDownWaves),
+                     (size_t)slots * 34 + 64, s, a, cols);
+}
+
 template <int DT, int EPL> hipError_t run(const FewTokens& a, hipStream_t s) {
   const int P = a.T * a.k, slots = few_slots(P, a.E_loc);
   int ranks = 0;
@@ -424,16 +564,21 @@ template <int DT, int EPL> hipError_t run(const FewTokens& a, hipStream_t s) {
       n = 1;
     return n;
   }();
-  const int64_t units = (int64_t)slots * (a.Fp / 16), cap = (int64_t)kNumCUs * per_cu;
-  hipLaunchKernelGGL((few_up_kernel<DT, EPL>), dim3((unsigned)(units < cap ? units : cap)), dim3(64 * kUpWaves),
+  // as many workgroups as are resident at once, in whole rounds of the compute
+  // units; of those the kernel uses what the chosen experts' columns take
+  const int64_t units = ((int64_t)slots * a.F + 15) / 16, cap = (int64_t)kNumCUs * per_cu;
+  const int64_t rounds = (units + kNumCUs - 1) / kNumCUs * kNumCUs;
+  hipLaunchKernelGGL((few_up_kernel<DT, EPL>), dim3((unsigned)(rounds < cap ? rounds : cap)), dim3(64 * kUpWaves),
                      up_lds(P, slots), s, a);
   if (a.adapter && a.lora[2].A)
     hipLaunchKernelGGL((few_rank_kernel<DT, EPL, true>), dim3(P, few_u_width(a.lora[2].r) / 4), dim3(256), 0, s, a);
-  const size_t lds = (size_t)P * 4 + (size_t)slots * 34 + 64;
+  // columns of a workgroup of DOWN: d shared out evenly over the compute units,
+  // in as few rounds of them as 32 columns each allow
+  const int share = (a.d + 32 * kNumCUs - 1) / (32 * kNumCUs) * kNumCUs, cols = (a.d + share - 1) / share;
   if (a.F % kFragElems<DT> == 0)
-    hipLaunchKernelGGL((few_down_kernel<DT, 16, true>), dim3((a.d + 15) / 16), dim3(1024), lds, s, a);
+    cols <= 16 ? down<DT, 1, true>(a, cols, slots, s) : down<DT, 2, true>(a, cols, slots, s);
   else
-    hipLaunchKernelGGL((few_down_kernel<DT, 16, false>), dim3((a.d + 15) / 16), dim3(1024), lds, s, a);
+    cols <= 16 ? down<DT, 1, false>(a, cols, slots, s) : down<DT, 2, false>(a, cols, slots, s);
   return hipGetLastError();
 }
 
@@ -442,6 +587,8 @@ template <int DT> hipError_t run_e(const FewTokens& a, hipStream_t s) {
 }
 
 }  // namespace
+
+size_t few_table_size(int T, int k, int E_loc) { return few_table_bytes(few_slots(T * k, E_loc)); }
 
 hipError_t launch_few_tokens(const FewTokens& a, hipStream_t s) {
   return a.dtype == 0 ? run_e<0>(a, s) : a.dtype == 1 ? run_e<1>(a, s) : run_e<2>(a, s);

@@ -83,6 +83,17 @@ template <int DT> __device__ __forceinline__ void store_part(char* p, u32x4_t v,
     }
 }
 
+// v with zeros in place of the elements from the n-th on (n may be negative).
+template <int DT> __device__ __forceinline__ u32x4_t first_elems(u32x4_t v, int n) {
+  constexpr int PER = 4 / Elem<DT>::kBytes;  // elements of a dword
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (PER == 1) v[j] = j < n ? v[j] : 0u;
+    else v[j] = 2 * j + 1 < n ? v[j] : 2 * j < n ? v[j] & 0xFFFFu : 0u;
+  }
+  return v;
+}
+
 // KE elements as fp32 and back (rounded to nearest even).
 template <int DT> __device__ __forceinline__ void widen(u32x4_t v, float* f) {
   Vec<DT, kFragElems<DT>> e;

@@ -76,9 +76,10 @@ def test_few_token_workspace():
         c = dict(T=4, d=64, E=8, k=2, F=33, eb=0, ee=8, dtype=BF16, flags=0, L=3)
         c.update(over)
         return mok.mok_few_token_workspace_query(mok.few_token_config(*c.values()), lora)
-    assert size() == 1024                          # eight rows of h, 64 wide (33 padded to whole steps)
-    assert size(dtype=F32) == 2048 and size(T=0) == 0
-    assert size(_stacks((P[0], P[1], None, 9), (None, None, None, 0), (P[0], P[1], None, 8))) == 1024 + 512 + 256
+    # eight rows of h, 64 wide (33 padded), and the tables of eight experts: 16 + 8 * 34 bytes
+    assert size() == 1024 + 512
+    assert size(dtype=F32) == 2048 + 512 and size(T=0) == 0
+    assert size(_stacks((P[0], P[1], None, 9), (None, None, None, 0), (P[0], P[1], None, 8))) == 1536 + 512 + 256
     with pytest.raises(mok.MokError):
         size(T=17)
     assert mok.lib().mok_few_token_workspace_query(None, None, ctypes.byref(ctypes.c_size_t())) == BAD
