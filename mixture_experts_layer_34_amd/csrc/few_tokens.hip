@@ -29,7 +29,7 @@
 namespace mok {
 namespace {
 
-constexpr int kUpWaves = 4;  // waves that share the K of a unit of UP
+constexpr int kUpWaves = 8;  // waves that share the K of a tile of UP
 [[maybe_unused]] constexpr int kUnroll = 4;  // K steps of a chunk; one chunk is in flight while one is multiplied
 
 // Tables of a workgroup in LDS.
@@ -329,7 +329,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
       acc[1] = mma<DT>(load_part<DT>(p3 + o, left), vx, acc[1]);
     }
     const int l = a.adapter && pair >= 0 ? adapter_of(a, i16) : -1;
-    if (l >= 0) {  // wave w adds the adapter's share of row 4 g + w of the tile
+    if (l >= 0 && w < 4) {  // wave w adds the adapter's share of row 4 g + w of the tile
       const int nr = n0 + 4 * g + w;
       if (4 * g + w < cols)
 #pragma unroll
@@ -376,7 +376,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
 
 // A workgroup owns `cols` columns of out, up to 16 NT: as many as give every
 // compute unit the same share.
-constexpr int kDownWaves = 16;
+constexpr int kDownWaves = 8;
 template <int DT, int NT, bool WHOLE>
 __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, int cols) {
 #if defined(__HIP_DEVICE_COMPILE__)
