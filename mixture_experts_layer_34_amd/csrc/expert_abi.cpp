@@ -346,7 +346,7 @@ mok_status mok_lora_rows_backward(const void* dout, const void* x, const float* 
                                   c.dtype, l.splits, lora_width(w->r)}, s);
     if (e == hipSuccess)
       e = launch_lora_grad(LoraGrad{map, {x, dout}, {du, u}, {dA, dB}, {c.K, c.N}, w->scale, w->r, c.dtype,
-                                    l.grad.tile_rows, l.grad.part_bytes ? (float*)(ws + l.sums) : nullptr}, s);
+                                    l.grad.ranges, l.grad.part_bytes ? (float*)(ws + l.sums) : nullptr}, s);
   }
   return result(e);
 }

@@ -30,6 +30,7 @@ struct LoraRank {
   const void* A;   // [G, r, K]
   float* part;
   int K, r, dtype, splits;
+  int height, ranges;  // set by the launcher
 };
 
 // out_row = base_row + scale_g B_g (sum_s part[s][row]); the sum to u where that is given,
@@ -54,14 +55,14 @@ struct LoraGrad {
   int width[2];
   const float* scale;
   int r, dtype;
-  int tile_rows;  // lora_grad_plan
-  float* part;    // NULL where no group can have several tiles
+  int ranges;   // lora_grad_plan
+  float* part;  // NULL with one range
 };
 
-// Rows of a tile of the grad kernel, and the bytes that the sums of groups of
-// several tiles take (0 where no group can have several).
+// Ranges of rows that the grad kernel's workgroups take, and the bytes that the sums
+// of groups in several of them take.
 struct LoraGradPlan {
-  int tile_rows;
+  int ranges;
   int64_t part_bytes;
 };
 LoraGradPlan lora_grad_plan(int rows, int G, int r, int K, int N, int dtype);

@@ -29,36 +29,90 @@
 namespace mok {
 namespace {
 
-struct Tile {
-  int g, row0, row1;    // rows [row0, row1) of group g; g < 0: none
-  int first, row_first; // the group's first tile and row
-  int n;                // the group's tiles
-};
-
 __device__ __forceinline__ int cut(int v, int rows) { return v < 0 ? 0 : v > rows ? rows : v; }
 
-// The t-th tile of mt rows, the groups' tiles counted one after the other.
-__device__ __forceinline__ Tile find_tile(const LoraMap& m, int t, int mt) {
+// The groups' rows, shared out evenly in n ranges of `each` rows.  (A compute unit
+// with more rows than another ends later by as much: they get even shares of the
+// memory's rate.)  What a kernel reads before it can ask for its first row adds to
+// its time in full, so one load brings all offsets of up to 63 groups, a lane each.
+struct Rows {
+  int offset;  // of group `lane`, or the end of the last
+  int first, last, each;
+  __device__ __forceinline__ int begin(int i) const {
+    const int64_t at = first + (int64_t)each * i;
+    return at < last ? (int)at : last;
+  }
+  __device__ __forceinline__ int range_of(int row) const { return (row - first) / each; }
+};
+__device__ __forceinline__ Rows rows_of(const LoraMap& m, int n) {
+  Rows r;
+  const int lane = lane_id();
+  r.offset = m.offsets[lane < m.G ? lane : m.G];
+  r.first = cut(__builtin_amdgcn_readfirstlane(r.offset), m.rows);
+  r.last = cut(m.G < 64 ? __builtin_amdgcn_readlane(r.offset, m.G) : m.offsets[m.G], m.rows);
+  r.last = r.last > r.first ? r.last : r.first;
+  r.each = (r.last - r.first + n - 1) / n;
+  r.each = r.each > 0 ? r.each : 1;
+  return r;
+}
+
+// The rows of a range that are of one group: those from `row` on.
+struct Part {
+  int g, end;    // the group; the end of its rows in the range
+  int lo, hi;    // all of the group's rows
+};
+__device__ __forceinline__ Part part_at(const LoraMap& m, const Rows& rows, int row, int end) {
+  const int lane = lane_id();
+  int g, lo, hi;
+  // the offsets behind the first that are at or before row
+  if (m.G < 64) {
+    g = __popcll(__ballot(lane > 0 && lane < m.G && rows.offset <= row));
+    lo = __builtin_amdgcn_readlane(rows.offset, g);
+    hi = __builtin_amdgcn_readlane(rows.offset, g + 1);
+  } else {
+    g = 0;
+#pragma unroll 4
+    for (int g0 = 1; g0 < m.G; g0 += 64) {
+      const int at = g0 + lane;
+      g += __popcll(__ballot(at < m.G && m.offsets[at < m.G ? at : 0] <= row));
+    }
+    g = __builtin_amdgcn_readfirstlane(g);
+    lo = m.offsets[g];
+    hi = m.offsets[g + 1];
+  }
+  lo = cut(lo, m.rows);
+  hi = cut(hi, m.rows);
+  const int e = hi < end ? hi : end;
+  return Part{g, e > row ? e : row + 1, lo, hi};  // (offsets that fall: a row at a time)
+}
+
+// The t-th tile of `height` rows of one group, the groups' tiles counted one after
+// the other; g < 0: none.
+__device__ __forceinline__ Part find_tile(const LoraMap& m, int t, int height, int* row0) {
   const int lane = lane_id();
   int before = 0;
   for (int g0 = 0; g0 < m.G; g0 += 64) {
     const int g = g0 + lane;
-    const int lo = cut(m.offsets[g < m.G ? g : m.G], m.rows);
-    const int hi = cut(m.offsets[g < m.G ? g + 1 : m.G], m.rows);
-    const int n = hi > lo ? (hi - lo + mt - 1) / mt : 0;
+    const int lo = cut(m.offsets[g < m.G ? g : m.G], m.rows), hi = cut(m.offsets[g < m.G ? g + 1 : m.G], m.rows);
+    const int n = hi > lo ? (int)((unsigned)(hi - lo + height - 1) / (unsigned)height) : 0;
     const int to = wave_prefix(n) + before;
     const uint64_t hit = __ballot(t >= to - n && t < to);
     if (hit) {
       const int l = __ffsll((unsigned long long)hit) - 1;
-      const int num = __builtin_amdgcn_readlane(n, l), first = __builtin_amdgcn_readlane(to, l) - num,
-                a = __builtin_amdgcn_readlane(lo, l), b = __builtin_amdgcn_readlane(hi, l);
-      const int row0 = a + (t - first) * mt;
-      return Tile{g0 + l, row0, row0 + mt < b ? row0 + mt : b, first, a, num};
+      const int first = __builtin_amdgcn_readlane(to - n, l);
+      const int a = __builtin_amdgcn_readlane(lo, l), b = __builtin_amdgcn_readlane(hi, l);
+      *row0 = a + (t - first) * height;
+      return Part{g0 + l, *row0 + height < b ? *row0 + height : b, a, b};
     }
     before = __builtin_amdgcn_readlane(to, 63);
   }
-  return Tile{-1, 0, 0, 0, 0, 0};
+  return Part{-1, 0, 0, 0};
 }
+
+// Workgroup b of n (a multiple of 8) on XCD b % 8: its place in the order in which
+// every XCD has an eighth of the rows, so that a group's A or B comes to one or
+// two of the eight L2s.
+__device__ __forceinline__ int by_xcd(int b, int n) { return (b & 7) * (n >> 3) + (b >> 3); }
 
 // The token of a sorted row; -1: none.  No branch, so that several are in flight
 // at once: without a map a word of the offsets is read in its place.
@@ -73,305 +127,352 @@ __device__ __forceinline__ int token_of(const LoraMap& m, int row) { return toke
 // ------------------------------------------------------------------ rank
 constexpr int kRankWaves = 4;
 
+// grid: (tiles of a.height rows of one group, or ranges of rows, in eights; shares of K)
 template <int DT, int RT, int M> __global__ __launch_bounds__(64 * kRankWaves) void lora_rank_kernel(LoraRank a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int KE = kFragElems<DT>, STEP = kFragStep<DT>, S = Elem<DT>::kBytes;
-  constexpr int U = RT >= 4 ? 1 : RT == 2 || M == 4 ? 2 : 4;  // K steps of a chunk
+  constexpr int U = RT >= 4 ? 1 : RT == 2 || M > 2 ? 2 : 4;  // K steps of a chunk
   __shared__ f32x4_t red[kRankWaves - 1][M][RT][64];
   const int lane = lane_id(), w = wave_id(), i16 = lane & 15, g4 = lane >> 4;
-  const Tile t = find_tile(a.map, blockIdx.x, 16 * M);
-  if (t.g < 0) return;
   const int full = a.K / STEP, steps = (a.K + STEP - 1) / STEP;
   // this workgroup's K steps, [s0, s1): its waves take chunks in turn, so that
   // what they read at a time is neighbouring
   const int s0 = (int)((int64_t)steps * blockIdx.y / a.splits), s1 = (int)((int64_t)steps * (blockIdx.y + 1) / a.splits);
   const int ns = (s1 < full ? s1 : full) - s0;  // whole steps
   const int64_t at = (int64_t)(s0 * STEP + g4 * KE) * S;
-  const char *px[M], *pa[RT];
-  int tok[M];
-#pragma unroll
-  for (int m = 0; m < M; ++m) {
-    const int row = t.row0 + 16 * m + i16;
-    tok[m] = token_of(a.map, row < t.row1 ? row : t.row1 - 1);
-    px[m] = (const char*)a.in + (int64_t)(tok[m] < 0 ? 0 : tok[m]) * a.K * S + at;
+  const int place = by_xcd(blockIdx.x, gridDim.x);
+  Rows rows{};
+  Part t{0, 0, 0, 0};
+  int row0, end;
+  if (a.height) {
+    t = find_tile(a.map, place, a.height, &row0);
+    if (t.g < 0) return;
+    end = t.end;
+  } else {
+    if (place >= a.ranges) return;
+    rows = rows_of(a.map, a.ranges);
+    row0 = rows.begin(place);
+    end = rows.begin(place + 1);
   }
+  for (; row0 < end; row0 += 16 * M) {
+    if (row0 >= t.end) t = part_at(a.map, rows, row0, end);
+    const int row1 = row0 + 16 * M < t.end ? row0 + 16 * M : t.end;
+    const char *px[M], *pa[RT];
+    int word[M], tok[M];
 #pragma unroll
-  for (int q = 0; q < RT; ++q) {
-    const int rr = 16 * q + i16 < a.r ? 16 * q + i16 : a.r - 1;
-    pa[q] = (const char*)a.A + ((int64_t)t.g * a.r + rr) * a.K * S + at;
-  }
-  f32x4_t acc[M][RT];
-#pragma unroll
-  for (int m = 0; m < M; ++m)
-#pragma unroll
-    for (int q = 0; q < RT; ++q) acc[m][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  u32x4_t qx[2][U][M], qa[2][U][RT];
-  auto load = [&](int buf, int j, int step) {
-    const int o = step * STEP * S;
-#pragma unroll
-    for (int m = 0; m < M; ++m) qx[buf][j][m] = load16<DT>(px[m] + o);
-#pragma unroll
-    for (int q = 0; q < RT; ++q) qa[buf][j][q] = load16<DT>(pa[q] + o);
-  };
-  auto mul = [&](int buf, int j) {
-#pragma unroll
-    for (int m = 0; m < M; ++m)
-#pragma unroll
-      for (int q = 0; q < RT; ++q) acc[m][q] = mma<DT>(qa[buf][j][q], qx[buf][j][m], acc[m][q]);
-  };
-  // Chunk c + 1 is in flight while chunk c is multiplied.  No load stands under a
-  // condition (the last one is asked for again): behind a branch the compiler
-  // can only wait for every load, and the ring would run empty at each turn.  And
-  // it may not move loads to their uses, where they save it registers.
-  const int all = ns / U, chunks = all > w ? (all - w + kRankWaves - 1) / kRankWaves : 0;
-  auto load_chunk = [&](int buf, int c) {
-#pragma unroll
-    for (int j = 0; j < U; ++j) load(buf, j, (c * kRankWaves + w) * U + j);
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  auto mul_chunk = [&](int buf) {
-#pragma unroll
-    for (int j = 0; j < U; ++j) mul(buf, j);
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  if (chunks) {
-    load_chunk(0, 0);
-    int c = 0;
-    for (; c + 2 <= chunks; c += 2) {
-      load_chunk(1, c + 1);
-      mul_chunk(0);
-      load_chunk(0, c + 2 < chunks ? c + 2 : chunks - 1);
-      mul_chunk(1);
+    for (int m = 0; m < M; ++m) {
+      const int row = row0 + 16 * m + i16;
+      word[m] = token_word(a.map, row < row1 ? row : row1 - 1);
     }
-    if (c < chunks) mul_chunk(0);
-  }
-  // the steps that fill no chunk, a wave each, and the step that K ends in
-  for (int i = all * U; i < ns; ++i)
-    if (i % kRankWaves == w) {
-      load(0, 0, i);
-      mul(0, 0);
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const int row = row0 + 16 * m + i16;
+      tok[m] = token_in(a.map, row < row1 ? row : row1 - 1, word[m]);
+      px[m] = (const char*)a.in + (int64_t)(tok[m] < 0 ? 0 : tok[m]) * a.K * S + at;
     }
-  if (s1 > full && w == 0) {
-    const int left = a.K - full * STEP - g4 * KE, o = (full - s0) * STEP * S;
-#pragma unroll
-    for (int m = 0; m < M; ++m) qx[0][0][m] = load_part<DT>(px[m] + o, left);
-#pragma unroll
-    for (int q = 0; q < RT; ++q) qa[0][0][q] = load_part<DT>(pa[q] + o, left);
-    mul(0, 0);
-  }
-  if (w > 0)
-#pragma unroll
-    for (int m = 0; m < M; ++m)
-#pragma unroll
-      for (int q = 0; q < RT; ++q) red[w - 1][m][q][lane] = acc[m][q];
-  __syncthreads();
-  if (w > 0) return;
-#pragma unroll
-  for (int m = 0; m < M; ++m) {
-    const int row = t.row0 + 16 * m + i16;
-    if (row >= t.row1) continue;
-    float* to = a.part + ((int64_t)blockIdx.y * a.map.rows + row) * (16 * RT);
 #pragma unroll
     for (int q = 0; q < RT; ++q) {
-      f32x4_t v = acc[m][q];
-#pragma unroll
-      for (int k = 0; k < kRankWaves - 1; ++k) v += red[k][m][q][lane];
-      const int r0 = 16 * q + 4 * g4;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = tok[m] < 0 || r0 + i >= a.r ? 0.f : v[i];
-      *reinterpret_cast<f32x4_t*>(to + r0) = v;
+      const int rr = 16 * q + i16 < a.r ? 16 * q + i16 : a.r - 1;
+      pa[q] = (const char*)a.A + ((int64_t)t.g * a.r + rr) * a.K * S + at;
     }
+    f32x4_t acc[M][RT];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int q = 0; q < RT; ++q) acc[m][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    u32x4_t qx[2][U][M], qa[2][U][RT];
+    auto load = [&](int buf, int j, int step) {
+      const int o = step * STEP * S;
+#pragma unroll
+      for (int m = 0; m < M; ++m) qx[buf][j][m] = load16<DT>(px[m] + o);
+#pragma unroll
+      for (int q = 0; q < RT; ++q) qa[buf][j][q] = load16<DT>(pa[q] + o);
+    };
+    auto mul = [&](int buf, int j) {
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int q = 0; q < RT; ++q) acc[m][q] = mma<DT>(qa[buf][j][q], qx[buf][j][m], acc[m][q]);
+    };
+    // Chunk c + 1 is in flight while chunk c is multiplied.  No load stands under a
+    // condition (the last one is asked for again): behind a branch the compiler
+    // can only wait for every load, and the ring would run empty at each turn.  And
+    // it may not move loads to their uses, where they save it registers.
+    const int all = ns / U, chunks = all > w ? (all - w + kRankWaves - 1) / kRankWaves : 0;
+    auto load_chunk = [&](int buf, int c) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) load(buf, j, (c * kRankWaves + w) * U + j);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto mul_chunk = [&](int buf) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) mul(buf, j);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    if (chunks) {
+      load_chunk(0, 0);
+      int c = 0;
+      for (; c + 2 <= chunks; c += 2) {
+        load_chunk(1, c + 1);
+        mul_chunk(0);
+        load_chunk(0, c + 2 < chunks ? c + 2 : chunks - 1);
+        mul_chunk(1);
+      }
+      if (c < chunks) mul_chunk(0);
+    }
+    // the steps that fill no chunk, a wave each, and the step that K ends in
+    for (int i = all * U; i < ns; ++i)
+      if (i % kRankWaves == w) {
+        load(0, 0, i);
+        mul(0, 0);
+      }
+    if (s1 > full && w == 0) {
+      const int left = a.K - full * STEP - g4 * KE, o = (full - s0) * STEP * S;
+#pragma unroll
+      for (int m = 0; m < M; ++m) qx[0][0][m] = load_part<DT>(px[m] + o, left);
+#pragma unroll
+      for (int q = 0; q < RT; ++q) qa[0][0][q] = load_part<DT>(pa[q] + o, left);
+      mul(0, 0);
+    }
+    if (w > 0)
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int q = 0; q < RT; ++q) red[w - 1][m][q][lane] = acc[m][q];
+    __syncthreads();
+    if (w == 0)
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        const int row = row0 + 16 * m + i16;
+        float* to = a.part + ((int64_t)blockIdx.y * a.map.rows + row) * (16 * RT);
+#pragma unroll
+        for (int q = 0; q < RT; ++q) {
+          f32x4_t v = acc[m][q];
+#pragma unroll
+          for (int k = 0; k < kRankWaves - 1; ++k) v += red[k][m][q][lane];
+          const int r0 = 16 * q + 4 * g4;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = tok[m] < 0 || r0 + i >= a.r ? 0.f : v[i];
+          if (row < row1) *reinterpret_cast<f32x4_t*>(to + r0) = v;
+        }
+      }
+    row0 = row1 - 16 * M;  // the next rows, of this group or another
+    if (row1 < end) __syncthreads();  // the sums are read before they are written again
   }
 #endif
 }
 
 // ------------------------------------------------------------------ add
 constexpr int kAddWaves = 4;
-constexpr int kAddCols = 64 * kAddWaves;  // columns of a workgroup
-constexpr int kBareTokens = 256;          // tokens a workgroup looks over for rows of no adapter
+constexpr int kBareTokens = 16;  // tokens a wave looks over for rows of no adapter
 
-// Rows of no adapter: out = base, or 0.  A wave looks over kBareTokens / kAddWaves
-// tokens at once.
-template <int DT> __device__ __forceinline__ void bare_rows(const LoraAdd& a, int slab, int block) {
-  constexpr int KE = kFragElems<DT>, S = Elem<DT>::kBytes, LPR = kAddCols / KE, RPW = 64 / LPR;
-  constexpr int TOKENS = kBareTokens / kAddWaves;
-  const int lane = lane_id(), w = wave_id();
-  const int64_t t0 = (int64_t)block * kBareTokens + w * TOKENS;
-  const int col = slab * kAddCols + (lane % LPR) * KE;
+// 64-column blocks of a wave (8192 x 4096 of rank 16: 39.4 us with two, 45.0 with
+// one, 47.0 with four; 24576 x 1408 of rank 32: 65 with two, 76 with one).
+template <int DT, int RT> constexpr int kAddBlocks = RT >= 4 || DT == 0 ? 1 : 2;
+
+// Rows of no adapter: out = base, or 0.  A wave looks over kBareTokens tokens at once.
+template <int DT> __device__ __forceinline__ void bare_rows(const LoraAdd& a, int wave) {
+  constexpr int KE = kFragElems<DT>, S = Elem<DT>::kBytes;
+  const int lane = lane_id();
+  const int64_t t0 = (int64_t)wave * kBareTokens;
   bool bare = false;
-  if (lane < TOKENS && t0 + lane < a.map.rows) {
+  if (lane < kBareTokens && t0 + lane < a.map.rows) {
     const int row = a.map.row_of_pair[t0 + lane];
     bare = row < 0 || row >= a.map.rows;
   }
-  uint64_t left = __ballot(bare);
-  while (left) {
-    // the next RPW such rows, one for each LPR lanes
-    int t = -1;
+  for (uint64_t left = __ballot(bare); left; left &= left - 1) {
+    const int64_t at = (t0 + __ffsll((unsigned long long)left) - 1) * a.N;
+    const char* from = (const char*)a.base + at * S;
+    char* to = (char*)a.out + at * S;
+    if (a.N >= KE && a.base) {  // eight accesses in flight; one that would end outside copies the last KE columns
+      for (int c0 = lane * KE; c0 < a.N; c0 += 8 * 64 * KE) {
+        u32x4_t v[8];
+        int col[8];
 #pragma unroll
-    for (int i = 0; i < RPW; ++i)
-      if (left) {
-        const int at = __ffsll((unsigned long long)left) - 1;
-        left &= left - 1;
-        t = lane / LPR == i ? at : t;
+        for (int i = 0; i < 8; ++i) {
+          col[i] = c0 + i * 64 * KE;
+          col[i] = col[i] < a.N - KE ? col[i] : a.N - KE;
+          v[i] = load16<DT>(from + col[i] * S);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) store16<DT>(to + col[i] * S, v[i]);
       }
-    if (t < 0 || col >= a.N) continue;
-    const int64_t at = ((t0 + t) * a.N + col) * S;
-    const u32x4_t v = a.base ? load_part<DT>((const char*)a.base + at, a.N - col) : u32x4_t{0, 0, 0, 0};
-    store_part<DT>((char*)a.out + at, v, a.N - col);
+    } else {
+      for (int col = lane * KE; col < a.N; col += 64 * KE)
+        store_part<DT>(to + col * S, a.base ? load_part<DT>(from + col * S, a.N - col) : u32x4_t{0, 0, 0, 0}, a.N - col);
+    }
   }
 }
 
-// slabs: workgroups beside each other along N, each of kAddCols columns, the
-// fastest in the grid (neighbours then write neighbouring bytes of the same rows).
-// tiles: workgroups of a slab that take tiles of MT rows; those behind them look
-// for rows of no adapter.
-template <int DT, int RT, int MT>
-__global__ __launch_bounds__(64 * kAddWaves) void lora_add_kernel(LoraAdd a, int slabs, int tiles) {
+// A wave takes a range of the rows and a block of columns; the blocks of a range
+// are neighbouring waves.  bare: workgroups that look for rows of no adapter.
+template <int DT, int RT>
+__global__ __launch_bounds__(64 * kAddWaves) void lora_add_kernel(LoraAdd a, int ranges, int bare) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int KE = kFragElems<DT>, S = Elem<DT>::kBytes, Q = 16 / KE;  // Q: accesses of a lane's sixteen columns
-  constexpr int SUB = MT / 16, W = 16 * RT;
-  const int slab = blockIdx.x % slabs, tile = blockIdx.x / slabs;
-  if (tile >= tiles) {
-    bare_rows<DT>(a, slab, tile - tiles);
+  constexpr int CT = kAddBlocks<DT, RT>, W = 16 * RT;
+  const int lane = lane_id(), w = wave_id(), i16 = lane & 15, g4 = lane >> 4;
+  if ((int)blockIdx.x < bare) {
+    bare_rows<DT>(a, blockIdx.x * kAddWaves + w);
     return;
   }
-  const int lane = lane_id(), w = wave_id(), i16 = lane & 15, g4 = lane >> 4;
-  const int base = slab * kAddCols + w * 64;
-  const Tile t = find_tile(a.map, tile, MT);
-  if (t.g < 0 || base >= a.N) return;
-  const bool keeps = a.u && slab == 0 && w == 0;
-  const bool whole = base + 64 <= a.N;  // every lane has all of its columns
+  const int blocks = (a.N + 64 * CT - 1) / (64 * CT);
+  const int unit = by_xcd(blockIdx.x - bare, gridDim.x - bare) * kAddWaves + w, block = unit % blocks, range = unit / blocks;
+  if (range >= ranges) return;
+  const Rows rows = rows_of(a.map, ranges);
+  const int base = block * 64 * CT, end = rows.begin(range + 1);
+  const bool keeps = a.u && block == 0;
+  const bool whole = base + 64 * CT <= a.N;  // every lane has all of its columns
   // 16-bit types: virtual K of 2 * 16 RT, the high parts, then the low ones
   auto rank_of = [&](int s) { const int c = 4 * s + g4; return DT == 0 ? 4 * c : 8 * (c % (2 * RT)); };
-  // Columns: access j of a lane is KE neighbours from column base + 4 KE j + KE g4
-  // on (64 bytes a row and access), results q = j KE / 4 + h its elements 4 h + 0..3.
-  const char* rows_b[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int n = base + 4 * KE * (4 * q / KE) + KE * (i16 >> 2) + 4 * q % KE + (i16 & 3);
-    rows_b[q] = (const char*)a.B + ((int64_t)t.g * a.N + (n < a.N ? n : a.N - 1)) * a.r * S;
-  }
-  u32x4_t qb[4][RT];
-  if (a.r % KE == 0) {  // no branch between the loads
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int s = 0; s < RT; ++s) {
-        const int r0 = rank_of(s);
-        const u32x4_t v = load16<DT>(rows_b[q] + (r0 < a.r ? r0 : 0) * S);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) qb[q][s][j] = r0 < a.r ? v[j] : 0u;
-      }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int s = 0; s < RT; ++s) {
-        const int r0 = rank_of(s);
-        qb[q][s] = load_part<DT>(rows_b[q] + r0 * S, r0 < a.r ? a.r - r0 : 0);
-      }
-  }
-  const float scale = a.scale ? a.scale[t.g] : 1.f;
   const int col = base + KE * g4;
-  int row[SUB], tok[SUB];
-#pragma unroll
-  for (int b = 0; b < SUB; ++b) {
-    const int at = t.row0 + 16 * b + i16;
-    row[b] = at < t.row1 ? at : t.row1 - 1;
-    tok[b] = token_of(a.map, row[b]);
-  }
-  // all rows of the tile in flight at once
-  u32x4_t y[SUB][Q];
-#pragma unroll
-  for (int b = 0; b < SUB; ++b) {
-    const char* from = (const char*)a.base + ((int64_t)(tok[b] < 0 ? 0 : tok[b]) * a.N + col) * S;
-    if (!a.base) {
-#pragma unroll
-      for (int j = 0; j < Q; ++j) y[b][j] = u32x4_t{0, 0, 0, 0};
-    } else if (whole) {
-#pragma unroll
-      for (int j = 0; j < Q; ++j) y[b][j] = load16<DT>(from + 64 * j);
-    } else {
-#pragma unroll
-      for (int j = 0; j < Q; ++j) {
-        const int left = a.N - col - j * 4 * KE;
-        y[b][j] = load_part<DT>(from + 64 * j, left < 0 ? 0 : left);
-      }
-    }
-  }
-#pragma unroll
-  for (int b = 0; b < SUB; ++b) {
-    if (t.row0 + 16 * b >= t.row1) break;
-    const bool live = t.row0 + 16 * b + i16 < t.row1 && tok[b] >= 0;
-    float v[RT][KE];
-    float big = 0.f;
-#pragma unroll
-    for (int s = 0; s < RT; ++s) {
-      const int r0 = rank_of(s);
-      const float* from = a.part + (int64_t)row[b] * W + r0;
-#pragma unroll
-      for (int j = 0; j < KE; j += 4) {
-        f32x4_t sum = *reinterpret_cast<const f32x4_t*>(from + j);
-#pragma unroll 4
-        for (int p = 1; p < a.splits; ++p)
-          sum += *reinterpret_cast<const f32x4_t*>(from + (int64_t)p * a.map.rows * W + j);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[s][j + i] = sum[i];
-      }
-      if (keeps && t.row0 + 16 * b + i16 < t.row1 && (DT == 0 || 4 * s + g4 < 2 * RT))
-#pragma unroll
-        for (int j = 0; j < KE; ++j)
-          if (r0 + j < a.u_width) a.u[(int64_t)row[b] * a.u_width + r0 + j] = v[s][j];
-#pragma unroll
-      for (int j = 0; j < KE; ++j) {
-        v[s][j] *= scale;
-        big = fmaxf(big, fabsf(v[s][j]));
-      }
-    }
-    float up = 1.f;  // fp16: the row's sums brought to [1, 2) by a power of two, exactly, and back at the end
-    if constexpr (DT == 2) {
-      big = fmaxf(big, __shfl_xor(big, 16, 64));
-      big = fmaxf(big, __shfl_xor(big, 32, 64));
-      const int e = big > 0.f && big < INFINITY ? (big < 0x1p-126f ? -126 : ilogbf(big)) : 0;
-      up = ldexpf(1.f, e);
-      const float down = ldexpf(1.f, -e);
+  for (int row0 = rows.begin(range); row0 < end;) {
+    const Part t = part_at(a.map, rows, row0, end);
+    const float scale = a.scale ? a.scale[t.g] : 1.f;
+
+    // sixteen rows at a time: the next ones are in flight, and the tokens of
+    // those behind, while these are worked on (no load under a condition, none
+    // moved to its use; rows past the group ask for its last one again)
+    u32x4_t qb[CT][4][RT];
+    int word[2], tok[2];
+    u32x4_t y[2][CT][Q];
+    f32x4_t u[2][RT][KE / 4];
+    auto at_row = [&](int r) { return r + i16 < t.end ? r + i16 : t.end - 1; };
+    auto words = [&](int buf, int r) {
+      word[buf] = token_word(a.map, at_row(r));
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto load = [&](int buf, int r) {
+      tok[buf] = token_in(a.map, at_row(r), word[buf]);
+      const int64_t at = ((int64_t)(tok[buf] < 0 ? 0 : tok[buf]) * a.N + col) * S;
 #pragma unroll
       for (int s = 0; s < RT; ++s)
 #pragma unroll
-        for (int j = 0; j < KE; ++j) v[s][j] *= down;
-    }
-    f32x4_t acc[4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        for (int j = 0; j < KE / 4; ++j)
+          u[buf][s][j] = *reinterpret_cast<const f32x4_t*>(a.part + (int64_t)at_row(r) * W + rank_of(s) + 4 * j);
+      if (whole && a.base) {
 #pragma unroll
-    for (int s = 0; s < RT; ++s) {
-      u32x4_t f = narrow<DT>(v[s]);
-      if constexpr (DT != 0) {
-        float hi[KE];
-        widen<DT>(f, hi);
+        for (int c = 0; c < CT; ++c)
 #pragma unroll
-        for (int j = 0; j < KE; ++j) hi[j] = v[s][j] - hi[j];
-        const u32x4_t lo = narrow<DT>(hi);
+          for (int j = 0; j < Q; ++j) y[buf][c][j] = load16<DT>((const char*)a.base + at + 64 * (c * Q + j));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto work = [&](int buf, int r) {
+      const bool live = r + i16 < t.end && tok[buf] >= 0;
+      const int64_t at = ((int64_t)(tok[buf] < 0 ? 0 : tok[buf]) * a.N + col) * S;
+      float v[RT][KE];
+      float big = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = 4 * s + g4 < 2 * RT ? f[j] : lo[j];
+      for (int s = 0; s < RT; ++s) {
+        const int r0 = rank_of(s);
+#pragma unroll
+        for (int j = 0; j < KE / 4; ++j) {
+          f32x4_t sum = u[buf][s][j];
+          const float* from = a.part + (int64_t)at_row(r) * W + r0 + 4 * j;
+#pragma unroll 8
+          for (int p = 1; p < a.splits; ++p) sum += *reinterpret_cast<const f32x4_t*>(from + (int64_t)p * a.map.rows * W);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[s][4 * j + i] = sum[i];
+        }
+        if (keeps && r + i16 < t.end && (DT == 0 || 4 * s + g4 < 2 * RT))
+#pragma unroll
+          for (int j = 0; j < KE; ++j)
+            if (r0 + j < a.u_width) a.u[(int64_t)(r + i16) * a.u_width + r0 + j] = v[s][j];
+#pragma unroll
+        for (int j = 0; j < KE; ++j) {
+          v[s][j] *= scale;
+          big = fmaxf(big, fabsf(v[s][j]));
+        }
+      }
+      float up = 1.f;  // fp16: the row's sums brought to [1, 2) by a power of two, exactly, and back at the end
+      if constexpr (DT == 2) {
+        big = fmaxf(big, __shfl_xor(big, 16, 64));
+        big = fmaxf(big, __shfl_xor(big, 32, 64));
+        const int e = big > 0.f && big < INFINITY ? (big < 0x1p-126f ? -126 : ilogbf(big)) : 0;
+        up = ldexpf(1.f, e);
+        const float down = ldexpf(1.f, -e);
+#pragma unroll
+        for (int s = 0; s < RT; ++s)
+#pragma unroll
+          for (int j = 0; j < KE; ++j) v[s][j] *= down;
+      }
+      u32x4_t f[RT];
+#pragma unroll
+      for (int s = 0; s < RT; ++s) {
+        f[s] = narrow<DT>(v[s]);
+        if constexpr (DT != 0) {
+          float rest[KE];
+          widen<DT>(f[s], rest);
+#pragma unroll
+          for (int j = 0; j < KE; ++j) rest[j] = v[s][j] - rest[j];
+          const u32x4_t lo = narrow<DT>(rest);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[s][j] = 4 * s + g4 < 2 * RT ? f[s][j] : lo[j];
+        }
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) acc[q] = mma<DT>(qb[q][s], f, acc[q]);
-    }
-    if (!live) continue;
-    char* to = (char*)a.out + ((int64_t)tok[b] * a.N + col) * S;
+      for (int c = 0; c < CT; ++c) {
+        f32x4_t acc[4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-    for (int j = 0; j < Q; ++j) {
-      float o[KE];
-      widen<DT>(y[b][j], o);
+        for (int s = 0; s < RT; ++s)
 #pragma unroll
-      for (int i = 0; i < KE; ++i) o[i] = fmaf(acc[(j * KE + i) / 4][i % 4], up, o[i]);
-      const u32x4_t r = narrow<DT>(o);
-      if (whole) {
-        store16<DT>(to + 64 * j, r);
-      } else {
-        const int left = a.N - col - j * 4 * KE;
-        if (left > 0) store_part<DT>(to + 64 * j, r, left);
+          for (int q = 0; q < 4; ++q) acc[q] = mma<DT>(qb[c][q][s], f[s], acc[q]);
+        if (!live) continue;
+#pragma unroll
+        for (int j = 0; j < Q; ++j) {
+          const int left = a.N - col - 4 * KE * (c * Q + j);
+          if (!whole && left <= 0) continue;
+          float o[KE];
+          u32x4_t old = {0, 0, 0, 0};
+          if (a.base) old = whole ? y[buf][c][j] : load_part<DT>((const char*)a.base + at + 64 * (c * Q + j), left);
+          widen<DT>(old, o);
+#pragma unroll
+          for (int i = 0; i < KE; ++i) o[i] = fmaf(acc[(j * KE + i) / 4][i % 4], up, o[i]);
+          char* to = (char*)a.out + at + 64 * (c * Q + j);
+          if (whole) store16<DT>(to, narrow<DT>(o));
+          else store_part<DT>(to, narrow<DT>(o), left);
+        }
       }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    words(0, row0);
+    words(1, row0 + 16);
+    // Columns: access j of a lane in block c is KE neighbours from column base + 64 c
+    // + 4 KE j + KE g4 on (64 bytes a row and access), results q = j KE / 4 + h its
+    // elements 4 h + 0..3.
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = base + 64 * c + 4 * KE * (4 * q / KE) + KE * (i16 >> 2) + 4 * q % KE + (i16 & 3);
+        const char* from = (const char*)a.B + ((int64_t)t.g * a.N + (n < a.N ? n : a.N - 1)) * a.r * S;
+#pragma unroll
+        for (int s = 0; s < RT; ++s) {
+          const int r0 = rank_of(s);
+          qb[c][q][s] = a.r % KE == 0 ? load16<DT>(from + (r0 < a.r ? r0 : 0) * S)
+                                      : load_part<DT>(from + r0 * S, r0 < a.r ? a.r - r0 : 0);
+        }
+      }
+    __builtin_amdgcn_sched_barrier(0);
+    load(0, row0);
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int s = 0; s < RT; ++s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) qb[c][q][s][j] = rank_of(s) < a.r ? qb[c][q][s][j] : 0u;
+    for (int r = row0; r < t.end; r += 32) {
+      load(1, r + 16);
+      words(0, r + 32);
+      work(0, r);
+      load(0, r + 32);
+      words(1, r + 48);
+      if (r + 16 < t.end) work(1, r + 16);
     }
+    row0 = t.end;
   }
 #endif
 }
@@ -379,22 +480,12 @@ __global__ __launch_bounds__(64 * kAddWaves) void lora_add_kernel(LoraAdd a, int
 // ------------------------------------------------------------------ grad
 constexpr int kGradWaves = 4;
 
-// Rows of a tile: enough tiles for three workgroups a compute unit (a compute
-// unit takes no more than about 23 GB/s from HBM, so all of them have to be at
-// work to the end), and no more, for a group of several tiles adds their sums.
-int grad_rows(int rows, int K, int N, int cols) {
-  const int64_t slabs = (K + cols - 1) / cols + (N + cols - 1) / cols;
-  const int64_t n = (int64_t)rows * slabs / (3 * kNumCUs);
-  return n < 128 ? 128 : n > (1 << 20) ? (1 << 20) : (int)((n + 127) / 128 * 128);
-}
-
-// Places of the tiles' sums that are still to be added: the first tiles of two
-// groups of several tiles start more than a tile's height apart, and so do two
-// later tiles; one place for each height's first tile and one for a later one.
-__host__ __device__ inline int grad_places(int rows, int tile_rows) { return 2 * (rows / tile_rows + 1); }
-__device__ __forceinline__ int64_t grad_place(const LoraGrad& a, const Tile& t, int row, int frags) {
+// Where a range leaves its sum of a group that others share: in place 0 if the
+// group began before it, else in place 1 (of the ranges' two each no group but
+// the first and the last of a range wants one).
+__device__ __forceinline__ int64_t grad_place(int ranges, int range, bool began, int frags) {
   const int64_t unit = (int64_t)blockIdx.z * gridDim.x + blockIdx.x;
-  return (unit * grad_places(a.map.rows, a.tile_rows) + 2 * (row / a.tile_rows) + (row != t.row_first)) * frags * 64;
+  return ((unit * ranges + range) * 2 + began) * frags * 64;
 }
 
 // A group's gradients from the sums of a wave: lane 16 g4 + i16 holds ranks
@@ -430,9 +521,9 @@ __device__ __forceinline__ void write_grad(const LoraGrad& a, int g, int mat, in
   }
 }
 
-// grid: (slabs of 16 KE columns of the wider matrix, tile, matrix and RT rank
-// tiles).  A group of one tile is written at once; a group of several leaves its
-// tiles' sums for lora_grad_sum_kernel, which adds them in the tiles' order.
+// grid: (slabs of 16 KE columns of the wider matrix, ranges of rows, matrix and RT
+// rank tiles).  A group that lies in one range is written at once; of one that does
+// not each range leaves its sum for lora_grad_sum_kernel, which adds them in order.
 template <int DT, int RT, bool FULL> __global__ __launch_bounds__(64 * kGradWaves) void lora_grad_kernel(LoraGrad a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int KE = kFragElems<DT>, S = Elem<DT>::kBytes, COLS = 16 * KE, U = 4, ROUND = 4 * kGradWaves;
@@ -441,140 +532,152 @@ template <int DT, int RT, bool FULL> __global__ __launch_bounds__(64 * kGradWave
   const int mat = blockIdx.z & 1, q0 = (blockIdx.z >> 1) * RT;
   const int W = a.width[mat];
   if ((int)blockIdx.x * COLS >= W) return;
-  const Tile t = find_tile(a.map, blockIdx.y, a.tile_rows);
-  if (t.g < 0) return;
-  const int g = t.g;
+  const int ranges = gridDim.y;
+  const Rows rows = rows_of(a.map, ranges);
+  const int begin = rows.begin(blockIdx.y), end = rows.begin(blockIdx.y + 1);
   // a lane whose columns end outside takes the last KE, its neighbour's again:
   // both write the same sums (W < KE: columns past W read one by one below)
   const int at = blockIdx.x * COLS + i16 * KE, last = W > KE ? W - KE : 0;
   const int col = at < last ? at : last;
-  const int lo = t.row0, hi = t.row1;
   const char* wide = (const char*)a.wide[mat] + (int64_t)col * S;
   const float* v = a.v[mat];
   const int vw = mat == 0 ? lora_width(a.r) : a.r;  // floats of a row of v
   int rank[RT];
 #pragma unroll
   for (int q = 0; q < RT; ++q) rank[q] = 16 * (q0 + q) + i16 < a.r ? 16 * (q0 + q) + i16 : a.r - 1;
+  for (int row0 = begin; row0 < end;) {
+    const Part t = part_at(a.map, rows, row0, end);
+    const int lo = row0, hi = t.end;
+    f32x4_t acc[RT][KE];
+#pragma unroll
+    for (int q = 0; q < RT; ++q)
+#pragma unroll
+      for (int j = 0; j < KE; ++j) acc[q][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    // wave w takes rows 4 w .. 4 w + 3 of every ROUND, U rounds a batch: a batch's
+    // rows are in flight while the batch before is multiplied, and their tokens
+    // were read one batch earlier.  Rows past the group read its last row and count 0.
+    // Nothing that was loaded is looked at before its turn, which would wait for it.
+    int word[2][U];
+    bool live[2][U];
+    u32x4_t x[2][U];
+    float f[2][U][RT];
+    auto tokens = [&](int buf, int r0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int row = r0 + u * ROUND + g4;
+        word[buf][u] = token_word(a.map, row < hi ? row : hi - 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto load = [&](int buf, int r0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int row = r0 + u * ROUND + g4, at_row = row < hi ? row : hi - 1;
+        const int tok = token_in(a.map, at_row, word[buf][u]);
+        const char* p = wide + (int64_t)(tok < 0 ? 0 : tok) * W * S;
+        x[buf][u] = FULL ? load16<DT>(p) : load_part<DT>(p, W);
+#pragma unroll
+        for (int q = 0; q < RT; ++q) f[buf][u][q] = v[(int64_t)at_row * vw + rank[q]];
+        live[buf][u] = row < hi && tok >= 0;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto mul = [&](int buf) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float e[KE];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[buf][u][j] = live[buf][u] ? x[buf][u][j] : 0u;
+        widen<DT>(x[buf][u], e);
+#pragma unroll
+        for (int q = 0; q < RT; ++q) {
+          const float c = live[buf][u] ? f[buf][u][q] : 0.f;
+#pragma unroll
+          for (int j = 0; j < KE; ++j)
+            acc[q][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(c, e[j], acc[q][j], 0, 0, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    constexpr int BATCH = ROUND * U;
+    const int first = lo + 4 * w;
+    if (first < hi) {  // no load under a condition in the loop, as in the rank kernel
+      tokens(0, first);
+      tokens(1, first + BATCH);
+      load(0, first);
+      int r0 = first;
+      for (; r0 + BATCH < hi; r0 += 2 * BATCH) {
+        load(1, r0 + BATCH);
+        tokens(0, r0 + 2 * BATCH);
+        mul(0);
+        load(0, r0 + 2 * BATCH);
+        tokens(1, r0 + 3 * BATCH);
+        mul(1);
+      }
+      if (r0 < hi) mul(0);
+    }
+    // the waves' sums, half by half
+#pragma unroll
+    for (int half = kGradWaves / 2; half > 0; half /= 2) {
+      if (w >= half && w < 2 * half)
+#pragma unroll
+        for (int q = 0; q < RT; ++q)
+#pragma unroll
+          for (int j = 0; j < KE; ++j) red[w - half][q][j][lane] = acc[q][j];
+      __syncthreads();
+      if (w < half)
+#pragma unroll
+        for (int q = 0; q < RT; ++q)
+#pragma unroll
+          for (int j = 0; j < KE; ++j) acc[q][j] += red[w][q][j][lane];
+      __syncthreads();
+    }
+    if (w == 0) {
+      if (t.lo < begin || t.hi > end) {
+        f32x4_t* part = (f32x4_t*)a.part + grad_place(ranges, blockIdx.y, t.lo >= begin, RT * KE) + lane;
+#pragma unroll
+        for (int q = 0; q < RT; ++q)
+#pragma unroll
+          for (int j = 0; j < KE; ++j) part[(q * KE + j) * 64] = acc[q][j];
+      } else {
+        write_grad<DT, RT>(a, t.g, mat, q0, at, col, acc);
+      }
+    }
+    row0 = hi;
+  }
+#endif
+}
+
+// One wave for each slab, group, matrix and rank tiles.
+template <int DT, int RT> __global__ __launch_bounds__(64) void lora_grad_sum_kernel(LoraGrad a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int KE = kFragElems<DT>, COLS = 16 * KE;
+  const int lane = lane_id(), i16 = lane & 15;
+  const int mat = blockIdx.z & 1, q0 = (blockIdx.z >> 1) * RT, g = blockIdx.y;
+  const int W = a.width[mat];
+  if ((int)blockIdx.x * COLS >= W) return;
+  const Rows rows = rows_of(a.map, a.ranges);
+  const int lo = cut(a.map.offsets[g], a.map.rows), hi = cut(a.map.offsets[g + 1], a.map.rows);
+  // (offsets that fall name rows outside: no ranges)
+  if (hi <= lo || lo < rows.first || hi > rows.last) return;
+  const int r0 = rows.range_of(lo), r1 = rows.range_of(hi - 1);
+  if (r0 == r1) return;
+  const int at = blockIdx.x * COLS + i16 * KE, last = W > KE ? W - KE : 0;
   f32x4_t acc[RT][KE];
 #pragma unroll
   for (int q = 0; q < RT; ++q)
 #pragma unroll
     for (int j = 0; j < KE; ++j) acc[q][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  // wave w takes rows 4 w .. 4 w + 3 of every ROUND, U rounds a batch: a batch's
-  // rows are in flight while the batch before is multiplied, and their tokens
-  // were read one batch earlier.  Rows past the group read its last row and count 0.
-  // Nothing that was loaded is looked at before its turn, which would wait for it.
-  int word[2][U];
-  bool live[2][U];
-  u32x4_t x[2][U];
-  float f[2][U][RT];
-  auto tokens = [&](int buf, int r0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int row = r0 + u * ROUND + g4;
-      word[buf][u] = token_word(a.map, row < hi ? row : hi - 1);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  auto load = [&](int buf, int r0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int row = r0 + u * ROUND + g4, at_row = row < hi ? row : hi - 1;
-      const int tok = token_in(a.map, at_row, word[buf][u]);
-      const char* p = wide + (int64_t)(tok < 0 ? 0 : tok) * W * S;
-      x[buf][u] = FULL ? load16<DT>(p) : load_part<DT>(p, W);
-#pragma unroll
-      for (int q = 0; q < RT; ++q) f[buf][u][q] = v[(int64_t)at_row * vw + rank[q]];
-      live[buf][u] = row < hi && tok >= 0;
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  auto mul = [&](int buf) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float e[KE];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[buf][u][j] = live[buf][u] ? x[buf][u][j] : 0u;
-      widen<DT>(x[buf][u], e);
-#pragma unroll
-      for (int q = 0; q < RT; ++q) {
-        const float c = live[buf][u] ? f[buf][u][q] : 0.f;
-#pragma unroll
-        for (int j = 0; j < KE; ++j)
-          acc[q][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(c, e[j], acc[q][j], 0, 0, 0);
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  constexpr int BATCH = ROUND * U;
-  const int first = lo + 4 * w;
-  if (first < hi) {  // no load under a condition in the loop, as in the rank kernel
-    tokens(0, first);
-    tokens(1, first + BATCH);
-    load(0, first);
-    int r0 = first;
-    for (; r0 + BATCH < hi; r0 += 2 * BATCH) {
-      load(1, r0 + BATCH);
-      tokens(0, r0 + 2 * BATCH);
-      mul(0);
-      load(0, r0 + 2 * BATCH);
-      tokens(1, r0 + 3 * BATCH);
-      mul(1);
-    }
-    if (r0 < hi) mul(0);
-  }
-  // the waves' sums, half by half
-#pragma unroll
-  for (int half = kGradWaves / 2; half > 0; half /= 2) {
-    if (w >= half && w < 2 * half)
-#pragma unroll
-      for (int q = 0; q < RT; ++q)
-#pragma unroll
-        for (int j = 0; j < KE; ++j) red[w - half][q][j][lane] = acc[q][j];
-    __syncthreads();
-    if (w < half)
-#pragma unroll
-      for (int q = 0; q < RT; ++q)
-#pragma unroll
-        for (int j = 0; j < KE; ++j) acc[q][j] += red[w][q][j][lane];
-    __syncthreads();
-  }
-  if (w > 0) return;
-  if (t.n > 1) {
-    f32x4_t* part = (f32x4_t*)a.part + grad_place(a, t, t.row0, RT * KE) + lane;
-#pragma unroll
-    for (int q = 0; q < RT; ++q)
-#pragma unroll
-      for (int j = 0; j < KE; ++j) part[(q * KE + j) * 64] = acc[q][j];
-  } else {
-    write_grad<DT, RT>(a, t.g, mat, q0, at, col, acc);
-  }
-#endif
-}
-
-// One wave a unit of a group of several tiles; grid as above, for its first tile.
-template <int DT, int RT> __global__ __launch_bounds__(64) void lora_grad_sum_kernel(LoraGrad a) {
-  constexpr int KE = kFragElems<DT>, COLS = 16 * KE;
-  const int lane = lane_id(), i16 = lane & 15;
-  const int mat = blockIdx.z & 1, q0 = (blockIdx.z >> 1) * RT;
-  const int W = a.width[mat];
-  if ((int)blockIdx.x * COLS >= W) return;
-  const Tile t = find_tile(a.map, blockIdx.y, a.tile_rows);
-  if (t.g < 0 || t.n < 2 || t.row0 != t.row_first) return;
-  const int at = blockIdx.x * COLS + i16 * KE, last = W > KE ? W - KE : 0;
-  f32x4_t acc[RT][KE];
 #pragma unroll 2
-  for (int k = 0; k < t.n; ++k) {
-    const f32x4_t* part = (const f32x4_t*)a.part + grad_place(a, t, t.row_first + k * a.tile_rows, RT * KE) + lane;
+  for (int r = r0; r <= r1; ++r) {
+    const f32x4_t* part = (const f32x4_t*)a.part + grad_place(a.ranges, r, r == r0, RT * KE) + lane;
 #pragma unroll
     for (int q = 0; q < RT; ++q)
 #pragma unroll
-      for (int j = 0; j < KE; ++j) {
-        const f32x4_t v = part[(q * KE + j) * 64];
-        acc[q][j] = k ? acc[q][j] + v : v;
-      }
+      for (int j = 0; j < KE; ++j) acc[q][j] += part[(q * KE + j) * 64];
   }
-  write_grad<DT, RT>(a, t.g, mat, q0, at, at < last ? at : last, acc);
+  write_grad<DT, RT>(a, g, mat, q0, at, at < last ? at : last, acc);
+#endif
 }
 
 // ------------------------------------------------------------------ prepare
@@ -613,42 +716,62 @@ template <typename E> __global__ __launch_bounds__(256) void lora_prepare_kernel
   }
 }
 
-// Tiles of MT rows at most: whole ones, and one more for each group with rows.
-int64_t most_tiles(int rows, int G, int mt) {
-  const int64_t a = (int64_t)(rows + mt - 1) / mt + G;
-  return a < rows ? a : rows;
-}
 int rank_tiles(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : 8; }
-// Rows of a rank tile, in sixteens: as many as a group has on average, so that
-// A is read once for up to 64 rows (four tiles of rank 128 want too many registers).
-int rank_m(int rows, int G, int r) {
-  const int64_t each = (rows + G - 1) / G;
-  return each <= 16 ? 1 : each <= 32 || r > 64 ? 2 : 4;
-}
-bool few_rows(int rows, int G) { return rows <= 16 * (int64_t)G; }
 
-template <int DT, int RT, int M> hipError_t rank_tiles_of(const LoraRank& a, hipStream_t s) {
-  hipLaunchKernelGGL((lora_rank_kernel<DT, RT, M>), dim3((unsigned)most_tiles(a.map.rows, a.map.G, 16 * M), a.splits),
-                     dim3(64 * kRankWaves), 0, s, a);
+// How the rank kernel shares the rows out.  A workgroup's time is mostly one pass
+// over K, whatever its rows, so none should make two where others make one: tiles
+// of one group, as low as leaves no compute unit a workgroup more than the others
+// (one each up to 48 rows, else two), counted for the worst places of the groups'
+// ends.  Where the rows want more passes anyhow, even ranges of rows across groups.
+struct RankShare {
+  int height, places;  // height 0: ranges
+};
+RankShare rank_share(int rows, int G, int r) {
+  const int most = r > 64 ? 32 : 64;  // rows of a pass
+  for (int n = 1; n <= 2; ++n) {
+    const int free = n * kNumCUs - G;
+    if (free <= 0) continue;
+    int h = (int)(((int64_t)rows + free - 1) / free);
+    h = h < 16 ? 16 : h;
+    if (h <= (n == 1 && most > 48 ? 48 : most)) {
+      const int tiles = (rows + h - 1) / h + G;
+      return RankShare{h, tiles < rows ? tiles : rows};
+    }
+  }
+  if (rows <= 16 * (int64_t)G) return RankShare{16, (rows + 15) / 16 + G < rows ? (rows + 15) / 16 + G : rows};
+  return RankShare{0, 2 * kNumCUs};
+}
+
+template <int DT, int RT, int M> hipError_t rank_m(const LoraRank& a, int places, hipStream_t s) {
+  hipLaunchKernelGGL((lora_rank_kernel<DT, RT, M>), dim3((places + 7) / 8 * 8, a.splits), dim3(64 * kRankWaves), 0, s, a);
   return hipGetLastError();
 }
-template <int DT, int RT> hipError_t rank_of(const LoraRank& a, hipStream_t s) {
-  const int m = rank_m(a.map.rows, a.map.G, a.r);
-  if constexpr (RT < 8)
-    if (m == 4) return rank_tiles_of<DT, RT, 4>(a, s);
-  return m == 1 ? rank_tiles_of<DT, RT, 1>(a, s) : rank_tiles_of<DT, RT, 2>(a, s);
+template <int DT, int RT> hipError_t rank_of(const LoraRank& b, hipStream_t s) {
+  LoraRank a = b;
+  const RankShare share = rank_share(a.map.rows, a.map.G, a.r);
+  a.height = share.height;
+  a.ranges = share.places;
+  const int each = share.height ? share.height : 64;
+  if (each <= 16) return rank_m<DT, RT, 1>(a, share.places, s);
+  if constexpr (RT < 8) {  // more than two tiles of rank 128 want too many registers
+    if (each > 48) return rank_m<DT, RT, 4>(a, share.places, s);
+    if (each > 32) return rank_m<DT, RT, 3>(a, share.places, s);
+  }
+  return rank_m<DT, RT, 2>(a, share.places, s);
 }
 
-template <int DT, int RT, int MT> hipError_t add_tiles(const LoraAdd& a, hipStream_t s) {
-  const int tiles = (int)most_tiles(a.map.rows, a.map.G, MT);
-  const int bare = a.map.row_of_pair && a.out != a.base ? (a.map.rows + kBareTokens - 1) / kBareTokens : 0;
-  const int slabs = (a.N + kAddCols - 1) / kAddCols;
-  hipLaunchKernelGGL((lora_add_kernel<DT, RT, MT>), dim3((tiles + bare) * slabs), dim3(64 * kAddWaves), 0, s, a, slabs,
-                     tiles);
-  return hipGetLastError();
-}
 template <int DT, int RT> hipError_t add_of(const LoraAdd& a, hipStream_t s) {
-  return few_rows(a.map.rows, a.map.G) ? add_tiles<DT, RT, 16>(a, s) : add_tiles<DT, RT, 64>(a, s);
+  const int64_t blocks = (a.N + 64 * kAddBlocks<DT, RT> - 1) / (64 * kAddBlocks<DT, RT>);
+  // twelve waves a compute unit (eight 39 us, sixteen 41 at 8192 x 4096), but no
+  // less than a row each
+  int64_t ranges = (12 * kNumCUs + blocks - 1) / blocks;
+  if (ranges > a.map.rows) ranges = a.map.rows;
+  const int bare = a.map.row_of_pair && a.out != a.base
+                       ? (a.map.rows + 8 * kBareTokens * kAddWaves - 1) / (8 * kBareTokens * kAddWaves) * 8
+                       : 0;
+  hipLaunchKernelGGL((lora_add_kernel<DT, RT>), dim3((unsigned)((blocks * ranges + 8 * kAddWaves - 1) / (8 * kAddWaves) * 8 + bare)),
+                     dim3(64 * kAddWaves), 0, s, a, (int)ranges, bare);
+  return hipGetLastError();
 }
 
 int grad_tiles(int r) { return r <= 16 ? 1 : 2; }  // rank tiles of a workgroup of the grad kernel
@@ -659,15 +782,15 @@ int grad_slabs(int K, int N, int dtype) {
 int grad_units(int r) { return 2 * ((r + 16 * grad_tiles(r) - 1) / (16 * grad_tiles(r))); }
 
 template <int DT, int RT> hipError_t grad_of(const LoraGrad& a, hipStream_t s) {
-  const dim3 grid(grad_slabs(a.width[0], a.width[1], DT), (unsigned)most_tiles(a.map.rows, a.map.G, a.tile_rows),
-                  grad_units(a.r));
+  const int slabs = grad_slabs(a.width[0], a.width[1], DT), units = grad_units(a.r);
+  const dim3 grid(slabs, a.ranges, units);
   // FULL: a row of each matrix holds a whole 16-byte access
   if (a.width[0] >= kFragElems<DT> && a.width[1] >= kFragElems<DT>)
     hipLaunchKernelGGL((lora_grad_kernel<DT, RT, true>), grid, dim3(64 * kGradWaves), 0, s, a);
   else
     hipLaunchKernelGGL((lora_grad_kernel<DT, RT, false>), grid, dim3(64 * kGradWaves), 0, s, a);
-  if (a.part)
-    hipLaunchKernelGGL((lora_grad_sum_kernel<DT, RT>), grid, dim3(64), 0, s, a);
+  if (a.ranges > 1)
+    hipLaunchKernelGGL((lora_grad_sum_kernel<DT, RT>), dim3(slabs, a.map.G, units), dim3(64), 0, s, a);
   return hipGetLastError();
 }
 
@@ -688,29 +811,25 @@ template <int DT> hipError_t grad_dt(const LoraGrad& a, hipStream_t s) {
 }  // namespace
 
 int lora_splits(int rows, int G, int r, int K, int dtype) {
-  const int64_t tiles = most_tiles(rows, G, 16 * rank_m(rows, G, r));
-  if (tiles == 0) return 1;
-  const int steps = K / (dtype == 0 ? 16 : 32);
-  // four workgroups a compute unit, for it is the compute units, each with its
-  // own limit of loads in flight, that have to be kept evenly at work; eight K
-  // steps a wave (four with a few tiles); and parts of no more than an eighth of
-  // the bytes that they come from
-  int64_t n = (4 * kNumCUs + tiles - 1) / tiles;
-  const int64_t each = steps / ((tiles <= 64 ? 4 : 8) * kRankWaves);
-  const int64_t bytes = (int64_t)K * (dtype == 0 ? 4 : 2) / (8 * 4 * lora_width(r));
-  if (n > each) n = each;
-  if (tiles > 64 && n > bytes) n = bytes;
-  return n < 1 ? 1 : n > 16 ? 16 : (int)n;
+  if (rows == 0) return 1;
+  // two workgroups a compute unit where the rows do not fill half of them, for each
+  // share is read again by the add kernel; four K steps or more for each wave
+  const int places = rank_share(rows, G, r).places;
+  const int n = places > kNumCUs / 2 ? 1 : 2 * kNumCUs / places, each = K / (dtype == 0 ? 16 : 32) / (4 * kRankWaves);
+  return each < 1 ? 1 : n > each ? (each > 16 ? 16 : each) : n > 16 ? 16 : n;
 }
 
 LoraGradPlan lora_grad_plan(int rows, int G, int r, int K, int N, int dtype) {
-  LoraGradPlan p;
   const int cols = dtype == 0 ? 16 * kFragElems<0> : 16 * kFragElems<1>;
-  p.tile_rows = grad_rows(rows, K, N, cols);
-  // no group can have a second tile: no sums to add
-  p.part_bytes = rows > p.tile_rows ? (int64_t)grad_places(rows, p.tile_rows) * grad_units(r) * grad_slabs(K, N, dtype) *
-                                          grad_tiles(r) * (cols / 16) * 64 * 16
-                                    : 0;
+  // three workgroups a compute unit, but 128 rows each or more
+  const int64_t slabs = (K + cols - 1) / cols + (N + cols - 1) / cols;
+  int64_t n = 3 * kNumCUs / slabs;
+  if (n > rows / 128) n = rows / 128;
+  LoraGradPlan p;
+  p.ranges = n < 1 ? 1 : (int)n;
+  p.part_bytes = p.ranges > 1 ? (int64_t)p.ranges * 2 * grad_units(r) * grad_slabs(K, N, dtype) * grad_tiles(r) *
+                                    (cols / 16) * 64 * 16
+                              : 0;
   return p;
 }
 
