@@ -13,6 +13,7 @@ gradients are the _backward functions', and the forward calls refuse rows, gates
 scales, weights and adapters that require one while gradients are recorded."""
 from __future__ import annotations
 
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -347,8 +348,14 @@ class LoraWeights:
         self.view("LoraWeights")
 
     def view(self, fn: str):
-        """(groups, N, K, the C view), the arrays checked against each other."""
+        """(groups, N, K, r, the C view): the arrays checked against each other,
+        again only after one of them was given other storage or strides."""
         a, b, s = self.A, self.B, self.scale
+        now = (a.data_ptr(), b.data_ptr(), a.shape, b.shape, a.dtype, b.dtype, a.is_contiguous() and b.is_contiguous(),
+               None if s is None else (s.data_ptr(), s.shape, s.dtype, s.is_contiguous()))
+        seen = self.__dict__.get("_seen")
+        if seen is not None and seen[0] == now:
+            return seen[1]
         n = a.dim()
         _need(n in (3, 4) and b.dim() == n and a.shape[:-2] == b.shape[:-2] and a.shape[-2] == b.shape[-1], fn,
               "A [G, r, K] and B [G, N, r], or A [L, E, r, K] and B [L, E, N, r] expected")
@@ -361,41 +368,51 @@ class LoraWeights:
         _need(all(t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0) for t in (a, b, s)), fn,
               "contiguous, 16-byte aligned arrays expected")
         _need(all(t is None or t.data_ptr() or not t.numel() for t in (a, b, s)), fn, "arrays without memory")
-        return a.shape[:-2], b.shape[-2], a.shape[-1], mok.lora_weights(a, b, s, r)
+        v = (tuple(a.shape[:-2]), b.shape[-2], a.shape[-1], r, mok.lora_weights(a, b, s, r))
+        self.__dict__["_seen"] = (now, v)
+        return v
 
     def to(self, device) -> LoraWeights:
         return LoraWeights(self.A.to(device), self.B.to(device), None if self.scale is None else self.scale.to(device))
 
+    def __reduce__(self):
+        return LoraWeights, (self.A, self.B, self.scale)
+
+
+@functools.lru_cache(maxsize=256)
+def _lora_plan(rows, E, eb, ee, K, N, dt, r):
+    """(the C config, bytes of the forward call's workspace, of the backward call's)."""
+    cfg = mok.lora_config(rows, E, eb, ee, K, N, dt)
+    return (cfg, *mok.mok_lora_workspace_query(cfg, r))
+
 
 def _lora_args(fn: str, x, dout, amap: PairMap, w: LoraWeights, sorted_rows: bool):
-    """Checks rows [rows, K] and [rows, N] (either may be None) against a map
-    and its adapters; returns (rows, N, K, r, the C views of weights and config,
-    the map's arrays)."""
-    groups, N, K, wc = w.view(fn)
-    ref = x if x is not None else dout
-    dt = _DTYPES.get(ref.dtype)
+    """Checks rows [rows, K] and [rows, N] (the latter may be None) against a map
+    and its adapters; returns (rows, N, K, r, the weights' C view, the plan, the
+    map's arrays)."""
+    groups, N, K, r, wc = w.view(fn)
+    dt = _DTYPES.get(x.dtype)
     rows = amap.T * amap.k
     _need(len(groups) == 1 and groups[0] == amap.expert_end - amap.expert_begin, fn,
           "adapters A [G, r, K] of the map's local groups expected")
     _need(sorted_rows or amap.k == 1, fn, "a map of one group a row (k = 1) expected, or sorted rows")
-    _need(dt is not None and w.A.dtype == ref.dtype, fn, "rows of the adapters' type expected")
-    for t, width in ((x, K), (dout, N)):
-        _need(t is None or (t.shape == (rows, width) and t.dtype == ref.dtype), fn,
-              "x [rows, K] and y or dout [rows, N] of one type, a row for each of the map's, expected")
+    _need(dt is not None and w.A.dtype == x.dtype, fn, "rows of the adapters' type expected")
+    _need(x.shape == (rows, K) and (dout is None or (dout.shape == (rows, N) and dout.dtype == x.dtype)), fn,
+          "x [rows, K] and y or dout [rows, N] of one type, a row for each of the map's, expected")
     offsets = _of_shape(fn, "offsets", amap.offsets, (amap.E + 1,))
     pair = rop = None
     if not sorted_rows:
         pair = _of_shape(fn, "pair_of_row", amap.pair_of_row, (rows,))
         rop = _of_shape(fn, "row_of_pair", amap.row_of_pair, (amap.T, amap.k))
-    _on(fn, ref, x, dout, w.A, offsets, pair, rop)
-    cfg = mok.lora_config(rows, amap.E, amap.expert_begin, amap.expert_end, K, N, dt)
-    return rows, N, K, w.A.shape[1], wc, cfg, (_ready(pair), _ready(rop), _ready(offsets))
+    _on(fn, x, dout, w.A, offsets, pair, rop)
+    plan = _lora_plan(rows, amap.E, amap.expert_begin, amap.expert_end, K, N, dt, r)
+    return rows, N, K, r, wc, plan, (_ready(pair), _ready(rop), _ready(offsets))
 
 
 def _added_to(fn: str, base, out, shape, like, *inputs):
     """The base (contiguous) and the output of a sum, which may be one array."""
     if base is not None:
-        _need(base.shape == shape and base.dtype == like.dtype, fn, f"rows to add to of {like.dtype} {list(shape)} expected")
+        _need(base.shape == shape and base.dtype == like.dtype, fn, "rows to add to like the output expected")
         _on(fn, like, base)
     same = out is not None and base is not None and out.data_ptr() == base.data_ptr() and out.is_contiguous() and \
         base.is_contiguous()
@@ -416,13 +433,13 @@ def lora_rows(x: torch.Tensor, amap: PairMap, w: LoraWeights, y: torch.Tensor | 
     are.  `out` may be y itself.  With save the result is (out, u), u = A_g x_q
     in fp32 [rows, r] and sorted rows, for lora_rows_backward."""
     fn = "lora_rows"
-    rows, N, K, r, wc, cfg, (pair, rop, offsets) = _lora_args(fn, x, y, amap, w, sorted_rows)
+    rows, N, K, r, wc, (cfg, nws, _), (pair, rop, offsets) = _lora_args(fn, x, y, amap, w, sorted_rows)
     _unrecorded(fn, x, y, out, w.scale)
     _unrecorded(fn, w.A, w.B)
     x = _ready(x)
     y, out = _added_to(fn, y, out, (rows, N), x, x, pair, rop, offsets, w.A, w.B, w.scale)
     u = torch.empty((rows, r), dtype=torch.float32, device=x.device) if save else None
-    ws = torch.empty(mok.mok_lora_workspace_query(cfg, r)[0], dtype=torch.uint8, device=x.device)
+    ws = torch.empty(nws, dtype=torch.uint8, device=x.device)
     _call(mok.mok_lora_rows, x, x, y, pair, rop, offsets, wc, cfg, out, u, ws)
     return (out, u) if save else out
 
@@ -434,20 +451,34 @@ def lora_rows_backward(dout: torch.Tensor, x: torch.Tensor, u: torch.Tensor, ama
     [G, r, K] and dB [G, N, r] in fp32, 0 for a group without rows.  y's
     gradient is dout itself."""
     fn = "lora_rows_backward"
-    rows, N, K, r, wc, cfg, (pair, rop, offsets) = _lora_args(fn, x, dout, amap, w, sorted_rows)
+    rows, N, K, r, wc, (cfg, _, nws), (pair, rop, offsets) = _lora_args(fn, x, dout, amap, w, sorted_rows)
     _need(u.dtype == torch.float32 and u.shape == (rows, r), fn, "fp32 u [rows, r] of the forward call expected")
     _on(fn, x, u)
     dout, x, u = _ready(dout), _ready(x), _ready(u)
     base, dx = _added_to(fn, base, out, (rows, K), x, dout, x, u, pair, rop, offsets, w.A, w.B, w.scale)
     dA = torch.empty(w.A.shape, dtype=torch.float32, device=x.device)
     dB = torch.empty(w.B.shape, dtype=torch.float32, device=x.device)
-    ws = torch.empty(max(mok.mok_lora_workspace_query(cfg, r)[1], 16), dtype=torch.uint8, device=x.device)
+    ws = torch.empty(max(nws, 16), dtype=torch.uint8, device=x.device)
     _call(mok.mok_lora_rows_backward, x, dout, x, u, base, pair, rop, offsets, wc, cfg, dx, dA, dB, ws)
     return dx, dA, dB
 
 
 # ------------------------------------------------------------------ the layer for a few tokens
 _GATING = {"softmax": 0, "sigmoid": mok.MOK_FLAG_SIGMOID_GATES}
+
+
+@functools.lru_cache(maxsize=256)
+def _few_plan(T, d, E, k, F, eb, ee, dt, flags, L, ranks):
+    """(the C config, bytes of the workspace); ranks: of the adapters of w1, w3
+    and w2 (0: none), or None."""
+    cfg = mok.few_token_config(T, d, E, k, F, eb, ee, dt, flags, L)
+    lora = None
+    if ranks is not None:
+        lora = (mok.mok_lora_weights * 3)()
+        for m, r in enumerate(ranks):
+            if r:
+                lora[m] = mok.lora_weights(16, 16, None, r)  # read for their sizes alone
+    return cfg, mok.mok_few_token_workspace_query(cfg, lora)
 
 
 def few_token_layer(x: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor,
@@ -478,16 +509,16 @@ def few_token_layer(x: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, w3:
     _on(fn, x, logits, w1, w3, w2, adapter)
     _unrecorded(fn, x, logits, out, w1)
     _unrecorded(fn, w3, w2)
-    L, lc, read = 0, None, []
+    L, lc, read, ranks = 0, None, (), None
     _need((lora is None) == (adapter is None), fn, "lora and adapter expected together")
     if lora is not None:
         _need(adapter.dtype == torch.int32 and adapter.shape == (T,), fn, "int32 adapter [T] expected")
         _need(len(lora) == 3, fn, "lora of w1, w3 and w2 expected")
-        lc = (mok.mok_lora_weights * 3)()
+        lc, read, ranks = (mok.mok_lora_weights * 3)(), [], [0, 0, 0]
         for m, (lw, N, K) in enumerate(zip(lora, (F, F, d), (d, d, F))):
             if lw is None:
                 continue
-            groups, n, kk, c = lw.view(fn)
+            groups, n, kk, ranks[m], c = lw.view(fn)
             _need(len(groups) == 2 and groups[1] == E_loc and (n, kk) == (N, K) and lw.A.dtype == x.dtype and
                   L in (0, groups[0]) and groups[0], fn, "adapters [L, E_loc, ...] of the weights' type and sizes expected")
             _on(fn, x, lw.A)
@@ -495,12 +526,13 @@ def few_token_layer(x: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, w3:
             L = groups[0]
             lc[m] = c
             read += [lw.A, lw.B, lw.scale]
+        ranks = tuple(ranks)
     x, logits, w1, w3, w2, adapter = (_ready(t) for t in (x, logits, w1, w3, w2, adapter))
     out = _output(fn, out, (T, d), x.dtype, x.device, x, logits, w1, w3, w2, adapter, *read)
+    cfg, nws = _few_plan(T, d, E, k, F, expert_begin, expert_begin + E_loc, dt,
+                         _GATING[gating] | (mok.MOK_FLAG_RENORM_GATES if renorm else 0), L, ranks)
     idx = torch.empty((T, k), dtype=torch.int32, device=x.device)
     gate = torch.empty((T, k), dtype=torch.float32, device=x.device)
-    cfg = mok.few_token_config(T, d, E, k, F, expert_begin, expert_begin + E_loc, dt,
-                               _GATING[gating] | (mok.MOK_FLAG_RENORM_GATES if renorm else 0), L)
-    ws = torch.empty(mok.mok_few_token_workspace_query(cfg, lc), dtype=torch.uint8, device=x.device)
+    ws = torch.empty(nws, dtype=torch.uint8, device=x.device)
     _call(mok.mok_few_token_layer, x, x, logits, w1, w3, w2, adapter, lc, cfg, out, idx, gate, ws)
     return out, idx, gate

@@ -164,7 +164,7 @@ def test_weights_are_checked_and_moved():
         with pytest.raises(ValueError):
             X.LoraWeights(a, b, s)
     w = X.LoraWeights(z(2, 3, 8, 4).transpose(2, 3), z(2, 3, 5, 4), z(2))
-    assert w.A.is_contiguous() and w.to("cpu").view("t")[:3] == ((2, 3), 5, 8)
+    assert w.A.is_contiguous() and w.to("cpu").view("t")[:4] == ((2, 3), 5, 8, 4)
     w.A.resize_(2, 3, 4, 7)
     with pytest.raises(ValueError):
         X.lora_rows(z(4, 7), _map(4, 3), w)
