@@ -821,10 +821,12 @@ int lora_splits(int rows, int G, int r, int K, int dtype) {
 
 LoraGradPlan lora_grad_plan(int rows, int G, int r, int K, int N, int dtype) {
   const int cols = dtype == 0 ? 16 * kFragElems<0> : 16 * kFragElems<1>;
-  // three workgroups a compute unit, but 128 rows each or more
+  // three workgroups a compute unit, but 128 rows each or more, or a group (44 rows
+  // of 36 adapters, 256 to 3930 columns: 130 us by one range, for each group is a pass)
   const int64_t slabs = (K + cols - 1) / cols + (N + cols - 1) / cols;
   int64_t n = 3 * kNumCUs / slabs;
-  if (n > rows / 128) n = rows / 128;
+  const int64_t most = rows / 128 > G ? rows / 128 : rows < G ? rows : G;
+  if (n > most) n = most;
   LoraGradPlan p;
   p.ranges = n < 1 ? 1 : (int)n;
   p.part_bytes = p.ranges > 1 ? (int64_t)p.ranges * 2 * grad_units(r) * grad_slabs(K, N, dtype) * grad_tiles(r) *

@@ -43,7 +43,9 @@ LAYERS = [(1, 64, 64, 4, 1, "bf16"), (1, 1, 1, 1, 1, "f32"), (2, 32, 16, 3, 3, "
           (5, 130, 67, 17, 4, "bf16"), (7, 91, 33, 9, 2, "f16"), (16, 64, 48, 4, 2, "bf16"),
           (16, 256, 320, 16, 8, "bf16"), (9, 257, 129, 64, 6, "f32"), (13, 512, 96, 130, 5, "bf16"),
           (16, 100, 40, 300, 64, "bf16"), (4, 40, 200, 1024, 8, "f16"), (11, 1000, 72, 6, 6, "bf16"),
-          (16, 33, 31, 64, 64, "f32"), (6, 2048, 32, 8, 2, "bf16"), (8, 24, 2080, 8, 3, "f16")]
+          (16, 33, 31, 64, 64, "f32"), (6, 2048, 32, 8, 2, "bf16"), (8, 24, 2080, 8, 3, "f16"),
+          (2, 5000, 24, 3, 2, "bf16"), (3, 9001, 17, 2, 1, "f16"), (4, 16, 3001, 5, 2, "f32"),
+          (16, 24, 16, 1024, 64, "bf16")]  # most experts and pairs: the tables at their largest
 
 
 @pytest.mark.parametrize("T,d,F,E,k,dt", LAYERS)
@@ -149,6 +151,29 @@ def test_strides_other_memory_and_given_outputs():
     out = torch.empty_like(x)
     got = X.few_token_layer(xs, ls, w1, w3, ws, 2, out=out)
     assert got[0] is out and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_gradients_and_overlaps_are_refused():
+    T, d, F, E = 3, 64, 32, 4
+    args = _case(T, d, F, E, E, "bf16", 33)
+    adapter, lora = _lora(T, d, F, E, 2, (8, 8, 8), "bf16", 34)
+    for t in (*args, lora[0].A, lora[1].B, lora[2].scale):
+        t.requires_grad_()
+        with pytest.raises(RuntimeError, match="autograd"):
+            X.few_token_layer(*args, 2, adapter=adapter, lora=lora)
+        with torch.no_grad():
+            X.few_token_layer(*args, 2, adapter=adapter, lora=lora)
+        t.requires_grad_(False)
+    for out in (args[0], args[2].view(-1)[:T * d].view(T, d), lora[2].B.view(-1)[:T * d].view(T, d)):
+        with pytest.raises(ValueError, match="overlap"):
+            X.few_token_layer(*args, 2, adapter=adapter, lora=lora, out=out)
+    with pytest.raises(ValueError, match="together"):
+        X.few_token_layer(*args, 2, adapter=adapter)
+    with pytest.raises(ValueError, match="adapters"):
+        X.few_token_layer(*args, 2, adapter=adapter, lora=(lora[2], lora[1], lora[0]))
+    for k in (0, 5):
+        with pytest.raises(X.mok.MokError):
+            X.few_token_layer(*args, k)
 
 
 def test_two_streams_and_captured_graphs():

@@ -50,6 +50,11 @@ ROWS = [(1, 64, 64, 1, 16, "bf16"), (1, 1, 1, 1, 1, "f32"), (3, 33, 17, 2, 3, "b
         (200, 320, 300, 2, 128, "bf16"), (90, 72, 90, 1, 100, "f16"), (1000, 128, 256, 7, 16, "bf16"),
         (700, 4096, 64, 3, 16, "bf16"), (33, 64, 64, 300, 4, "bf16"), (2000, 40, 48, 1000, 2, "f32"),
         (5, 2048, 2048, 1024, 8, "f16")]
+# how the rows are shared out: one group a tile of 33 to 64 rows, even ranges across
+# groups (many rows; a high rank; more groups than tiles fit beside), many groups
+SHARES = [(9000, 64, 72, 4, 16, "bf16"), (13000, 40, 33, 20, 5, "f16"), (20000, 64, 64, 5, 24, "bf16"),
+          (40000, 32, 48, 3, 4, "bf16"), (17500, 48, 40, 6, 100, "f16"), (12000, 32, 24, 600, 2, "f32"),
+          (3000, 136, 260, 100, 16, "bf16"), (60, 96, 1100, 40, 20, "f32")]
 
 
 @pytest.mark.parametrize("T,K,N,G,r,dt", ROWS)
@@ -77,6 +82,41 @@ def test_gradients_in_token_order(T, K, N, G, r, dt):
         close(dB, ref["dB"][0], ref["dB"][1] + 2 * U * ref["dB"][0].abs(), "dB")
         again = X.lora_rows_backward(dout, x, u, amap, w, base=b)
         assert all(torch.equal(p, q) for p, q in zip((dx, dA, dB), again))
+
+
+@pytest.mark.parametrize("T,K,N,G,r,dt", SHARES)
+def test_every_way_the_rows_are_shared_out(T, K, N, G, r, dt):
+    note(f"lora share T={T} K={K} N={N} G={G} r={r} {dt}")
+    ids, x, y, w = _case(T, K, N, G, r, dt, T + G)
+    amap = _map(ids, G)
+    _, u = _check(ids, x, y, w, dt, amap, "out")
+    ref = lora_grad64(y, x, u_of(u, amap), ids, w.A, w.B, w.scale)
+    dx, dA, dB = X.lora_rows_backward(y, x, u, amap, w)
+    close(dx, ref["dx"][0], rounded(*ref["dx"], dt), "dx")
+    close(dA, ref["dA"][0], ref["dA"][1] + 2 * U * ref["dA"][0].abs(), "dA")
+    close(dB, ref["dB"][0], ref["dB"][1] + 2 * U * ref["dB"][0].abs(), "dB")
+
+
+def test_gradients_and_overlaps_are_refused():
+    T, K, N, G, r = 12, 64, 64, 2, 8
+    ids, x, y, w = _case(T, K, N, G, r, "bf16", 13)
+    amap = _map(ids, G)
+    for t in (x, y, w.A, w.B, w.scale):
+        t.requires_grad_()
+        with pytest.raises(RuntimeError, match="autograd"):
+            X.lora_rows(x, amap, w, y=y)
+        with torch.no_grad():
+            X.lora_rows(x, amap, w, y=y)
+        t.requires_grad_(False)
+    both = torch.zeros((2 * T, N), dtype=x.dtype, device="cuda")
+    for base, out in ((both[:T], both[4:T + 4]), (None, x), (y, w.A.view(-1)[:T * N].view(T, N))):
+        with pytest.raises(ValueError, match="overlap"):
+            X.lora_rows(x, amap, w, y=base, out=out)
+    _, u = X.lora_rows(x, amap, w, save=True)
+    with pytest.raises(ValueError, match="overlap"):
+        X.lora_rows_backward(y, x, u, amap, w, out=x)
+    with pytest.raises(ValueError, match="u \\[rows, r\\]"):
+        X.lora_rows_backward(y, x, u[:, :4], amap, w)
 
 
 @pytest.mark.parametrize("kind", ["one", "none"])
