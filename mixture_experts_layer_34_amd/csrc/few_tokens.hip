@@ -9,8 +9,9 @@
 //
 // Bound by reading each chosen expert's three matrices once.  What that takes:
 //  - Routing needs no launch: every workgroup of UP routes the tokens itself
-//    (the logits are a few KB in L2) and then takes units of (expert, sixteen
-//    columns of h) in turn.  Workgroup 0 writes the routing out.
+//    (the logits are a few KB in L2) and then takes tiles of up to sixteen columns
+//    of h in turn.  Workgroup 0 writes the routing out, and the experts' pairs for
+//    DOWN.
 //  - No sort and no gather: an expert has a token once at most, so the sixteen
 //    columns of a matrix instruction are the sixteen tokens whatever the expert.
 //    Columns of tokens without the expert repeat the row of one that has it
@@ -22,6 +23,8 @@
 //    their fp32 sums meet in LDS in wave order.
 // h is rounded once to the type of the weights, as the layer's own H is; all
 // sums are fp32 in a fixed order.
+// At d 4096, F 1536, 8 of 128 experts (bf16): one token 39 + 20 us (201 and 101 MB;
+// 5.1 TB/s together), sixteen 525 us (3.1 GB, 5.9 TB/s).
 #include "few_tokens.h"
 #include "frag.h"
 #include "mok_internal.h"

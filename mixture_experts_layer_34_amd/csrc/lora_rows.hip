@@ -6,21 +6,23 @@
 //   dA_g = s_g sum_q du_q x_q^T,  dB_g = s_g sum_q dout_q u_q^T
 // over the rows q of adapter g.
 //
-// All of it is bound by moving the rows once: with ranks of 8 to 128 beside
-// widths of thousands the products are a few percent of what the matrix cores
-// do in that time.  Four kernels:
-//  - rank (u and du): a workgroup takes a tile of one adapter's rows, its waves
-//    share K and meet in LDS; with few rows K is split over workgroups too, whose
-//    fp32 parts the next kernel adds in order (no atomics).
-//  - add (out and dx): the transposed product B u^T, so that a lane holds sixteen
-//    neighbouring columns of one row: 128 bytes a row and wave, y in, out back.  A
-//    wave keeps its 64 rows of B in registers and runs over its rows.  u enters
-//    16-bit matrix instructions as a high and a low part (a K of 2 r), so that it
-//    loses nothing next to out's own rounding.
-//  - grad (dA and dB): K is the rows there.  v_mfma_f32_16x16x4 takes one value
-//    of each operand a lane, so the j-th elements of sixteen lanes' 16-byte loads
-//    are an operand as they are: no transposing, and u and du keep their 32 bits.
-//  - prepare: A^T and B^T for the backward pass, which then runs the first two
+// All of it is bound by moving the rows once: with ranks of 8 to 32 beside widths
+// of thousands the products are a few percent of what the matrix cores do in that
+// time.  The kernels, with what they take at 8192 rows of 4096 bf16 columns and
+// rank 16 (a copy of one such matrix into another takes 24-26 us there):
+//  - rank (u and du; 17.6-20.6 us): a workgroup takes a tile of one adapter's rows,
+//    its waves share K and meet in LDS; with few rows K is split over workgroups too,
+//    whose fp32 parts the next kernel adds in order (no atomics).
+//  - add (out and dx; 37 us): the transposed product B u^T, so that a lane holds
+//    neighbouring columns of one row, y in, out back.  A wave keeps the B of its
+//    128 columns in registers and runs over its rows.  u enters 16-bit matrix
+//    instructions as a high and a low part (a K of 2 r), so that it loses nothing
+//    next to out's own rounding.
+//  - grad (dA and dB; 38 us for both matrices, 3.5 TB/s): K is the rows there.
+//    v_mfma_f32_16x16x4 takes one value of each operand a lane, so the j-th elements
+//    of sixteen lanes' 16-byte loads are an operand as they are: no transposing, and u
+//    and du keep their 32 bits.  From rank 64 on that instruction's rate bounds it.
+//  - prepare (5 us): A^T and B^T for the backward pass, which then runs the first two
 //    kernels on them (du: rank with B^T; dx: add with A^T).
 #include "frag.h"
 #include "lora_rows.h"
