@@ -326,10 +326,18 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
         acc[1] = mma<DT>(load16<DT>(p3 + o), vx, acc[1]);
       }
     if (full * STEP < a.d && w == 0) {
-      const int left = a.d - full * STEP - g * KE, o = full * STEP * S;
-      const u32x4_t vx = load_part<DT>(px + o, left);
-      acc[0] = mma<DT>(load_part<DT>(p1 + o, left), vx, acc[0]);
-      acc[1] = mma<DT>(load_part<DT>(p3 + o, left), vx, acc[1]);
+      const int k = full * STEP + g * KE;
+      if (a.d >= KE) {
+        const int at = tail_at<DT>(k, a.d), o = (at - g * KE) * S;  // the pointers stand at element g KE
+        const u32x4_t v1 = load16<DT>(p1 + o), v3 = load16<DT>(p3 + o), vx = but_first<DT>(load16<DT>(px + o), k - at);
+        acc[0] = mma<DT>(v1, vx, acc[0]);
+        acc[1] = mma<DT>(v3, vx, acc[1]);
+      } else {
+        const int left = a.d - k, o = full * STEP * S;
+        const u32x4_t vx = load_part<DT>(px + o, left);
+        acc[0] = mma<DT>(load_part<DT>(p1 + o, left), vx, acc[0]);
+        acc[1] = mma<DT>(load_part<DT>(p3 + o, left), vx, acc[1]);
+      }
     }
     const int l = a.adapter && pair >= 0 ? adapter_of(a, i16) : -1;
     if (l >= 0 && w < 4) {  // wave w adds the adapter's share of row 4 g + w of the tile
@@ -380,7 +388,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
 // A workgroup owns `cols` columns of out, up to 16 NT: as many as give every
 // compute unit the same share.
 constexpr int kDownWaves = 8;
-template <int DT, int NT, bool WHOLE>
+// LONG: F >= KE.
+template <int DT, int NT, bool WHOLE, bool LONG>
 __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, int cols) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int KE = kFragElems<DT>, STEP = kFragStep<DT>, S = Elem<DT>::kBytes, U = kUnroll, NW = kDownWaves;
@@ -417,7 +426,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
   u32x4_t qw[2][U][NT], qh[2][U];
   int left[2];  // !WHOLE: elements of F from the lane's first of the chunk
   // WHOLE: F is a multiple of KE, a lane's 16 bytes lie in F or past it; a
-  // lane past it reads the row's first bytes and zeros of h.
+  // lane past it reads the row's first bytes and zeros of h.  Otherwise the lane
+  // that F ends in reads the row's last 16 bytes and moves them to their places.
   auto load = [&](int buf) {
     const int e = __builtin_amdgcn_readfirstlane(s_expert[slot]);
     const int pair = s_pair[slot * 16 + i16];
@@ -431,6 +441,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
         if constexpr (WHOLE) qw[buf][j][q] = load16<DT>(wp + wrow[q] + (k < a.F ? k : 0) * S);
+        else if constexpr (LONG) qw[buf][j][q] = load16<DT>(wp + wrow[q] + tail_at<DT>(k, a.F) * S);
         else qw[buf][j][q] = load_part<DT>(wp + wrow[q] + k * S, k < a.F ? a.F - k : 0);
       }
       const auto v = __builtin_amdgcn_raw_buffer_load_b128(hrs, k < a.F ? hoff + k * S : 0xC0000000u, 0, 0);
@@ -445,7 +456,13 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
   auto mul = [&](int buf) {
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      if constexpr (!WHOLE) qh[buf][j] = first_elems<DT>(qh[buf][j], left[buf] - j * STEP);  // past F nothing was written
+      if constexpr (!WHOLE) {
+        const int in = left[buf] - j * STEP;
+        qh[buf][j] = first_elems<DT>(qh[buf][j], in);  // past F nothing was written
+        if constexpr (LONG)
+#pragma unroll
+          for (int q = 0; q < NT; ++q) qw[buf][j][q] = shift_elems<DT>(qw[buf][j][q], in < KE ? KE - in : 0);
+      }
 #pragma unroll
       for (int q = 0; q < NT; ++q) acc[q] = mma<DT>(qw[buf][j][q], qh[buf][j], acc[q]);
     }
@@ -548,8 +565,8 @@ template <int DT, int EPL, bool DOWN> __global__ __launch_bounds__(256) void few
 #endif
 }
 
-template <int DT, int NT, bool WHOLE> void down(const FewTokens& a, int cols, int slots, hipStream_t s) {
-  hipLaunchKernelGGL((few_down_kernel<DT, NT, WHOLE>), dim3((a.d + cols - 1) / cols), dim3(64 * kDownWaves),
+template <int DT, int NT, bool WHOLE, bool LONG> void down(const FewTokens& a, int cols, int slots, hipStream_t s) {
+  hipLaunchKernelGGL((few_down_kernel<DT, NT, WHOLE, LONG>), dim3((a.d + cols - 1) / cols), dim3(64 * kDownWaves),
                      (size_t)slots * 34 + 64, s, a, cols);
 }
 
@@ -579,9 +596,11 @@ template <int DT, int EPL> hipError_t run(const FewTokens& a, hipStream_t s) {
   // in as few rounds of them as 32 columns each allow
   const int share = (a.d + 32 * kNumCUs - 1) / (32 * kNumCUs) * kNumCUs, cols = (a.d + share - 1) / share;
   if (a.F % kFragElems<DT> == 0)
-    cols <= 16 ? down<DT, 1, true>(a, cols, slots, s) : down<DT, 2, true>(a, cols, slots, s);
+    cols <= 16 ? down<DT, 1, true, true>(a, cols, slots, s) : down<DT, 2, true, true>(a, cols, slots, s);
+  else if (a.F > kFragElems<DT>)
+    cols <= 16 ? down<DT, 1, false, true>(a, cols, slots, s) : down<DT, 2, false, true>(a, cols, slots, s);
   else
-    cols <= 16 ? down<DT, 1, false>(a, cols, slots, s) : down<DT, 2, false>(a, cols, slots, s);
+    cols <= 16 ? down<DT, 1, false, false>(a, cols, slots, s) : down<DT, 2, false, false>(a, cols, slots, s);
   return hipGetLastError();
 }
 

@@ -94,6 +94,42 @@ template <int DT> __device__ __forceinline__ u32x4_t first_elems(u32x4_t v, int 
   return v;
 }
 
+// v with zeros in place of its first n elements (n >= 0).
+template <int DT> __device__ __forceinline__ u32x4_t but_first(u32x4_t v, int n) {
+  constexpr int PER = 4 / Elem<DT>::kBytes;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (PER == 1) v[j] = j >= n ? v[j] : 0u;
+    else v[j] = 2 * j >= n ? v[j] : 2 * j + 1 >= n ? v[j] & 0xFFFF0000u : 0u;
+  }
+  return v;
+}
+
+// The step that a row of n elements (n >= KE) ends in, a lane's elements from k
+// on: both operands are read from `tail_at`, whole and inside the row, and one of
+// them gets zeros for the elements that another lane or step has counted.
+template <int DT> __device__ __forceinline__ int tail_at(int k, int n) {
+  return k < n - kFragElems<DT> ? k : n - kFragElems<DT>;
+}
+
+// v moved down by n elements (0 <= n; zeros come in, all of it for n >= KE).
+template <int DT> __device__ __forceinline__ u32x4_t shift_elems(u32x4_t v, int n) {
+  constexpr int PER = 4 / Elem<DT>::kBytes;
+  const int q = n / PER;
+  u32x4_t t;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) t[j] = q & 1 ? (j < 3 ? v[j < 3 ? j + 1 : 3] : 0u) : v[j];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = q >= 4 ? 0u : q & 2 ? (j < 2 ? t[j < 2 ? j + 2 : 3] : 0u) : t[j];
+  if constexpr (PER == 2) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t[j] = (v[j] >> 16) | (j < 3 ? v[j < 3 ? j + 1 : 3] << 16 : 0u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = n & 1 ? t[j] : v[j];
+  }
+  return v;
+}
+
 // KE elements as fp32 and back (rounded to nearest even).
 template <int DT> __device__ __forceinline__ void widen(u32x4_t v, float* f) {
   Vec<DT, kFragElems<DT>> e;

@@ -229,11 +229,21 @@ template <int DT, int RT, int M> __global__ __launch_bounds__(64 * kRankWaves) v
         mul(0, 0);
       }
     if (s1 > full && w == 0) {
-      const int left = a.K - full * STEP - g4 * KE, o = (full - s0) * STEP * S;
+      const int k = full * STEP + g4 * KE;
+      if (a.K >= KE) {
+        const int at_k = tail_at<DT>(k, a.K), o = (at_k - g4 * KE - s0 * STEP) * S;  // the pointers stand at s0 STEP + g4 KE
 #pragma unroll
-      for (int m = 0; m < M; ++m) qx[0][0][m] = load_part<DT>(px[m] + o, left);
+        for (int m = 0; m < M; ++m) qx[0][0][m] = load16<DT>(px[m] + o);
 #pragma unroll
-      for (int q = 0; q < RT; ++q) qa[0][0][q] = load_part<DT>(pa[q] + o, left);
+        for (int q = 0; q < RT; ++q) qa[0][0][q] = load16<DT>(pa[q] + o);
+#pragma unroll
+        for (int m = 0; m < M; ++m) qx[0][0][m] = but_first<DT>(qx[0][0][m], k - at_k);
+      } else {
+#pragma unroll
+        for (int m = 0; m < M; ++m) qx[0][0][m] = load_part<DT>(px[m], a.K - k);
+#pragma unroll
+        for (int q = 0; q < RT; ++q) qa[0][0][q] = load_part<DT>(pa[q], a.K - k);
+      }
       mul(0, 0);
     }
     if (w > 0)
