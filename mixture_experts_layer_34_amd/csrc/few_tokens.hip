@@ -197,7 +197,8 @@ template <int DT> __device__ __forceinline__ float rank_dot(const char* b, const
 // LDS of UP: idx and gate [P] each, then the tables.
 __host__ __device__ inline size_t up_lds(int P, int slots) { return (size_t)P * 8 + (size_t)slots * 34 + 64; }
 
-template <int DT, int EPL>
+// ODD: rows of x, W1 and W3 of an odd number of 16-bit elements.
+template <int DT, int EPL, bool ODD>
 __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int KE = kFragElems<DT>, STEP = kFragStep<DT>, S = Elem<DT>::kBytes, U = kUnroll;
@@ -266,14 +267,14 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
     t.px = (const char*)a.x + tx * row_bytes + (int64_t)(g * KE) * S;
     return t;
   };
-  u32x4_t q1[2][U], q3[2][U], qx[2][U];
+  Quad<DT, ODD> q1[2][U], q3[2][U], qx[2][U];
   auto load = [&](int buf, const char* p1, const char* p3, const char* px, int c) {
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int o = ((c * kUpWaves + w) * U + j) * STEP * S;
-      q1[buf][j] = load16<DT>(p1 + o);
-      q3[buf][j] = load16<DT>(p3 + o);
-      qx[buf][j] = load16<DT>(px + o);
+      q1[buf][j].load(p1 + o);
+      q3[buf][j].load(p3 + o);
+      qx[buf][j].load(px + o);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -296,11 +297,13 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
     const int n0 = t.n0, cols = t.cols, e = t.e, pair = t.pair;
     const char *p1 = t.p1, *p3 = t.p3, *px = t.px;
     f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    const uint32_t h1 = shift_of<ODD>(p1), h3 = shift_of<ODD>(p3), hx = shift_of<ODD>(px);
     auto mul = [&](int buf) {
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        acc[0] = mma<DT>(q1[buf][j], qx[buf][j], acc[0]);
-        acc[1] = mma<DT>(q3[buf][j], qx[buf][j], acc[1]);
+        const u32x4_t vx = qx[buf][j].get(hx);
+        acc[0] = mma<DT>(q1[buf][j].get(h1), vx, acc[0]);
+        acc[1] = mma<DT>(q3[buf][j].get(h3), vx, acc[1]);
       }
       __builtin_amdgcn_sched_barrier(0);
     };
@@ -388,8 +391,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
 // A workgroup owns `cols` columns of out, up to 16 NT: as many as give every
 // compute unit the same share.
 constexpr int kDownWaves = 8;
-// LONG: F >= KE.
-template <int DT, int NT, bool WHOLE, bool LONG>
+// LONG: F >= KE.  ODD: rows of W2 of an odd number of 16-bit elements.
+template <int DT, int NT, bool WHOLE, bool LONG, bool ODD>
 __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, int cols) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int KE = kFragElems<DT>, STEP = kFragStep<DT>, S = Elem<DT>::kBytes, U = kUnroll, NW = kDownWaves;
@@ -423,7 +426,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
   f32x4_t acc[NT];
 #pragma unroll
   for (int q = 0; q < NT; ++q) acc[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  u32x4_t qw[2][U][NT], qh[2][U];
+  Quad<DT, ODD> qw[2][U][NT];
+  u32x4_t qh[2][U];
+  uint32_t shift[2][U][NT];
   int left[2];  // !WHOLE: elements of F from the lane's first of the chunk
   // WHOLE: F is a multiple of KE, a lane's 16 bytes lie in F or past it; a
   // lane past it reads the row's first bytes and zeros of h.  Otherwise the lane
@@ -440,9 +445,14 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
       const int k = (ch * U + j) * STEP + g * KE;
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
-        if constexpr (WHOLE) qw[buf][j][q] = load16<DT>(wp + wrow[q] + (k < a.F ? k : 0) * S);
-        else if constexpr (LONG) qw[buf][j][q] = load16<DT>(wp + wrow[q] + tail_at<DT>(k, a.F) * S);
-        else qw[buf][j][q] = load_part<DT>(wp + wrow[q] + k * S, k < a.F ? a.F - k : 0);
+        if constexpr (LONG) {
+          const char* from = wp + wrow[q] + (WHOLE ? (k < a.F ? k : 0) : tail_at<DT>(k, a.F)) * S;
+          qw[buf][j][q].load(from);
+          shift[buf][j][q] = shift_of<ODD>(from);
+        } else {
+          qw[buf][j][q].v = load_part<DT>(wp + wrow[q] + k * S, k < a.F ? a.F - k : 0);
+          shift[buf][j][q] = 0;
+        }
       }
       const auto v = __builtin_amdgcn_raw_buffer_load_b128(hrs, k < a.F ? hoff + k * S : 0xC0000000u, 0, 0);
       qh[buf][j] = u32x4_t{(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
@@ -459,12 +469,16 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
       if constexpr (!WHOLE) {
         const int in = left[buf] - j * STEP;
         qh[buf][j] = first_elems<DT>(qh[buf][j], in);  // past F nothing was written
-        if constexpr (LONG)
-#pragma unroll
-          for (int q = 0; q < NT; ++q) qw[buf][j][q] = shift_elems<DT>(qw[buf][j][q], in < KE ? KE - in : 0);
       }
 #pragma unroll
-      for (int q = 0; q < NT; ++q) acc[q] = mma<DT>(qw[buf][j][q], qh[buf][j], acc[q]);
+      for (int q = 0; q < NT; ++q) {
+        u32x4_t vw = qw[buf][j][q].get(shift[buf][j][q]);
+        if constexpr (!WHOLE && LONG) {
+          const int in = left[buf] - j * STEP;
+          vw = shift_elems<DT>(vw, in < KE ? KE - in : 0);
+        }
+        acc[q] = mma<DT>(vw, qh[buf][j], acc[q]);
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -565,9 +579,25 @@ template <int DT, int EPL, bool DOWN> __global__ __launch_bounds__(256) void few
 #endif
 }
 
-template <int DT, int NT, bool WHOLE, bool LONG> void down(const FewTokens& a, int cols, int slots, hipStream_t s) {
-  hipLaunchKernelGGL((few_down_kernel<DT, NT, WHOLE, LONG>), dim3((a.d + cols - 1) / cols), dim3(64 * kDownWaves),
+template <int DT, int NT, bool WHOLE, bool LONG, bool ODD> void down(const FewTokens& a, int cols, int slots, hipStream_t s) {
+  hipLaunchKernelGGL((few_down_kernel<DT, NT, WHOLE, LONG, ODD>), dim3((a.d + cols - 1) / cols), dim3(64 * kDownWaves),
                      (size_t)slots * 34 + 64, s, a, cols);
+}
+
+template <int DT, int EPL, bool ODD> void up(const FewTokens& a, int P, int slots, hipStream_t s) {
+  static const int per_cu = [] {
+    int n = 0;
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, few_up_kernel<DT, EPL, ODD>, 64 * kUpWaves, 8192) !=
+            hipSuccess || n < 1)
+      n = 1;
+    return n;
+  }();
+  // as many workgroups as are resident at once, in whole rounds of the compute
+  // units; of those the kernel uses what the chosen experts' columns take
+  const int64_t units = ((int64_t)slots * a.F + 15) / 16, cap = (int64_t)kNumCUs * per_cu;
+  const int64_t rounds = (units + kNumCUs - 1) / kNumCUs * kNumCUs;
+  hipLaunchKernelGGL((few_up_kernel<DT, EPL, ODD>), dim3((unsigned)(rounds < cap ? rounds : cap)), dim3(64 * kUpWaves),
+                     up_lds(P, slots), s, a);
 }
 
 template <int DT, int EPL> hipError_t run(const FewTokens& a, hipStream_t s) {
@@ -577,30 +607,22 @@ template <int DT, int EPL> hipError_t run(const FewTokens& a, hipStream_t s) {
     if (a.lora[m].A) ranks += few_u_width(a.lora[m].r) / 4;
   if (a.adapter && ranks)
     hipLaunchKernelGGL((few_rank_kernel<DT, EPL, false>), dim3(P, ranks), dim3(256), 0, s, a);
-  static const int per_cu = [] {
-    int n = 0;
-    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, few_up_kernel<DT, EPL>, 64 * kUpWaves, 8192) != hipSuccess ||
-        n < 1)
-      n = 1;
-    return n;
-  }();
-  // as many workgroups as are resident at once, in whole rounds of the compute
-  // units; of those the kernel uses what the chosen experts' columns take
-  const int64_t units = ((int64_t)slots * a.F + 15) / 16, cap = (int64_t)kNumCUs * per_cu;
-  const int64_t rounds = (units + kNumCUs - 1) / kNumCUs * kNumCUs;
-  hipLaunchKernelGGL((few_up_kernel<DT, EPL>), dim3((unsigned)(rounds < cap ? rounds : cap)), dim3(64 * kUpWaves),
-                     up_lds(P, slots), s, a);
+  if (DT != 0 && a.d % 2) up<DT, EPL, DT != 0>(a, P, slots, s);
+  else up<DT, EPL, false>(a, P, slots, s);
   if (a.adapter && a.lora[2].A)
     hipLaunchKernelGGL((few_rank_kernel<DT, EPL, true>), dim3(P, few_u_width(a.lora[2].r) / 4), dim3(256), 0, s, a);
   // columns of a workgroup of DOWN: d shared out evenly over the compute units,
   // in as few rounds of them as 32 columns each allow
   const int share = (a.d + 32 * kNumCUs - 1) / (32 * kNumCUs) * kNumCUs, cols = (a.d + share - 1) / share;
-  if (a.F % kFragElems<DT> == 0)
-    cols <= 16 ? down<DT, 1, true, true>(a, cols, slots, s) : down<DT, 2, true, true>(a, cols, slots, s);
-  else if (a.F > kFragElems<DT>)
-    cols <= 16 ? down<DT, 1, false, true>(a, cols, slots, s) : down<DT, 2, false, true>(a, cols, slots, s);
+  constexpr int KE = kFragElems<DT>;
+  if (a.F % KE == 0)
+    cols <= 16 ? down<DT, 1, true, true, false>(a, cols, slots, s) : down<DT, 2, true, true, false>(a, cols, slots, s);
+  else if (a.F < KE)
+    cols <= 16 ? down<DT, 1, false, false, false>(a, cols, slots, s) : down<DT, 2, false, false, false>(a, cols, slots, s);
+  else if (DT != 0 && a.F % 2)
+    cols <= 16 ? down<DT, 1, false, true, DT != 0>(a, cols, slots, s) : down<DT, 2, false, true, DT != 0>(a, cols, slots, s);
   else
-    cols <= 16 ? down<DT, 1, false, false>(a, cols, slots, s) : down<DT, 2, false, false>(a, cols, slots, s);
+    cols <= 16 ? down<DT, 1, false, true, false>(a, cols, slots, s) : down<DT, 2, false, true, false>(a, cols, slots, s);
   return hipGetLastError();
 }
 

@@ -130,7 +130,8 @@ __device__ __forceinline__ int token_of(const LoraMap& m, int row) { return toke
 constexpr int kRankWaves = 4;
 
 // grid: (tiles of a.height rows of one group, or ranges of rows, in eights; shares of K)
-template <int DT, int RT, int M> __global__ __launch_bounds__(64 * kRankWaves) void lora_rank_kernel(LoraRank a) {
+// ODD: rows of an odd number of 16-bit elements.
+template <int DT, int RT, int M, bool ODD> __global__ __launch_bounds__(64 * kRankWaves) void lora_rank_kernel(LoraRank a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int KE = kFragElems<DT>, STEP = kFragStep<DT>, S = Elem<DT>::kBytes;
   constexpr int U = RT >= 4 ? 1 : RT == 2 || M > 2 ? 2 : 4;  // K steps of a chunk
@@ -182,19 +183,24 @@ template <int DT, int RT, int M> __global__ __launch_bounds__(64 * kRankWaves) v
     for (int m = 0; m < M; ++m)
 #pragma unroll
       for (int q = 0; q < RT; ++q) acc[m][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    u32x4_t qx[2][U][M], qa[2][U][RT];
+    Quad<DT, ODD> qx[2][U][M], qa[2][U][RT];
     auto load = [&](int buf, int j, int step) {
       const int o = step * STEP * S;
 #pragma unroll
-      for (int m = 0; m < M; ++m) qx[buf][j][m] = load16<DT>(px[m] + o);
+      for (int m = 0; m < M; ++m) qx[buf][j][m].load(px[m] + o);
 #pragma unroll
-      for (int q = 0; q < RT; ++q) qa[buf][j][q] = load16<DT>(pa[q] + o);
+      for (int q = 0; q < RT; ++q) qa[buf][j][q].load(pa[q] + o);
     };
     auto mul = [&](int buf, int j) {
+      u32x4_t vx[M];
 #pragma unroll
-      for (int m = 0; m < M; ++m)
+      for (int m = 0; m < M; ++m) vx[m] = qx[buf][j][m].get(shift_of<ODD>(px[m]));
 #pragma unroll
-        for (int q = 0; q < RT; ++q) acc[m][q] = mma<DT>(qa[buf][j][q], qx[buf][j][m], acc[m][q]);
+      for (int q = 0; q < RT; ++q) {
+        const u32x4_t va = qa[buf][j][q].get(shift_of<ODD>(pa[q]));
+#pragma unroll
+        for (int m = 0; m < M; ++m) acc[m][q] = mma<DT>(va, vx[m], acc[m][q]);
+      }
     };
     // Chunk c + 1 is in flight while chunk c is multiplied.  No load stands under a
     // condition (the last one is asked for again): behind a branch the compiler
@@ -230,21 +236,25 @@ template <int DT, int RT, int M> __global__ __launch_bounds__(64 * kRankWaves) v
       }
     if (s1 > full && w == 0) {
       const int k = full * STEP + g4 * KE;
+      u32x4_t vx[M], va[RT];
       if (a.K >= KE) {
         const int at_k = tail_at<DT>(k, a.K), o = (at_k - g4 * KE - s0 * STEP) * S;  // the pointers stand at s0 STEP + g4 KE
 #pragma unroll
-        for (int m = 0; m < M; ++m) qx[0][0][m] = load16<DT>(px[m] + o);
+        for (int m = 0; m < M; ++m) vx[m] = load16<DT>(px[m] + o);
 #pragma unroll
-        for (int q = 0; q < RT; ++q) qa[0][0][q] = load16<DT>(pa[q] + o);
+        for (int q = 0; q < RT; ++q) va[q] = load16<DT>(pa[q] + o);
 #pragma unroll
-        for (int m = 0; m < M; ++m) qx[0][0][m] = but_first<DT>(qx[0][0][m], k - at_k);
+        for (int m = 0; m < M; ++m) vx[m] = but_first<DT>(vx[m], k - at_k);
       } else {
 #pragma unroll
-        for (int m = 0; m < M; ++m) qx[0][0][m] = load_part<DT>(px[m], a.K - k);
+        for (int m = 0; m < M; ++m) vx[m] = load_part<DT>(px[m], a.K - k);
 #pragma unroll
-        for (int q = 0; q < RT; ++q) qa[0][0][q] = load_part<DT>(pa[q], a.K - k);
+        for (int q = 0; q < RT; ++q) va[q] = load_part<DT>(pa[q], a.K - k);
       }
-      mul(0, 0);
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int q = 0; q < RT; ++q) acc[m][q] = mma<DT>(va[q], vx[m], acc[m][q]);
     }
     if (w > 0)
 #pragma unroll
@@ -755,7 +765,11 @@ RankShare rank_share(int rows, int G, int r) {
 }
 
 template <int DT, int RT, int M> hipError_t rank_m(const LoraRank& a, int places, hipStream_t s) {
-  hipLaunchKernelGGL((lora_rank_kernel<DT, RT, M>), dim3((places + 7) / 8 * 8, a.splits), dim3(64 * kRankWaves), 0, s, a);
+  const dim3 grid((places + 7) / 8 * 8, a.splits);
+  if (DT != 0 && a.K % 2)
+    hipLaunchKernelGGL((lora_rank_kernel<DT, RT, M, DT != 0>), grid, dim3(64 * kRankWaves), 0, s, a);
+  else
+    hipLaunchKernelGGL((lora_rank_kernel<DT, RT, M, false>), grid, dim3(64 * kRankWaves), 0, s, a);
   return hipGetLastError();
 }
 template <int DT, int RT> hipError_t rank_of(const LoraRank& b, hipStream_t s) {
