@@ -55,6 +55,22 @@ def test_layer(T, d, F, E, k, dt, gating, renorm):
     _check(_case(T, d, F, E, E, dt, T + d + F), k, dt, gating=gating, renorm=renorm)
 
 
+@pytest.mark.parametrize("T,d,F,dt", [(8, 2111, 1411, "bf16"), (16, 1409, 2113, "f16"), (3, 4097, 259, "bf16"),
+                                      (5, 769, 4099, "f16"), (9, 2110, 1410, "bf16")])
+def test_long_rows_off_their_dwords(T, d, F, dt):
+    """Odd numbers of 16-bit elements, with whole turns of the loads' rings."""
+    note(f"few tokens, odd rows T={T} d={d} F={F} {dt}")
+    args = _case(T, d, F, 5, 5, dt, T + d)
+    _check(args, 3, dt)
+    adapter, lora = _lora(T, d, F, 5, 2, (16, 5, 16), dt, d)
+    _check(args, 3, dt, adapter=adapter, lora=lora)
+    args[0][1, d - 1] = float("nan")  # the last element of a row, the neighbour of the next
+    got = X.few_token_layer(*args, 3)[0]
+    args[0][1, d - 1] = 0
+    keep = [t for t in range(T) if t != 1]
+    assert torch.equal(got[keep], X.few_token_layer(*args, 3)[0][keep]) and not torch.isfinite(got[1]).all()
+
+
 @pytest.mark.parametrize("gating,renorm", [("softmax", True), ("sigmoid", False)])
 @pytest.mark.parametrize("T,E,eb,n,k", [(5, 16, 4, 3, 2), (16, 64, 60, 4, 8), (1, 8, 7, 1, 1), (12, 128, 0, 16, 8)])
 def test_share_of_the_experts(T, E, eb, n, k, gating, renorm):

@@ -97,6 +97,25 @@ def test_every_way_the_rows_are_shared_out(T, K, N, G, r, dt):
     close(dB, ref["dB"][0], ref["dB"][1] + 2 * U * ref["dB"][0].abs(), "dB")
 
 
+@pytest.mark.parametrize("T,K,N,G,r,dt", [(70, 4095, 2047, 3, 16, "bf16"), (300, 1411, 2049, 5, 40, "f16"),
+                                          (2, 8191, 33, 2, 7, "bf16"), (33, 2110, 1410, 2, 16, "f16")])
+def test_long_rows_off_their_dwords(T, K, N, G, r, dt):
+    """Odd numbers of 16-bit elements, with whole turns of the loads' rings."""
+    note(f"lora, odd rows T={T} K={K} N={N} G={G} r={r} {dt}")
+    ids, x, y, w = _case(T, K, N, G, r, dt, T + K, bare=0.0)
+    amap = _map(ids, G)
+    _, u = _check(ids, x, y, w, dt, amap, "out")
+    ref = lora_grad64(y, x, u_of(u, amap), ids, w.A, w.B, w.scale)
+    dx, dA, dB = X.lora_rows_backward(y, x, u, amap, w)
+    close(dx, ref["dx"][0], rounded(*ref["dx"], dt), "dx")
+    close(dA, ref["dA"][0], ref["dA"][1] + 2 * U * ref["dA"][0].abs(), "dA")
+    close(dB, ref["dB"][0], ref["dB"][1] + 2 * U * ref["dB"][0].abs(), "dB")
+    clean = X.lora_rows(x, amap, w, y=y)
+    x[0, K - 1] = float("nan")  # the last element of a row, the neighbour of the next
+    got = X.lora_rows(x, amap, w, y=y)
+    assert torch.equal(got[1:], clean[1:])
+
+
 def test_gradients_and_overlaps_are_refused():
     T, K, N, G, r = 12, 64, 64, 2, 8
     ids, x, y, w = _case(T, K, N, G, r, "bf16", 13)
