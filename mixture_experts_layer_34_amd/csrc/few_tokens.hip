@@ -16,13 +16,17 @@
 //    columns of a matrix instruction are the sixteen tokens whatever the expert.
 //    Columns of tokens without the expert repeat the row of one that has it
 //    (no traffic) and are not stored.
-//  - No combine: with the gate applied to h in fp32, before its only rounding,
-//    the sum over a token's experts is a product whose K runs over all the
-//    chosen experts' F, zeros standing in for the pairs that are not.  A
-//    workgroup of DOWN owns sixteen columns of out, its waves share that K, and
-//    their fp32 sums meet in LDS in wave order.
-// h is rounded once to the type of the weights, as the layer's own H is; all
-// sums are fp32 in a fixed order.
+//  - No combine: with the gate applied to h in fp32, the sum over a token's
+//    experts is a product whose K runs over all the chosen experts' F, zeros
+//    standing in for the pairs that are not.  A workgroup of DOWN owns sixteen
+//    columns of out, its waves share that K, and their fp32 sums meet in LDS in
+//    wave order.
+// h goes from UP to DOWN in four bytes whatever the type, and enters the 16-bit
+// matrix instructions as a high and a low part (h_parts), so that it loses
+// nothing next to out's own rounding and keeps fp32's range: in 16 bits it would
+// be a second rounding as large as out's, and in fp16 an infinity past 65504 and
+// nothing below 3e-8.  The second instruction is free beside the bytes of W2.
+// All sums are fp32 in a fixed order.
 // At d 4096, F 1536, 8 of 128 experts (bf16): one token 39 + 20 us (201 and 101 MB;
 // 5.1 TB/s together), sixteen 525 us (3.1 GB, 5.9 TB/s).
 #include "few_tokens.h"
@@ -170,6 +174,49 @@ __device__ __forceinline__ void route_few(const FewTokens& a, int t0, int t1, in
       gate[t * k + lane] = g;
     }
   }
+}
+
+// What UP leaves of an element of h, and its value again.  bf16: the rounded part in
+// the high half and its rounded rest in the low one, off by 2^-16 of the value
+// at most.  fp16 and fp32: fp32 itself (fp16's range holds no h: DOWN splits it).
+template <int DT> __device__ __forceinline__ uint32_t h_word(float v) {
+  if constexpr (DT != 1) return __float_as_uint(v);
+  else return Elem<1>::pack(v - Elem<1>::hi(Elem<1>::pack(0.f, v)), v);
+}
+template <int DT> __device__ __forceinline__ float h_value(uint32_t w) {
+  if constexpr (DT != 1) return __uint_as_float(w);
+  else return Elem<1>::hi(w) + Elem<1>::lo(w);
+}
+
+// The larger of a lane's value and those of the lanes 16, 32 and 48 further on.
+__device__ __forceinline__ float column_max(float v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+#endif
+  return v;
+}
+
+// Eight words of h as the operands of two 16-bit matrix instructions.  fp16: of
+// h * down, cut to 11 bits, and of the rest cut likewise: off by 2^-20 of the value
+// at most, or by 2^-24 where the rest is subnormal.
+template <int DT> __device__ __forceinline__ void h_parts(const u32x4_t (&w)[2], float down, u32x4_t* hi, u32x4_t* lo) {
+#if defined(__HIP_DEVICE_COMPILE__)
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t w0 = w[j / 2][2 * j % 4], w1 = w[j / 2][2 * j % 4 + 1];
+    if constexpr (DT == 1) {
+      (*hi)[j] = __builtin_amdgcn_perm(w1, w0, 0x07060302);  // the high halves
+      (*lo)[j] = __builtin_amdgcn_perm(w1, w0, 0x05040100);  // the low ones
+    } else {
+      const float a = __uint_as_float(w0) * down, b = __uint_as_float(w1) * down;
+      (*hi)[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
+      (*lo)[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a - Elem<2>::lo((*hi)[j]), b - Elem<2>::hi((*hi)[j])));
+    }
+  }
+#endif
 }
 
 __device__ __forceinline__ int adapter_of(const FewTokens& a, int t) {
@@ -376,10 +423,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float va = acc[0][i], hv = va * sigmoidf_(va) * acc[1][i] * gt;
-          if (4 * g + i < cols) {
-            if constexpr (DT == 0) reinterpret_cast<float*>(a.h)[ho + i] = hv;
-            else reinterpret_cast<uint16_t*>(a.h)[ho + i] = (uint16_t)Elem<DT>::pack(hv, 0.f);
-          }
+          if (4 * g + i < cols) a.h[ho + i] = h_word<DT>(hv);
         }
       }
     }
@@ -419,7 +463,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
   const int chunks = (a.F + STEP * U - 1) / (STEP * U);  // of one expert
   const int all = nslots * chunks;  // the waves take them in turn: what they read at a time is neighbouring
   const int mine = all > w ? (all - w + NW - 1) / NW : 0;
-  const auto hrs = __builtin_amdgcn_make_buffer_rsrc(a.h, (short)0, (int)((int64_t)P * a.Fp * S), 0x00020000);
+  const auto hrs = __builtin_amdgcn_make_buffer_rsrc(a.h, (short)0, (int)((int64_t)P * a.Fp * 4), 0x00020000);
   // cursor of the next chunk to load; past the last one it stays on it
   const int skip_slots = NW / chunks, skip = NW - skip_slots * chunks;
   int slot = w / chunks, ch = w - slot * chunks;
@@ -427,8 +471,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
 #pragma unroll
   for (int q = 0; q < NT; ++q) acc[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   Quad<DT, ODD> qw[2][U][NT];
-  u32x4_t qh[2][U];
-  uint32_t shift[2][U][NT];
+  constexpr int HW = KE / 4;  // 16-byte accesses of a lane's words of h
+  u32x4_t qh[2][U][HW];
+  uint32_t odd[2];  // a bit for each access of a chunk that starts off a dword
   int left[2];  // !WHOLE: elements of F from the lane's first of the chunk
   // WHOLE: F is a multiple of KE, a lane's 16 bytes lie in F or past it; a
   // lane past it reads the row's first bytes and zeros of h.  Otherwise the lane
@@ -437,9 +482,10 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
     const int e = __builtin_amdgcn_readfirstlane(s_expert[slot]);
     const int pair = s_pair[slot * 16 + i16];
     // a pair that is not: an offset past the buffer, which loads zeros
-    const uint32_t hoff = pair >= 0 ? (uint32_t)(pair * a.Fp) * S : 0xC0000000u;
+    const uint32_t hoff = pair >= 0 ? (uint32_t)(pair * a.Fp) * 4 : 0xC0000000u;
     const char* wp = (const char*)a.w[2] + (int64_t)e * a.d * row_bytes;
     left[buf] = a.F - ch * U * STEP - g * KE;
+    odd[buf] = 0;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int k = (ch * U + j) * STEP + g * KE;
@@ -448,14 +494,16 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
         if constexpr (LONG) {
           const char* from = wp + wrow[q] + (WHOLE ? (k < a.F ? k : 0) : tail_at<DT>(k, a.F)) * S;
           qw[buf][j][q].load(from);
-          shift[buf][j][q] = shift_of<ODD>(from);
+          odd[buf] |= shift_of<ODD>(from) / 16 << (j * NT + q);
         } else {
           qw[buf][j][q].v = load_part<DT>(wp + wrow[q] + k * S, k < a.F ? a.F - k : 0);
-          shift[buf][j][q] = 0;
         }
       }
-      const auto v = __builtin_amdgcn_raw_buffer_load_b128(hrs, k < a.F ? hoff + k * S : 0xC0000000u, 0, 0);
-      qh[buf][j] = u32x4_t{(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
+#pragma unroll
+      for (int i = 0; i < HW; ++i) {
+        const auto v = __builtin_amdgcn_raw_buffer_load_b128(hrs, k < a.F ? hoff + k * 4 + 16 * i : 0xC0000000u, 0, 0);
+        qh[buf][j][i] = u32x4_t{(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
+      }
     }
     const bool wrap = ch + skip >= chunks;
     const int next = slot + skip_slots + wrap;
@@ -464,22 +512,54 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
     __builtin_amdgcn_sched_barrier(0);
   };
   auto mul = [&](int buf) {
+    if constexpr (!WHOLE) {  // past F nothing was written
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int i = 0; i < HW; ++i) qh[buf][j][i] = first_elems<0>(qh[buf][j][i], left[buf] - j * STEP - 4 * i);
+    }
+    // fp16: the chunk's h of a token brought to [2^14, 2^15) by a power of two, exactly,
+    // and its sum back (b: the exponent of the largest, off by 127)
+    float down = 1.f, up = 1.f;
+    f32x4_t part[NT];
+    if constexpr (DT == 2) {
+      float big = 0.f;
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+#pragma unroll
+        for (int i = 0; i < 4 * HW; ++i) big = fmaxf(big, fabsf(__uint_as_float(qh[buf][j][i / 4][i % 4])));
+      uint32_t b = __float_as_uint(column_max(big)) >> 23;
+      b = b < 15 ? 15 : b > 254 ? 254 : b;
+      down = __uint_as_float((268 - b) << 23);
+      up = __uint_as_float((b - 14) << 23);
+#pragma unroll
+      for (int q = 0; q < NT; ++q) part[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      if constexpr (!WHOLE) {
-        const int in = left[buf] - j * STEP;
-        qh[buf][j] = first_elems<DT>(qh[buf][j], in);  // past F nothing was written
-      }
+      u32x4_t hi, lo;
+      if constexpr (DT != 0) h_parts<DT>(qh[buf][j], down, &hi, &lo);
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
-        u32x4_t vw = qw[buf][j][q].get(shift[buf][j][q]);
+        u32x4_t vw = qw[buf][j][q].get((odd[buf] >> (j * NT + q) & 1) * 16);
         if constexpr (!WHOLE && LONG) {
           const int in = left[buf] - j * STEP;
           vw = shift_elems<DT>(vw, in < KE ? KE - in : 0);
         }
-        acc[q] = mma<DT>(vw, qh[buf][j], acc[q]);
+        f32x4_t& sum = DT == 2 ? part[q] : acc[q];
+        if constexpr (DT == 0) {
+          sum = mma<DT>(vw, qh[buf][j][0], sum);
+        } else {
+          sum = mma<DT>(vw, lo, sum);
+          sum = mma<DT>(vw, hi, sum);
+        }
       }
     }
+    if constexpr (DT == 2)
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[q][i] = fmaf(part[q][i], up, acc[q][i]);
     __builtin_amdgcn_sched_barrier(0);
   };
   if (mine) {  // no load under a condition, as in UP
@@ -563,13 +643,23 @@ template <int DT, int EPL, bool DOWN> __global__ __launch_bounds__(256) void few
   float* to = a.u[m] + (int64_t)p * few_u_width(r) + rr;
   float sum = 0.f;
   if (rr < r) {
-    const char* v = DOWN ? (const char*)a.h + (int64_t)p * a.Fp * S : (const char*)a.x + (int64_t)t * K * S;
+    const char* x = (const char*)a.x + (int64_t)t * K * S;
+    const uint32_t* h = a.h + (int64_t)p * a.Fp;
     const char* row = (const char*)a.lora[m].A + (((int64_t)l * a.E_loc + e) * r + rr) * K * S;
 #pragma unroll 4
     for (int c = lane * KE; c < K; c += 64 * KE) {
       float fa[KE], fv[KE];
       widen<DT>(load_part<DT>(row + (int64_t)c * S, K - c), fa);
-      widen<DT>(load_part<DT>(v + (int64_t)c * S, K - c), fv);
+      if constexpr (DOWN) {  // the row holds whole 16-byte words
+#pragma unroll
+        for (int i = 0; i < KE; i += 4) {
+          const u32x4_t v = first_elems<0>(*reinterpret_cast<const u32x4_t*>(h + (c + i < K ? c + i : c)), K - c - i);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) fv[i + j] = h_value<DT>(v[j]);
+        }
+      } else {
+        widen<DT>(load_part<DT>(x + (int64_t)c * S, K - c), fv);
+      }
 #pragma unroll
       for (int i = 0; i < KE; ++i) sum = fmaf(fa[i], fv[i], sum);
     }
