@@ -691,8 +691,7 @@ mok_status mok_quantize_int4(const void* src, int64_t rows, int64_t K, int32_t g
  *                   call in flight
  * Sums are fp32 in a fixed order (the same bits on every run); the gate is
  * applied to the first product's result h in fp32, h enters the second product
- * with fp32's range and 16 bits of mantissa or more (fp16: 2^-20 of h, or 2^-38 of
- * the largest of its token's and expert's 128 columns), and out is rounded once.
+ * with fp32's range and 16 bits of mantissa or more, and out is rounded once.
  *
  * Adapters (`adapter` and `lora` both NULL: none): token t with l = adapter[t] in
  * [0, L) has W + scale[l] B_{l,e} A_{l,e} in place of each of its experts'

@@ -58,7 +58,7 @@ mok_status few_layout(const mok_few_token_config* cfg, const mok_lora_weights* l
   if (bad_dtype(c.dtype) || (c.flags & ~(MOK_FLAG_SIGMOID_GATES | MOK_FLAG_RENORM_GATES))) return MOK_ERR_INVALID_ARG;
   const int64_t P = (int64_t)c.T * c.k;
   Parts p;
-  const int64_t h = P * few_h_width(c.ffn, c.dtype) * 4;  // whole 16-byte words: the tables follow at once
+  const int64_t h = P * few_h_width(c.ffn, c.dtype) * 4;  // whole 16 bytes: the tables follow at once
   o->h = p.take(h + (P ? few_table_size(c.T, c.k, c.expert_end - c.expert_begin) : 0));
   o->table = o->h + h;
   for (int m = 0; m < 3; ++m) {
@@ -259,7 +259,7 @@ mok_status mok_few_token_layer(const void* x, const float* router_logits, const 
   a.out = out;
   a.idx = topk_idx;
   a.gate = topk_gate;
-  a.h = (uint32_t*)((char*)workspace + l.h);
+  a.h = (char*)workspace + l.h;
   a.table = (char*)workspace + l.table;
   bool any = false;
   for (int m = 0; m < 3 && lora; ++m) {

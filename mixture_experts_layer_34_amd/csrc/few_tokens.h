@@ -26,7 +26,7 @@ struct FewTokens {
   void* out;
   int32_t* idx;
   float* gate;
-  uint32_t* h;  // [T k, Fp] gate * silu(a) * b, in columns [0, F), as h_word has it
+  void* h;      // gate * silu(a) * b, in columns [0, F): fp32 [T k, Fp], or two bf16 parts [T k, 2, Fp]
   void* table;  // few_table_size bytes: the chosen experts and their pairs
   float* u[3];  // [T k, rp] scale * A v of each pair, zeros past r
   FewLora lora[3];
@@ -34,8 +34,8 @@ struct FewTokens {
   int T, d, F, Fp, E, eb, E_loc, k, L, dtype, gating;
 };
 
-// Width of an h row in its 4-byte words: whole lines of 128 bytes for fp32, whole
-// 16-byte loads for the 16-bit types.
+// Width of an h row, of four bytes an element: whole lines of 128 bytes for fp32, whole
+// 16 bytes for the two parts of the 16-bit types.
 inline int few_h_width(int F, int dtype) { return dtype == 0 ? (F + 31) / 32 * 32 : (F + 3) / 4 * 4; }
 // Width of a u row: whole 16-byte loads.
 __host__ __device__ inline int few_u_width(int r) { return (r + 7) / 8 * 8; }

@@ -21,14 +21,15 @@
 //    standing in for the pairs that are not.  A workgroup of DOWN owns sixteen
 //    columns of out, its waves share that K, and their fp32 sums meet in LDS in
 //    wave order.
-// h goes from UP to DOWN in four bytes whatever the type, and enters the 16-bit
-// matrix instructions as a high and a low part (h_parts), so that it loses
-// nothing next to out's own rounding and keeps fp32's range: in 16 bits it would
-// be a second rounding as large as out's, and in fp16 an infinity past 65504 and
-// nothing below 3e-8.  The second instruction is free beside the bytes of W2.
+// h goes from UP to DOWN in four bytes whatever the type, for the 16-bit ones as
+// two bf16 parts (store_h), so that it loses nothing next to out's own rounding
+// and keeps fp32's range: in 16 bits it would be a second rounding as large as
+// out's, and in fp16 an infinity past 65504 and nothing below 3e-8.  DOWN takes up
+// to eight tokens' two parts as the sixteen columns of one matrix instruction, more
+// tokens' by a second one; fp16 weights are two bf16 parts there, exactly.
 // All sums are fp32 in a fixed order.
 // At d 4096, F 1536, 8 of 128 experts (bf16): one token 39 + 20 us (201 and 101 MB;
-// 5.1 TB/s together), sixteen 525 us (3.1 GB, 5.9 TB/s).
+// 5.1 TB/s together), sixteen 563 us (5.5 TB/s).
 #include "few_tokens.h"
 #include "frag.h"
 #include "mok_internal.h"
@@ -176,45 +177,43 @@ __device__ __forceinline__ void route_few(const FewTokens& a, int t0, int t1, in
   }
 }
 
-// What UP leaves of an element of h, and its value again.  bf16: the rounded part in
-// the high half and its rounded rest in the low one, off by 2^-16 of the value
-// at most.  fp16 and fp32: fp32 itself (fp16's range holds no h: DOWN splits it).
-template <int DT> __device__ __forceinline__ uint32_t h_word(float v) {
-  if constexpr (DT != 1) return __float_as_uint(v);
-  else return Elem<1>::pack(v - Elem<1>::hi(Elem<1>::pack(0.f, v)), v);
+// h of the 16-bit types: a row of bf16 values, and a row of their bf16 rests Fp
+// further on: off by 2^-16 of the value at most.  (fp16 itself has no range for h.)
+template <int DT> __device__ __forceinline__ void store_h(const FewTokens& a, int pair, int col, float v) {
+  if constexpr (DT == 0) {
+    reinterpret_cast<float*>(a.h)[(int64_t)pair * a.Fp + col] = v;
+  } else {
+    uint16_t* to = reinterpret_cast<uint16_t*>(a.h) + (int64_t)pair * 2 * a.Fp + col;
+    const uint32_t hi = Elem<1>::pack(v, 0.f);
+    to[0] = (uint16_t)hi;
+    to[a.Fp] = (uint16_t)Elem<1>::pack(v - Elem<1>::lo(hi), 0.f);
+  }
 }
-template <int DT> __device__ __forceinline__ float h_value(uint32_t w) {
-  if constexpr (DT != 1) return __uint_as_float(w);
-  else return Elem<1>::hi(w) + Elem<1>::lo(w);
+// KE elements of h from `col` on, the first n of them (zeros behind).
+template <int DT> __device__ __forceinline__ void load_h(const FewTokens& a, int pair, int col, int n, float* f) {
+  if constexpr (DT == 0) {
+    widen<0>(load_part<0>((const char*)a.h + ((int64_t)pair * a.Fp + col) * 4, n), f);
+  } else {
+    const char* at = (const char*)a.h + ((int64_t)pair * 2 * a.Fp + col) * 2;
+    float lo[8];
+    widen<1>(load_part<1>(at, n), f);
+    widen<1>(load_part<1>(at + 2 * a.Fp, n), lo);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] += lo[j];
+  }
 }
 
-// The larger of a lane's value and those of the lanes 16, 32 and 48 further on.
-__device__ __forceinline__ float column_max(float v) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-  const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
-#endif
-  return v;
-}
-
-// Eight words of h as the operands of two 16-bit matrix instructions.  fp16: of
-// h * down, cut to 11 bits, and of the rest cut likewise: off by 2^-20 of the value
-// at most, or by 2^-24 where the rest is subnormal.
-template <int DT> __device__ __forceinline__ void h_parts(const u32x4_t (&w)[2], float down, u32x4_t* hi, u32x4_t* lo) {
+// fp16 elements as two bf16 parts whose sum they are: 8 bits of the 11 cut off, and
+// the 3 that are left.
+__device__ __forceinline__ void split_f16(u32x4_t v, u32x4_t* hi, u32x4_t* lo) {
 #if defined(__HIP_DEVICE_COMPILE__)
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t w0 = w[j / 2][2 * j % 4], w1 = w[j / 2][2 * j % 4 + 1];
-    if constexpr (DT == 1) {
-      (*hi)[j] = __builtin_amdgcn_perm(w1, w0, 0x07060302);  // the high halves
-      (*lo)[j] = __builtin_amdgcn_perm(w1, w0, 0x05040100);  // the low ones
-    } else {
-      const float a = __uint_as_float(w0) * down, b = __uint_as_float(w1) * down;
-      (*hi)[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
-      (*lo)[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a - Elem<2>::lo((*hi)[j]), b - Elem<2>::hi((*hi)[j])));
-    }
+    const float a = Elem<2>::lo(v[j]), b = Elem<2>::hi(v[j]);
+    const uint32_t ua = __float_as_uint(a) & 0xFFFF0000u, ub = __float_as_uint(b) & 0xFFFF0000u;
+    const uint32_t ra = __float_as_uint(a - __uint_as_float(ua)), rb = __float_as_uint(b - __uint_as_float(ub));
+    (*hi)[j] = __builtin_amdgcn_perm(ub, ua, 0x07060302);  // the high halves of both
+    (*lo)[j] = __builtin_amdgcn_perm(rb, ra, 0x07060302);
   }
 #endif
 }
@@ -419,11 +418,10 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
       }
       if (pair >= 0) {
         const float gt = s.gate[pair];
-        const int64_t ho = (int64_t)pair * a.Fp + n0 + 4 * g;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float va = acc[0][i], hv = va * sigmoidf_(va) * acc[1][i] * gt;
-          if (4 * g + i < cols) a.h[ho + i] = h_word<DT>(hv);
+          if (4 * g + i < cols) store_h<DT>(a, pair, n0 + 4 * g + i, hv);
         }
       }
     }
@@ -435,15 +433,20 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
 // A workgroup owns `cols` columns of out, up to 16 NT: as many as give every
 // compute unit the same share.
 constexpr int kDownWaves = 8;
-// LONG: F >= KE.  ODD: rows of W2 of an odd number of 16-bit elements.
-template <int DT, int NT, bool WHOLE, bool LONG, bool ODD>
+// LONG: F >= KE.  ODD: rows of W2 of an odd number of 16-bit elements.  PARTS: matrix
+// instructions for the parts of h; with one, for the 16-bit types and at most eight
+// tokens, columns 0..7 are the first parts and 8..15 the second.  (Four tokens of
+// d 2048, F 1408 with adapters 102 us, by two 111; sixteen of d 4096, F 1536, which
+// need two, 563, where one rounded part alone took 535.)
+template <int DT, int NT, bool WHOLE, bool LONG, bool ODD, int PARTS>
 __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, int cols) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int KE = kFragElems<DT>, STEP = kFragStep<DT>, S = Elem<DT>::kBytes, U = kUnroll, NW = kDownWaves;
+  constexpr bool BOTH = DT != 0 && PARTS == 1;  // columns of both parts
   extern __shared__ __align__(16) char lds[];
   __shared__ f32x4_t red[NW][NT][64];
   const int tid = threadIdx.x, lane = tid & 63, w = wave_id();
-  const int i16 = lane & 15, g = lane >> 4;
+  const int i16 = lane & 15, g = lane >> 4, col = BOTH ? i16 & 7 : i16;  // col: the lane's token
   const int P = a.T * a.k, most = few_slots(P, a.E_loc);
   int16_t *s_pair = reinterpret_cast<int16_t*>(lds), *s_expert = s_pair + 16 * most;
   const int nslots = *reinterpret_cast<const int32_t*>(a.table);
@@ -463,7 +466,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
   const int chunks = (a.F + STEP * U - 1) / (STEP * U);  // of one expert
   const int all = nslots * chunks;  // the waves take them in turn: what they read at a time is neighbouring
   const int mine = all > w ? (all - w + NW - 1) / NW : 0;
-  const auto hrs = __builtin_amdgcn_make_buffer_rsrc(a.h, (short)0, (int)((int64_t)P * a.Fp * 4), 0x00020000);
+  // (the last row's last access may end eight bytes behind it, in the tables)
+  const auto hrs = __builtin_amdgcn_make_buffer_rsrc(a.h, (short)0, (int)((int64_t)P * a.Fp * 4 + 16), 0x00020000);
   // cursor of the next chunk to load; past the last one it stays on it
   const int skip_slots = NW / chunks, skip = NW - skip_slots * chunks;
   int slot = w / chunks, ch = w - slot * chunks;
@@ -471,8 +475,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
 #pragma unroll
   for (int q = 0; q < NT; ++q) acc[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   Quad<DT, ODD> qw[2][U][NT];
-  constexpr int HW = KE / 4;  // 16-byte accesses of a lane's words of h
-  u32x4_t qh[2][U][HW];
+  u32x4_t qh[2][U][PARTS];
   uint32_t odd[2];  // a bit for each access of a chunk that starts off a dword
   int left[2];  // !WHOLE: elements of F from the lane's first of the chunk
   // WHOLE: F is a multiple of KE, a lane's 16 bytes lie in F or past it; a
@@ -480,9 +483,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
   // that F ends in reads the row's last 16 bytes and moves them to their places.
   auto load = [&](int buf) {
     const int e = __builtin_amdgcn_readfirstlane(s_expert[slot]);
-    const int pair = s_pair[slot * 16 + i16];
+    const int pair = s_pair[slot * 16 + col];
     // a pair that is not: an offset past the buffer, which loads zeros
-    const uint32_t hoff = pair >= 0 ? (uint32_t)(pair * a.Fp) * 4 : 0xC0000000u;
+    const uint32_t hoff = pair >= 0 ? (uint32_t)(pair * a.Fp) * 4 + (BOTH && i16 > 7 ? a.Fp * 2 : 0) : 0xC0000000u;
     const char* wp = (const char*)a.w[2] + (int64_t)e * a.d * row_bytes;
     left[buf] = a.F - ch * U * STEP - g * KE;
     odd[buf] = 0;
@@ -500,8 +503,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
         }
       }
 #pragma unroll
-      for (int i = 0; i < HW; ++i) {
-        const auto v = __builtin_amdgcn_raw_buffer_load_b128(hrs, k < a.F ? hoff + k * 4 + 16 * i : 0xC0000000u, 0, 0);
+      for (int i = 0; i < PARTS; ++i) {
+        const auto v = __builtin_amdgcn_raw_buffer_load_b128(hrs, k < a.F ? hoff + k * S + i * a.Fp * 2 : 0xC0000000u, 0, 0);
         qh[buf][j][i] = u32x4_t{(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
       }
     }
@@ -512,33 +515,12 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
     __builtin_amdgcn_sched_barrier(0);
   };
   auto mul = [&](int buf) {
-    if constexpr (!WHOLE) {  // past F nothing was written
-#pragma unroll
-      for (int j = 0; j < U; ++j)
-#pragma unroll
-        for (int i = 0; i < HW; ++i) qh[buf][j][i] = first_elems<0>(qh[buf][j][i], left[buf] - j * STEP - 4 * i);
-    }
-    // fp16: the chunk's h of a token brought to [2^14, 2^15) by a power of two, exactly,
-    // and its sum back (b: the exponent of the largest, off by 127)
-    float down = 1.f, up = 1.f;
-    f32x4_t part[NT];
-    if constexpr (DT == 2) {
-      float big = 0.f;
-#pragma unroll
-      for (int j = 0; j < U; ++j)
-#pragma unroll
-        for (int i = 0; i < 4 * HW; ++i) big = fmaxf(big, fabsf(__uint_as_float(qh[buf][j][i / 4][i % 4])));
-      uint32_t b = __float_as_uint(column_max(big)) >> 23;
-      b = b < 15 ? 15 : b > 254 ? 254 : b;
-      down = __uint_as_float((268 - b) << 23);
-      up = __uint_as_float((b - 14) << 23);
-#pragma unroll
-      for (int q = 0; q < NT; ++q) part[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    }
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      u32x4_t hi, lo;
-      if constexpr (DT != 0) h_parts<DT>(qh[buf][j], down, &hi, &lo);
+      if constexpr (!WHOLE) {  // past F nothing was written
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) qh[buf][j][i] = first_elems<DT>(qh[buf][j][i], left[buf] - j * STEP);
+      }
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
         u32x4_t vw = qw[buf][j][q].get((odd[buf] >> (j * NT + q) & 1) * 16);
@@ -546,20 +528,15 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
           const int in = left[buf] - j * STEP;
           vw = shift_elems<DT>(vw, in < KE ? KE - in : 0);
         }
-        f32x4_t& sum = DT == 2 ? part[q] : acc[q];
-        if constexpr (DT == 0) {
-          sum = mma<DT>(vw, qh[buf][j][0], sum);
-        } else {
-          sum = mma<DT>(vw, lo, sum);
-          sum = mma<DT>(vw, hi, sum);
+        u32x4_t rest;
+        if constexpr (DT == 2) split_f16(vw, &vw, &rest);
+#pragma unroll
+        for (int i = PARTS - 1; i >= 0; --i) {
+          acc[q] = mma<DT == 0 ? 0 : 1>(vw, qh[buf][j][i], acc[q]);
+          if constexpr (DT == 2) acc[q] = mma<1>(rest, qh[buf][j][i], acc[q]);
         }
       }
     }
-    if constexpr (DT == 2)
-#pragma unroll
-      for (int q = 0; q < NT; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[q][i] = fmaf(part[q][i], up, acc[q][i]);
     __builtin_amdgcn_sched_barrier(0);
   };
   if (mine) {  // no load under a condition, as in UP
@@ -594,15 +571,18 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
 #pragma unroll
   for (int q = 0; q < NT; ++q) red[w][q][lane] = acc[q];
   __syncthreads();
-  if (w < NT && i16 < a.T) {  // a wave for each sixteen columns
+  if (w < NT) {  // a wave for each sixteen columns
     f32x4_t v = red[0][w][lane];
 #pragma unroll
     for (int k = 1; k < NW; ++k) v += red[k][w][lane];
+    if constexpr (BOTH)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v[i]), 0x128, 0xf, 0xf, false));  // row_ror 8
     const int n = n0 + 16 * w + 4 * g;
     const int64_t o = (int64_t)i16 * a.d + n;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (n + i < n1) {
+      if (i16 < a.T && n + i < n1) {
         if constexpr (DT == 0) reinterpret_cast<float*>(a.out)[o + i] = v[i];
         else reinterpret_cast<uint16_t*>(a.out)[o + i] = (uint16_t)Elem<DT>::pack(v[i], 0.f);
       }
@@ -644,22 +624,13 @@ template <int DT, int EPL, bool DOWN> __global__ __launch_bounds__(256) void few
   float sum = 0.f;
   if (rr < r) {
     const char* x = (const char*)a.x + (int64_t)t * K * S;
-    const uint32_t* h = a.h + (int64_t)p * a.Fp;
     const char* row = (const char*)a.lora[m].A + (((int64_t)l * a.E_loc + e) * r + rr) * K * S;
 #pragma unroll 4
     for (int c = lane * KE; c < K; c += 64 * KE) {
       float fa[KE], fv[KE];
       widen<DT>(load_part<DT>(row + (int64_t)c * S, K - c), fa);
-      if constexpr (DOWN) {  // the row holds whole 16-byte words
-#pragma unroll
-        for (int i = 0; i < KE; i += 4) {
-          const u32x4_t v = first_elems<0>(*reinterpret_cast<const u32x4_t*>(h + (c + i < K ? c + i : c)), K - c - i);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) fv[i + j] = h_value<DT>(v[j]);
-        }
-      } else {
-        widen<DT>(load_part<DT>(x + (int64_t)c * S, K - c), fv);
-      }
+      if constexpr (DOWN) load_h<DT>(a, p, c, K - c, fv);
+      else widen<DT>(load_part<DT>(x + (int64_t)c * S, K - c), fv);
 #pragma unroll
       for (int i = 0; i < KE; ++i) sum = fmaf(fa[i], fv[i], sum);
     }
@@ -669,9 +640,14 @@ template <int DT, int EPL, bool DOWN> __global__ __launch_bounds__(256) void few
 #endif
 }
 
+template <int DT, int NT, bool WHOLE, bool LONG, bool ODD, int PARTS>
+void down_parts(const FewTokens& a, int cols, int slots, hipStream_t s) {
+  hipLaunchKernelGGL((few_down_kernel<DT, NT, WHOLE, LONG, ODD, PARTS>), dim3((a.d + cols - 1) / cols),
+                     dim3(64 * kDownWaves), (size_t)slots * 34 + 64, s, a, cols);
+}
 template <int DT, int NT, bool WHOLE, bool LONG, bool ODD> void down(const FewTokens& a, int cols, int slots, hipStream_t s) {
-  hipLaunchKernelGGL((few_down_kernel<DT, NT, WHOLE, LONG, ODD>), dim3((a.d + cols - 1) / cols), dim3(64 * kDownWaves),
-                     (size_t)slots * 34 + 64, s, a, cols);
+  if (DT != 0 && a.T > 8) down_parts<DT, NT, WHOLE, LONG, ODD, DT == 0 ? 1 : 2>(a, cols, slots, s);
+  else down_parts<DT, NT, WHOLE, LONG, ODD, 1>(a, cols, slots, s);
 }
 
 template <int DT, int EPL, bool ODD> void up(const FewTokens& a, int P, int slots, hipStream_t s) {

@@ -34,14 +34,16 @@ def _check(args, k, dt, **kw):
     return got, ref
 
 
-# a chunk of h is 128 columns (64 for fp32): less than one, whole ones, a part at the
-# end, rows of less than 16 bytes, odd rows, and widths of out past 4096 (two column
-# tiles a workgroup)
+# at most eight tokens (both parts of h in one matrix instruction) and more; less than
+# a chunk of 128 columns of h, whole ones, a part at the end, rows of less than 16
+# bytes, odd rows, and widths of out past 4096 (two column tiles a workgroup)
 SHAPES = [(1, 64, 128, 4, 2, "bf16"), (16, 96, 256, 8, 4, "bf16"), (5, 130, 67, 9, 4, "bf16"),
           (3, 40, 5, 4, 2, "bf16"), (7, 4200, 129, 4, 2, "bf16"), (4, 4100, 130, 3, 2, "bf16"),
           (1, 64, 128, 4, 2, "f16"), (16, 96, 256, 8, 4, "f16"), (5, 130, 67, 9, 4, "f16"), (3, 40, 5, 4, 2, "f16"),
           (7, 4200, 129, 4, 2, "f16"), (4, 4100, 130, 3, 2, "f16"), (2, 4160, 64, 3, 1, "f16"),
-          (16, 200, 1411, 6, 3, "f16"), (6, 64, 97, 5, 2, "f32")]
+          (16, 200, 1411, 6, 3, "f16"), (8, 72, 1411, 6, 3, "bf16"), (9, 72, 1411, 6, 3, "bf16"),
+          (8, 4104, 67, 3, 2, "f16"), (9, 4104, 67, 3, 2, "f16"), (10, 40, 5, 4, 2, "bf16"), (12, 40, 1, 4, 2, "f16"),
+          (11, 4100, 129, 3, 1, "bf16"), (6, 64, 97, 5, 2, "f32")]
 
 
 @pytest.mark.parametrize("T,d,F,E,k,dt", SHAPES)
