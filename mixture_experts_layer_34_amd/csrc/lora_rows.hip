@@ -33,13 +33,25 @@ namespace {
 
 __device__ __forceinline__ int cut(int v, int rows) { return v < 0 ? 0 : v > rows ? rows : v; }
 
+// All groups' rows, whatever the offsets between the first and the last are.
+struct Span {
+  int first, last;
+  // an offset between them, cut to them: offsets that fall name no rows outside
+  __device__ __forceinline__ int in(int offset) const { return offset < first ? first : offset > last ? last : offset; }
+};
+__device__ __forceinline__ Span span_of(const LoraMap& m, int first, int last) {
+  first = cut(first, m.rows);
+  last = cut(last, m.rows);
+  return Span{first, last > first ? last : first};
+}
+
 // The groups' rows, shared out evenly in n ranges of `each` rows.  (A compute unit
 // with more rows than another ends later by as much: they get even shares of the
 // memory's rate.)  What a kernel reads before it can ask for its first row adds to
 // its time in full, so one load brings all offsets of up to 63 groups, a lane each.
-struct Rows {
+struct Rows : Span {
   int offset;  // of group `lane`, or the end of the last
-  int first, last, each;
+  int each;
   __device__ __forceinline__ int begin(int i) const {
     const int64_t at = first + (int64_t)each * i;
     return at < last ? (int)at : last;
@@ -50,9 +62,8 @@ __device__ __forceinline__ Rows rows_of(const LoraMap& m, int n) {
   Rows r;
   const int lane = lane_id();
   r.offset = m.offsets[lane < m.G ? lane : m.G];
-  r.first = cut(__builtin_amdgcn_readfirstlane(r.offset), m.rows);
-  r.last = cut(m.G < 64 ? __builtin_amdgcn_readlane(r.offset, m.G) : m.offsets[m.G], m.rows);
-  r.last = r.last > r.first ? r.last : r.first;
+  static_cast<Span&>(r) = span_of(m, __builtin_amdgcn_readfirstlane(r.offset),
+                                  m.G < 64 ? __builtin_amdgcn_readlane(r.offset, m.G) : m.offsets[m.G]);
   r.each = (r.last - r.first + n - 1) / n;
   r.each = r.each > 0 ? r.each : 1;
   return r;
@@ -82,8 +93,8 @@ __device__ __forceinline__ Part part_at(const LoraMap& m, const Rows& rows, int 
     lo = m.offsets[g];
     hi = m.offsets[g + 1];
   }
-  lo = cut(lo, m.rows);
-  hi = cut(hi, m.rows);
+  lo = rows.in(lo);
+  hi = rows.in(hi);
   const int e = hi < end ? hi : end;
   return Part{g, e > row ? e : row + 1, lo, hi};  // (offsets that fall: a row at a time)
 }
@@ -679,9 +690,8 @@ template <int DT, int RT> __global__ __launch_bounds__(64) void lora_grad_sum_ke
   const int W = a.width[mat];
   if ((int)blockIdx.x * COLS >= W) return;
   const Rows rows = rows_of(a.map, a.ranges);
-  const int lo = cut(a.map.offsets[g], a.map.rows), hi = cut(a.map.offsets[g + 1], a.map.rows);
-  // (offsets that fall name rows outside: no ranges)
-  if (hi <= lo || lo < rows.first || hi > rows.last) return;
+  const int lo = rows.in(a.map.offsets[g]), hi = rows.in(a.map.offsets[g + 1]);
+  if (hi <= lo) return;
   const int r0 = rows.range_of(lo), r1 = rows.range_of(hi - 1);
   if (r0 == r1) return;
   const int at = blockIdx.x * COLS + i16 * KE, last = W > KE ? W - KE : 0;
@@ -713,7 +723,8 @@ template <typename E> __global__ __launch_bounds__(256) void lora_prepare_kernel
   const int at = (isA ? blockIdx.x : blockIdx.x - ka) * 64, W = isA ? a.K : a.N;
   const int n = W - at < 64 ? W - at : 64;
   const int64_t g = (int64_t)blockIdx.y * r * W;
-  if (cut(a.map.offsets[blockIdx.y + 1], a.map.rows) <= cut(a.map.offsets[blockIdx.y], a.map.rows)) {
+  const Span span = span_of(a.map, a.map.offsets[0], a.map.offsets[a.map.G]);
+  if (span.in(a.map.offsets[blockIdx.y + 1]) <= span.in(a.map.offsets[blockIdx.y])) {
     float* out = (isA ? a.dA : a.dB) + g;
     for (int i = threadIdx.x; i < r * 64; i += 256) {
       if (!isA && i < n * r) out[(int64_t)at * r + i] = 0.f;
