@@ -760,8 +760,9 @@ mok_status mok_few_token_layer(const void* x, const float* router_logits, const 
  *   workspace       mok_lora_workspace_query bytes of scratch (may be 0 bytes),
  *                   one for each call in flight
  * Sums are fp32 in a fixed order: the same bits on every run.  out and dx are
- * rounded once; u and du enter their products with 16 bits of mantissa or more,
- * the sums of dA and dB with all of theirs.
+ * rounded once; u and du enter their products with 16 bits of mantissa or more
+ * (fp16: those less than 2^-22 of their row's largest are off by 2^-39 of it at
+ * most), the sums of dA and dB with all of theirs.
  * 0 <= rows < 2^30, 1 <= r <= 128, 1 <= K, N <= 2^20, rows * K and rows * N < 2^40,
  * 1 <= E <= 1024.
  * Errors: MOK_ERR_INVALID_ARG for a null or misaligned pointer, one of

@@ -418,13 +418,16 @@ __global__ __launch_bounds__(64 * kAddWaves) void lora_add_kernel(LoraAdd a, int
           big = fmaxf(big, fabsf(v[s][j]));
         }
       }
-      float up = 1.f;  // fp16: the row's sums brought to [1, 2) by a power of two, exactly, and back at the end
+      // fp16: the row's sums brought to [2^14, 2^15) by a power of two, exactly, and back
+      // at the end: a rank 2^-22 below the largest still has its 16 bits, and what is off
+      // of any is 2^-39 of the largest.  (At [1, 2) a rank lost bits from 2^-9 on.)
+      float up = 1.f;
       if constexpr (DT == 2) {
         big = fmaxf(big, __shfl_xor(big, 16, 64));
         big = fmaxf(big, __shfl_xor(big, 32, 64));
-        const int e = big > 0.f && big < INFINITY ? (big < 0x1p-126f ? -126 : ilogbf(big)) : 0;
-        up = ldexpf(1.f, e);
-        const float down = ldexpf(1.f, -e);
+        const int e = big > 0.f && big < INFINITY ? (big < 0x1p-112f ? -112 : ilogbf(big)) : 14;
+        up = ldexpf(1.f, e - 14);
+        const float down = ldexpf(1.f, 14 - e);
 #pragma unroll
         for (int s = 0; s < RT; ++s)
 #pragma unroll
