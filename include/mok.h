@@ -702,9 +702,9 @@ mok_status mok_quantize_int4(const void* src, int64_t rows, int64_t K, int32_t g
  *                   K], B dtype [L, E_loc, N, r] for that matrix [N, K], scale
  *                   float [L], its own r each; A and B both NULL: none
  * 0 <= T <= 16, 1 <= k <= min(E, 64), E <= 1024, 1 <= d, F <= 65536, L >= 1 with
- * adapters.  Finite values: a NaN logit ranks below every number, and an
- * infinity or NaN in W2 of an expert that any token chose reaches every token.
- * T = 0 does nothing.
+ * adapters.  A NaN logit ranks below every number (nothing is reported); an
+ * infinity or NaN in x, or in the weights of an expert or an adapter, reaches the
+ * tokens that it belongs to and no other.  T = 0 does nothing.
  * Errors: MOK_ERR_INVALID_ARG for a null or misaligned pointer or a shape or flag
  * outside these bounds; MOK_ERR_HIP for a failed launch.
  */

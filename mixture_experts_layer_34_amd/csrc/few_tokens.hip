@@ -477,6 +477,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
   Quad<DT, ODD> qw[2][U][NT];
   u32x4_t qh[2][U][PARTS];
   uint32_t odd[2];  // a bit for each access of a chunk that starts off a dword
+  bool has[2];      // the lane's token has the chunk's expert
   int left[2];  // !WHOLE: elements of F from the lane's first of the chunk
   // WHOLE: F is a multiple of KE, a lane's 16 bytes lie in F or past it; a
   // lane past it reads the row's first bytes and zeros of h.  Otherwise the lane
@@ -489,6 +490,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
     const char* wp = (const char*)a.w[2] + (int64_t)e * a.d * row_bytes;
     left[buf] = a.F - ch * U * STEP - g * KE;
     odd[buf] = 0;
+    has[buf] = pair >= 0;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int k = (ch * U + j) * STEP + g * KE;
@@ -515,6 +517,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
     __builtin_amdgcn_sched_barrier(0);
   };
   auto mul = [&](int buf) {
+    f32x4_t before[NT];
+#pragma unroll
+    for (int q = 0; q < NT; ++q) before[q] = acc[q];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       if constexpr (!WHOLE) {  // past F nothing was written
@@ -537,6 +542,11 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
         }
       }
     }
+    // zeros times an infinite or NaN weight: not a sum of a token without the expert
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[q][i] = has[buf] ? acc[q][i] : before[q][i];
     __builtin_amdgcn_sched_barrier(0);
   };
   if (mine) {  // no load under a condition, as in UP

@@ -493,7 +493,9 @@ def few_token_layer(x: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, w3:
     local and a token without one of them gets 0.  Routing as in the layer
     (MoeShape.gating, renorm).  lora = (l1, l3, l2), LoraWeights [L, E_loc, ...]
     of w1, w3 and w2 or None each, with int32 adapter [T]: token t's matrices are
-    W + scale B A of its adapter; an adapter outside [0, L) is none."""
+    W + scale B A of its adapter; an adapter outside [0, L) is none.  A NaN logit
+    ranks last; an infinity or NaN in x or in the weights of an expert reaches the
+    tokens of that row or expert and no other."""
     fn = "few_token_layer"
     dt = _DTYPES.get(x.dtype)
     _need(x.dim() == 2 and dt is not None and x.shape[0] <= 16, fn, "fp32, bf16 or fp16 x [T, d], T <= 16, expected")
