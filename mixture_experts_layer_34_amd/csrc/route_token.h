@@ -78,12 +78,15 @@ __device__ __forceinline__ void route_token(const float* __restrict__ row, int t
     for (int i = 0; i < EPL; ++i)
       if (lane + 64 * i == be) key[i] = 0ull;
     if (lane == 0) {
-      const float g = SIGM ? 1.0f / (1.0f + expf(-bv)) : expf(bv - m) * inv_s;
+      const float p = SIGM ? 1.0f / (1.0f + expf(-bv)) : expf(bv - m);
+      const float g = SIGM ? p : p * inv_s;
       idx_out[(int64_t)t * k + j] = be;
       idx_saved[(int64_t)t * k + j] = be;
       if constexpr (RENORM) {
         graw[j] = g;
-        gsum += g;
+        // the product enters the sum unrounded, written as such: few_tokens.hip's router
+        // gives the same gates bit for bit
+        gsum = SIGM ? gsum + p : fmaf(p, inv_s, gsum);
       } else {
         gate_out[(int64_t)t * k + j] = g;
         gate_saved[(int64_t)t * k + j] = g;
