@@ -297,17 +297,19 @@ template <int DT, int RT, int M, bool ODD> __global__ __launch_bounds__(64 * kRa
 
 // ------------------------------------------------------------------ add
 constexpr int kAddWaves = 4;
-constexpr int kBareTokens = 16;  // tokens a wave looks over for rows of no adapter
+constexpr int kBareTokens = 16;  // tokens a wave looks over at once for rows of no adapter
+// Most workgroups that look: a launch counts its threads in 32 bits, and 2^30 rows at
+// kBareTokens a wave would pass them.  Each goes on to further tokens where there are more.
+constexpr int kBareWorkgroups = 1 << 16;
 
 // 64-column blocks of a wave (8192 x 4096 of rank 16: 39.4 us with two, 45.0 with
 // one, 47.0 with four; 24576 x 1408 of rank 32: 65 with two, 76 with one).
 template <int DT, int RT> constexpr int kAddBlocks = RT >= 4 || DT == 0 ? 1 : 2;
 
-// Rows of no adapter: out = base, or 0.  A wave looks over kBareTokens tokens at once.
-template <int DT> __device__ __forceinline__ void bare_rows(const LoraAdd& a, int wave) {
+// Rows of no adapter: out = base, or 0.  For the kBareTokens tokens from t0 on, by a wave.
+template <int DT> __device__ __forceinline__ void bare_rows(const LoraAdd& a, int64_t t0) {
   constexpr int KE = kFragElems<DT>, S = Elem<DT>::kBytes;
   const int lane = lane_id();
-  const int64_t t0 = (int64_t)wave * kBareTokens;
   bool bare = false;
   if (lane < kBareTokens && t0 + lane < a.map.rows) {
     const int row = a.map.row_of_pair[t0 + lane];
@@ -346,7 +348,8 @@ __global__ __launch_bounds__(64 * kAddWaves) void lora_add_kernel(LoraAdd a, int
   constexpr int CT = kAddBlocks<DT, RT>, W = 16 * RT;
   const int lane = lane_id(), w = wave_id(), i16 = lane & 15, g4 = lane >> 4;
   if ((int)blockIdx.x < bare) {
-    bare_rows<DT>(a, blockIdx.x * kAddWaves + w);
+    for (int64_t t0 = (blockIdx.x * kAddWaves + w) * kBareTokens; t0 < a.map.rows; t0 += (int64_t)bare * kAddWaves * kBareTokens)
+      bare_rows<DT>(a, t0);
     return;
   }
   const int blocks = (a.N + 64 * CT - 1) / (64 * CT);
@@ -806,9 +809,10 @@ template <int DT, int RT> hipError_t add_of(const LoraAdd& a, hipStream_t s) {
   // less than a row each
   int64_t ranges = (12 * kNumCUs + blocks - 1) / blocks;
   if (ranges > a.map.rows) ranges = a.map.rows;
-  const int bare = a.map.row_of_pair && a.out != a.base
-                       ? (a.map.rows + 8 * kBareTokens * kAddWaves - 1) / (8 * kBareTokens * kAddWaves) * 8
-                       : 0;
+  int bare = a.map.row_of_pair && a.out != a.base
+                 ? (a.map.rows + 8 * kBareTokens * kAddWaves - 1) / (8 * kBareTokens * kAddWaves) * 8
+                 : 0;
+  if (bare > kBareWorkgroups) bare = kBareWorkgroups;
   hipLaunchKernelGGL((lora_add_kernel<DT, RT>), dim3((unsigned)((blocks * ranges + 8 * kAddWaves - 1) / (8 * kAddWaves) * 8 + bare)),
                      dim3(64 * kAddWaves), 0, s, a, (int)ranges, bare);
   return hipGetLastError();
