@@ -24,12 +24,13 @@
 // h goes from UP to DOWN in four bytes whatever the type, for the 16-bit ones as
 // two bf16 parts (store_h), so that it loses nothing next to out's own rounding
 // and keeps fp32's range: in 16 bits it would be a second rounding as large as
-// out's, and in fp16 an infinity past 65504 and nothing below 3e-8.  DOWN takes up
-// to eight tokens' two parts as the sixteen columns of one matrix instruction, more
-// tokens' by a second one; fp16 weights are two bf16 parts there, exactly.
+// out's, and in fp16 an infinity past 65504 and nothing below 3e-8.  DOWN takes the
+// two parts of eight tokens as the sixteen columns of a matrix instruction: all
+// tokens', or those that have the expert (build_turns).  fp16 weights are two bf16
+// parts there, exactly.
 // All sums are fp32 in a fixed order.
 // At d 4096, F 1536, 8 of 128 experts (bf16): one token 39 + 20 us (201 and 101 MB;
-// 5.1 TB/s together), sixteen 563 us (5.5 TB/s).
+// 5.1 TB/s together), sixteen 540 us (3.1 GB, 5.7 TB/s; with h in 16 bits 533).
 #include "few_tokens.h"
 #include "frag.h"
 #include "mok_internal.h"
@@ -177,16 +178,35 @@ __device__ __forceinline__ void route_few(const FewTokens& a, int t0, int t1, in
   }
 }
 
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2_on2_t __attribute__((ext_vector_type(2), aligned(2)));
+
 // h of the 16-bit types: a row of bf16 values, and a row of their bf16 rests Fp
 // further on: off by 2^-16 of the value at most.  (fp16 itself has no range for h.)
-template <int DT> __device__ __forceinline__ void store_h(const FewTokens& a, int pair, int col, float v) {
+// The first n of four neighbours.
+template <int DT> __device__ __forceinline__ void store_h(const FewTokens& a, int pair, int col, const float (&v)[4], int n) {
   if constexpr (DT == 0) {
-    reinterpret_cast<float*>(a.h)[(int64_t)pair * a.Fp + col] = v;
+    store_part<0>((char*)a.h + ((int64_t)pair * a.Fp + col) * 4,
+                  u32x4_t{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])}, n);
   } else {
     uint16_t* to = reinterpret_cast<uint16_t*>(a.h) + (int64_t)pair * 2 * a.Fp + col;
-    const uint32_t hi = Elem<1>::pack(v, 0.f);
-    to[0] = (uint16_t)hi;
-    to[a.Fp] = (uint16_t)Elem<1>::pack(v - Elem<1>::lo(hi), 0.f);
+    u32x2_t hi, lo;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      hi[i] = Elem<1>::pack(v[2 * i], v[2 * i + 1]);
+      lo[i] = Elem<1>::pack(v[2 * i] - Elem<1>::lo(hi[i]), v[2 * i + 1] - Elem<1>::hi(hi[i]));
+    }
+    if (n >= 4) {
+      *reinterpret_cast<u32x2_on2_t*>(to) = hi;
+      *reinterpret_cast<u32x2_on2_t*>(to + a.Fp) = lo;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < n) {
+          to[i] = (uint16_t)(hi[i / 2] >> (16 * (i & 1)));
+          to[a.Fp + i] = (uint16_t)(lo[i / 2] >> (16 * (i & 1)));
+        }
+    }
   }
 }
 // KE elements of h from `col` on, the first n of them (zeros behind).
@@ -216,6 +236,11 @@ __device__ __forceinline__ void split_f16(u32x4_t v, u32x4_t* hi, u32x4_t* lo) {
     (*lo)[j] = __builtin_amdgcn_perm(rb, ra, 0x07060302);
   }
 #endif
+}
+
+// The sum of a lane's column and of the one eight further on (mod 16).
+__device__ __forceinline__ float both_parts(float v) {
+  return v + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x128, 0xf, 0xf, false));  // row_ror 8
 }
 
 __device__ __forceinline__ int adapter_of(const FewTokens& a, int t) {
@@ -418,11 +443,10 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
       }
       if (pair >= 0) {
         const float gt = s.gate[pair];
+        float hv[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float va = acc[0][i], hv = va * sigmoidf_(va) * acc[1][i] * gt;
-          if (4 * g + i < cols) store_h<DT>(a, pair, n0 + 4 * g + i, hv);
-        }
+        for (int i = 0; i < 4; ++i) hv[i] = acc[0][i] * sigmoidf_(acc[0][i]) * acc[1][i] * gt;
+        store_h<DT>(a, pair, n0 + 4 * g, hv, cols - 4 * g);
       }
     }
     t = next;
@@ -433,27 +457,101 @@ __global__ __launch_bounds__(64 * kUpWaves) void few_up_kernel(FewTokens a) {
 // A workgroup owns `cols` columns of out, up to 16 NT: as many as give every
 // compute unit the same share.
 constexpr int kDownWaves = 8;
-// LONG: F >= KE.  ODD: rows of W2 of an odd number of 16-bit elements.  PARTS: matrix
-// instructions for the parts of h; with one, for the 16-bit types and at most eight
-// tokens, columns 0..7 are the first parts and 8..15 the second.  (Four tokens of
-// d 2048, F 1408 with adapters 102 us, by two 111; sixteen of d 4096, F 1536, which
-// need two, 563, where one rounded part alone took 535.)
-template <int DT, int NT, bool WHOLE, bool LONG, bool ODD, int PARTS>
+
+// More than eight tokens of a 16-bit type: each expert's tokens in turns of up to eight,
+// in their order; an expert with more has two turns, one after the other, the second
+// of which finds W2 in L2.  (Both parts by two matrix instructions of sixteen tokens
+// each want twice the accesses of h: 16 tokens of d 4096, F 1536, 8 of 128 experts took
+// 561 us so and take 540 in turns; all of 8 experts, two turns each, 95 and 99.)
+struct FewTurns {
+  int16_t* pair;   // [turns][8], -1: none
+  int8_t* at;      // [turns][16] the place of each token, -1: none
+  int16_t* expert; // [turns]
+};
+__host__ __device__ inline int few_turns(int P, int slots) { return slots + P / 9; }
+// For all threads of the workgroup; the number of turns.  over: 16 words.
+__device__ __forceinline__ int build_turns(const FewTokens& a, const FewTurns& s, int most, int turns, uint64_t* over) {
+  constexpr int N = 64 * kDownWaves;
+  const int tid = threadIdx.x, lane = lane_id(), w = wave_id();
+  const int nslots = *reinterpret_cast<const int32_t*>(a.table);
+  for (int i = tid; i < turns * 4; i += N) {
+    reinterpret_cast<uint32_t*>(s.pair)[i] = 0xFFFFFFFFu;
+    reinterpret_cast<uint32_t*>(s.at)[i] = 0xFFFFFFFFu;
+  }
+  uint32_t pairs[2][8];  // of slots tid and tid + N, two a word
+  int n[2] = {0, 0};
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int slot = tid + r * N;
+    if (64 * w + r * N >= most) continue;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      pairs[r][i] = slot < nslots ? reinterpret_cast<const uint32_t*>(table_pairs(a.table, most))[slot * 8 + i] : 0xFFFFFFFFu;
+      n[r] += ((int32_t)pairs[r][i] >= 0) + ((int16_t)pairs[r][i] >= 0);
+    }
+    const uint64_t b = __ballot(n[r] > 8);
+    if (lane == 0) over[w + r * kDownWaves] = b;
+  }
+  __syncthreads();
+  int second = 0;  // second turns of the slots before this wave's, and of all
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int slot = tid + r * N;
+    second = 0;
+    for (int i = 0; i < w + r * kDownWaves && 64 * i < most; ++i) second += __popcll(over[i]);
+    if (slot < nslots) {
+      const uint64_t b = over[w + r * kDownWaves];
+      const int v = slot + second + __popcll(b & ((1ull << lane) - 1ull));
+      const int16_t e = reinterpret_cast<const int16_t*>((const char*)a.table + 16)[slot];
+      s.expert[v] = e;
+      if (n[r] > 8) s.expert[v + 1] = e;
+      int c = 0;
+#pragma unroll
+      for (int t = 0; t < 16; ++t) {
+        const int16_t pair = (int16_t)(pairs[r][t / 2] >> (16 * (t & 1)));
+        if (pair < 0) continue;
+        s.pair[v * 8 + c] = pair;  // (place 8 of a turn is place 0 of the next)
+        s.at[(v + (c >> 3)) * 16 + t] = (int8_t)(c & 7);
+        ++c;
+      }
+    }
+  }
+  __syncthreads();
+  second = 0;
+  for (int i = 0; 64 * i < most; ++i) second += __popcll(over[i]);
+  return __builtin_amdgcn_readfirstlane(nslots + second);
+}
+
+// LONG: F >= KE.  ODD: rows of W2 of an odd number of 16-bit elements.  MANY: turns of
+// eight tokens (16-bit types).  A 16-bit type's columns 0..7 are the first parts of h
+// and 8..15 the second ones.
+template <int DT, int NT, bool WHOLE, bool LONG, bool ODD, bool MANY>
 __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, int cols) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int KE = kFragElems<DT>, STEP = kFragStep<DT>, S = Elem<DT>::kBytes, U = kUnroll, NW = kDownWaves;
-  constexpr bool BOTH = DT != 0 && PARTS == 1;  // columns of both parts
   extern __shared__ __align__(16) char lds[];
   __shared__ f32x4_t red[NW][NT][64];
   const int tid = threadIdx.x, lane = tid & 63, w = wave_id();
-  const int i16 = lane & 15, g = lane >> 4, col = BOTH ? i16 & 7 : i16;  // col: the lane's token
+  const int i16 = lane & 15, g = lane >> 4, col = DT != 0 ? i16 & 7 : i16;  // col: the lane's token, or its place
   const int P = a.T * a.k, most = few_slots(P, a.E_loc);
-  int16_t *s_pair = reinterpret_cast<int16_t*>(lds), *s_expert = s_pair + 16 * most;
-  const int nslots = *reinterpret_cast<const int32_t*>(a.table);
-  for (int i = tid; i < most * 8; i += 64 * NW)
-    reinterpret_cast<uint32_t*>(s_pair)[i] = reinterpret_cast<const uint32_t*>(table_pairs(a.table, most))[i];
-  for (int i = tid; i < most; i += 64 * NW) s_expert[i] = reinterpret_cast<const int16_t*>((const char*)a.table + 16)[i];
-  __syncthreads();
+  constexpr int COLS = MANY ? 8 : 16;  // pairs of a slot
+  int nslots;  // or turns
+  int16_t *s_pair = reinterpret_cast<int16_t*>(lds), *s_expert;
+  int8_t* s_at = nullptr;
+  if constexpr (MANY) {
+    __shared__ uint64_t over[2 * NW];
+    const int turns = few_turns(P, most);
+    s_at = reinterpret_cast<int8_t*>(s_pair + 8 * turns);
+    s_expert = reinterpret_cast<int16_t*>(s_at + 16 * turns);
+    nslots = build_turns(a, FewTurns{s_pair, s_at, s_expert}, most, turns, over);
+  } else {
+    s_expert = s_pair + 16 * most;
+    nslots = *reinterpret_cast<const int32_t*>(a.table);
+    for (int i = tid; i < most * 8; i += 64 * NW)
+      reinterpret_cast<uint32_t*>(s_pair)[i] = reinterpret_cast<const uint32_t*>(table_pairs(a.table, most))[i];
+    for (int i = tid; i < most; i += 64 * NW) s_expert[i] = reinterpret_cast<const int16_t*>((const char*)a.table + 16)[i];
+    __syncthreads();
+  }
 
   const int n0 = blockIdx.x * cols, n1 = n0 + cols < a.d ? n0 + cols : a.d;
   const int64_t row_bytes = (int64_t)a.F * S;
@@ -475,22 +573,22 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
 #pragma unroll
   for (int q = 0; q < NT; ++q) acc[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   Quad<DT, ODD> qw[2][U][NT];
-  u32x4_t qh[2][U][PARTS];
+  u32x4_t qh[2][U];
   uint32_t odd[2];  // a bit for each access of a chunk that starts off a dword
-  bool has[2];      // the lane's token has the chunk's expert
+  int at[2];        // the place of the lane's token in the chunk's columns, < 0: it has not the expert
   int left[2];  // !WHOLE: elements of F from the lane's first of the chunk
   // WHOLE: F is a multiple of KE, a lane's 16 bytes lie in F or past it; a
   // lane past it reads the row's first bytes and zeros of h.  Otherwise the lane
   // that F ends in reads the row's last 16 bytes and moves them to their places.
   auto load = [&](int buf) {
     const int e = __builtin_amdgcn_readfirstlane(s_expert[slot]);
-    const int pair = s_pair[slot * 16 + col];
+    const int pair = s_pair[slot * COLS + col];
     // a pair that is not: an offset past the buffer, which loads zeros
-    const uint32_t hoff = pair >= 0 ? (uint32_t)(pair * a.Fp) * 4 + (BOTH && i16 > 7 ? a.Fp * 2 : 0) : 0xC0000000u;
+    const uint32_t hoff = pair >= 0 ? (uint32_t)(pair * a.Fp) * 4 + (DT != 0 && i16 > 7 ? a.Fp * 2 : 0) : 0xC0000000u;
     const char* wp = (const char*)a.w[2] + (int64_t)e * a.d * row_bytes;
     left[buf] = a.F - ch * U * STEP - g * KE;
     odd[buf] = 0;
-    has[buf] = pair >= 0;
+    at[buf] = MANY ? s_at[slot * 16 + i16] : pair;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int k = (ch * U + j) * STEP + g * KE;
@@ -504,11 +602,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
           qw[buf][j][q].v = load_part<DT>(wp + wrow[q] + k * S, k < a.F ? a.F - k : 0);
         }
       }
-#pragma unroll
-      for (int i = 0; i < PARTS; ++i) {
-        const auto v = __builtin_amdgcn_raw_buffer_load_b128(hrs, k < a.F ? hoff + k * S + i * a.Fp * 2 : 0xC0000000u, 0, 0);
-        qh[buf][j][i] = u32x4_t{(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
-      }
+      const auto v = __builtin_amdgcn_raw_buffer_load_b128(hrs, k < a.F ? hoff + k * S : 0xC0000000u, 0, 0);
+      qh[buf][j] = u32x4_t{(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
     }
     const bool wrap = ch + skip >= chunks;
     const int next = slot + skip_slots + wrap;
@@ -517,15 +612,12 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
     __builtin_amdgcn_sched_barrier(0);
   };
   auto mul = [&](int buf) {
-    f32x4_t before[NT];
+    f32x4_t sum[NT];
 #pragma unroll
-    for (int q = 0; q < NT; ++q) before[q] = acc[q];
+    for (int q = 0; q < NT; ++q) sum[q] = MANY ? f32x4_t{0.f, 0.f, 0.f, 0.f} : acc[q];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      if constexpr (!WHOLE) {  // past F nothing was written
-#pragma unroll
-        for (int i = 0; i < PARTS; ++i) qh[buf][j][i] = first_elems<DT>(qh[buf][j][i], left[buf] - j * STEP);
-      }
+      if constexpr (!WHOLE) qh[buf][j] = first_elems<DT>(qh[buf][j], left[buf] - j * STEP);  // past F nothing was written
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
         u32x4_t vw = qw[buf][j][q].get((odd[buf] >> (j * NT + q) & 1) * 16);
@@ -535,18 +627,21 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
         }
         u32x4_t rest;
         if constexpr (DT == 2) split_f16(vw, &vw, &rest);
-#pragma unroll
-        for (int i = PARTS - 1; i >= 0; --i) {
-          acc[q] = mma<DT == 0 ? 0 : 1>(vw, qh[buf][j][i], acc[q]);
-          if constexpr (DT == 2) acc[q] = mma<1>(rest, qh[buf][j][i], acc[q]);
-        }
+        sum[q] = mma<DT == 0 ? 0 : 1>(vw, qh[buf][j], sum[q]);
+        if constexpr (DT == 2) sum[q] = mma<1>(rest, qh[buf][j], sum[q]);
       }
     }
-    // zeros times an infinite or NaN weight: not a sum of a token without the expert
+    // A token takes its own column's sum (MANY: both parts', from its place in the turn),
+    // and one without the expert none: zeros times an infinite weight are not 0.
 #pragma unroll
     for (int q = 0; q < NT; ++q)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[q][i] = has[buf] ? acc[q][i] : before[q][i];
+      for (int i = 0; i < 4; ++i) {
+        float v = sum[q][i];
+        if constexpr (MANY)
+          v = acc[q][i] + __uint_as_float(__builtin_amdgcn_ds_bpermute((16 * g + (at[buf] & 7)) * 4, __float_as_uint(both_parts(v))));
+        acc[q][i] = at[buf] >= 0 ? v : acc[q][i];
+      }
     __builtin_amdgcn_sched_barrier(0);
   };
   if (mine) {  // no load under a condition, as in UP
@@ -585,9 +680,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
     f32x4_t v = red[0][w][lane];
 #pragma unroll
     for (int k = 1; k < NW; ++k) v += red[k][w][lane];
-    if constexpr (BOTH)
+    if constexpr (DT != 0 && !MANY)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v[i]), 0x128, 0xf, 0xf, false));  // row_ror 8
+      for (int i = 0; i < 4; ++i) v[i] = both_parts(v[i]);
     const int n = n0 + 16 * w + 4 * g;
     const int64_t o = (int64_t)i16 * a.d + n;
 #pragma unroll
@@ -650,14 +745,13 @@ template <int DT, int EPL, bool DOWN> __global__ __launch_bounds__(256) void few
 #endif
 }
 
-template <int DT, int NT, bool WHOLE, bool LONG, bool ODD, int PARTS>
-void down_parts(const FewTokens& a, int cols, int slots, hipStream_t s) {
-  hipLaunchKernelGGL((few_down_kernel<DT, NT, WHOLE, LONG, ODD, PARTS>), dim3((a.d + cols - 1) / cols),
-                     dim3(64 * kDownWaves), (size_t)slots * 34 + 64, s, a, cols);
-}
 template <int DT, int NT, bool WHOLE, bool LONG, bool ODD> void down(const FewTokens& a, int cols, int slots, hipStream_t s) {
-  if (DT != 0 && a.T > 8) down_parts<DT, NT, WHOLE, LONG, ODD, DT == 0 ? 1 : 2>(a, cols, slots, s);
-  else down_parts<DT, NT, WHOLE, LONG, ODD, 1>(a, cols, slots, s);
+  const dim3 grid((a.d + cols - 1) / cols), block(64 * kDownWaves);
+  if (DT != 0 && a.T > 8)
+    hipLaunchKernelGGL((few_down_kernel<DT, NT, WHOLE, LONG, ODD, DT != 0>), grid, block,
+                       (size_t)few_turns(a.T * a.k, slots) * 34 + 64, s, a, cols);
+  else
+    hipLaunchKernelGGL((few_down_kernel<DT, NT, WHOLE, LONG, ODD, false>), grid, block, (size_t)slots * 34 + 64, s, a, cols);
 }
 
 template <int DT, int EPL, bool ODD> void up(const FewTokens& a, int P, int slots, hipStream_t s) {
@@ -668,8 +762,9 @@ template <int DT, int EPL, bool ODD> void up(const FewTokens& a, int P, int slot
       n = 1;
     return n;
   }();
-  // as many workgroups as are resident at once, in whole rounds of the compute
-  // units; of those the kernel uses what the chosen experts' columns take
+  // as many workgroups as are resident at once beside tables of 8 KB (larger ones leave
+  // fewer, and the rest follow), in whole rounds of the compute units; of those the
+  // kernel uses what the chosen experts' columns take
   const int64_t units = ((int64_t)slots * a.F + 15) / 16, cap = (int64_t)kNumCUs * per_cu;
   const int64_t rounds = (units + kNumCUs - 1) / kNumCUs * kNumCUs;
   hipLaunchKernelGGL((few_up_kernel<DT, EPL, ODD>), dim3((unsigned)(rounds < cap ? rounds : cap)), dim3(64 * kUpWaves),

@@ -44,6 +44,11 @@ SHAPES = [(1, 64, 128, 4, 2, "bf16"), (16, 96, 256, 8, 4, "bf16"), (5, 130, 67, 
           (16, 200, 1411, 6, 3, "f16"), (8, 72, 1411, 6, 3, "bf16"), (9, 72, 1411, 6, 3, "bf16"),
           (8, 4104, 67, 3, 2, "f16"), (9, 4104, 67, 3, 2, "f16"), (10, 40, 5, 4, 2, "bf16"), (12, 40, 1, 4, 2, "f16"),
           (11, 4100, 129, 3, 1, "bf16"), (6, 64, 97, 5, 2, "f32")]
+# more than eight tokens an expert: one expert, all of them, some of many (in both
+# halves of a thread's slots), beside ones with eight or fewer
+SHAPES += [(16, 72, 136, 1, 1, "bf16"), (9, 64, 64, 1, 1, "f16"), (16, 72, 264, 3, 3, "bf16"),
+           (13, 4104, 72, 2, 2, "f16"), (16, 48, 40, 700, 64, "bf16"), (16, 64, 48, 4, 2, "f16"),
+           (16, 40, 24, 90, 50, "bf16"), (10, 200, 520, 5, 4, "f16")]
 
 
 @pytest.mark.parametrize("T,d,F,E,k,dt", SHAPES)
@@ -107,3 +112,30 @@ def test_a_token_of_zeros_gets_zero(dt):
     args[0][2] = 0
     got = X.few_token_layer(*args, 2)[0]
     assert not got[2].any() and got[[0, 1, 3]].any(1).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T", [8, 9, 15, 16])
+def test_experts_of_most_tokens_beside_experts_of_one(T, dt):
+    """Slots past 512 with more than eight tokens each beside slots with one."""
+    d, F, E, k = 40, 24, 1024, 40
+    args = _case(T, d, F, E, dt, T)
+    hot = torch.arange(E - 25, E, device="cuda")
+    args[1][:, hot] = 20.0 - 0.25 * (hot - hot[0]).float()       # every token's first 25
+    args[1][1::2, hot[::3]] = -20.0                              # (half of them lack a third)
+    _, idx, _ = X.few_token_layer(*args, k)
+    n = torch.bincount(idx.flatten().long(), minlength=E)
+    assert (n == 1).any() and ((n > 8).sum() >= 16 or T == 8) and (n > 0).sum() > 128
+    _check(args, k, dt)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_sixteen_tokens_are_eight_and_eight(dt):
+    """A token's output does not depend on the tokens beside it: the bits of a
+    call of sixteen against two calls' of eight, but for the order of their sums."""
+    args = _case(16, 96, 264, 12, dt, 21)
+    whole = X.few_token_layer(*args, 3)[0]
+    for half in (slice(0, 8), slice(8, 16)):
+        part = X.few_token_layer(args[0][half], args[1][half], *args[2:], 3)[0]
+        ref, err = layer_once64(args[0][half], args[1][half], *args[2:], 3)
+        close(whole[half], part, 2 * rounded(ref, err, dt), "out")
