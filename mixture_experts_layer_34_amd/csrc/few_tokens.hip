@@ -184,10 +184,10 @@ typedef uint32_t u32x2_on2_t __attribute__((ext_vector_type(2), aligned(2)));
 // h of the 16-bit types: a row of bf16 values, and a row of their bf16 rests Fp
 // further on: off by 2^-16 of the value at most.  (fp16 itself has no range for h.)
 // The first n of four neighbours.
-template <int DT> __device__ __forceinline__ void store_h(const FewTokens& a, int pair, int col, const float (&v)[4], int n) {
+template <int DT>
+__device__ __forceinline__ void store_h(const FewTokens& a, int pair, int col, const float (&v)[4], int n) {
   if constexpr (DT == 0) {
-    store_part<0>((char*)a.h + ((int64_t)pair * a.Fp + col) * 4,
-                  u32x4_t{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])}, n);
+    store_part<0>((char*)a.h + ((int64_t)pair * a.Fp + col) * 4, narrow<0>(v), n);
   } else {
     uint16_t* to = reinterpret_cast<uint16_t*>(a.h) + (int64_t)pair * 2 * a.Fp + col;
     u32x2_t hi, lo;
@@ -474,6 +474,7 @@ __device__ __forceinline__ int build_turns(const FewTokens& a, const FewTurns& s
   constexpr int N = 64 * kDownWaves;
   const int tid = threadIdx.x, lane = lane_id(), w = wave_id();
   const int nslots = *reinterpret_cast<const int32_t*>(a.table);
+  const uint32_t* from = reinterpret_cast<const uint32_t*>(table_pairs(a.table, most));
   for (int i = tid; i < turns * 4; i += N) {
     reinterpret_cast<uint32_t*>(s.pair)[i] = 0xFFFFFFFFu;
     reinterpret_cast<uint32_t*>(s.at)[i] = 0xFFFFFFFFu;
@@ -486,7 +487,7 @@ __device__ __forceinline__ int build_turns(const FewTokens& a, const FewTurns& s
     if (64 * w + r * N >= most) continue;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      pairs[r][i] = slot < nslots ? reinterpret_cast<const uint32_t*>(table_pairs(a.table, most))[slot * 8 + i] : 0xFFFFFFFFu;
+      pairs[r][i] = slot < nslots ? from[slot * 8 + i] : 0xFFFFFFFFu;
       n[r] += ((int32_t)pairs[r][i] >= 0) + ((int16_t)pairs[r][i] >= 0);
     }
     const uint64_t b = __ballot(n[r] > 8);
@@ -549,7 +550,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
     nslots = *reinterpret_cast<const int32_t*>(a.table);
     for (int i = tid; i < most * 8; i += 64 * NW)
       reinterpret_cast<uint32_t*>(s_pair)[i] = reinterpret_cast<const uint32_t*>(table_pairs(a.table, most))[i];
-    for (int i = tid; i < most; i += 64 * NW) s_expert[i] = reinterpret_cast<const int16_t*>((const char*)a.table + 16)[i];
+    for (int i = tid; i < most; i += 64 * NW)
+      s_expert[i] = reinterpret_cast<const int16_t*>((const char*)a.table + 16)[i];
     __syncthreads();
   }
 
@@ -617,7 +619,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
     for (int q = 0; q < NT; ++q) sum[q] = MANY ? f32x4_t{0.f, 0.f, 0.f, 0.f} : acc[q];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      if constexpr (!WHOLE) qh[buf][j] = first_elems<DT>(qh[buf][j], left[buf] - j * STEP);  // past F nothing was written
+      // past F nothing was written
+      if constexpr (!WHOLE) qh[buf][j] = first_elems<DT>(qh[buf][j], left[buf] - j * STEP);
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
         u32x4_t vw = qw[buf][j][q].get((odd[buf] >> (j * NT + q) & 1) * 16);
@@ -638,8 +641,10 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewTokens a, 
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float v = sum[q][i];
-        if constexpr (MANY)
-          v = acc[q][i] + __uint_as_float(__builtin_amdgcn_ds_bpermute((16 * g + (at[buf] & 7)) * 4, __float_as_uint(both_parts(v))));
+        if constexpr (MANY) {
+          const int lane_of = 16 * g + (at[buf] & 7);
+          v = acc[q][i] + __uint_as_float(__builtin_amdgcn_ds_bpermute(4 * lane_of, __float_as_uint(both_parts(v))));
+        }
         acc[q][i] = at[buf] >= 0 ? v : acc[q][i];
       }
     __builtin_amdgcn_sched_barrier(0);

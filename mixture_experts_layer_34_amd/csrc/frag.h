@@ -174,10 +174,4 @@ template <int DT> __device__ __forceinline__ u32x4_t narrow(const float* f) {
   return u32x4_t{e.w[0], e.w[1], e.w[2], e.w[3]};
 }
 
-// One element.
-template <int DT> __device__ __forceinline__ float elem_at(const void* p, int64_t i) {
-  if constexpr (DT == 0) return reinterpret_cast<const float*>(p)[i];
-  else return Elem<DT>::lo(reinterpret_cast<const uint16_t*>(p)[i]);
-}
-
 }  // namespace mok

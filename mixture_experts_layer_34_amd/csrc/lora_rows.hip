@@ -15,7 +15,8 @@
 //    whose fp32 parts the next kernel adds in order (no atomics).
 //  - add (out and dx; 37 us): the transposed product B u^T, so that a lane holds
 //    neighbouring columns of one row, y in, out back.  A wave keeps the B of its
-//    128 columns in registers and runs over its rows.  u enters 16-bit matrix
+//    128 columns (64 for fp32 and for ranks past 32) in registers and runs over its
+//    rows.  u enters 16-bit matrix
 //    instructions as a high and a low part (a K of 2 r), so that it loses nothing
 //    next to out's own rounding.
 //  - grad (dA and dB; 38 us for both matrices, 3.5 TB/s): K is the rows there.
@@ -348,8 +349,8 @@ __global__ __launch_bounds__(64 * kAddWaves) void lora_add_kernel(LoraAdd a, int
   constexpr int CT = kAddBlocks<DT, RT>, W = 16 * RT;
   const int lane = lane_id(), w = wave_id(), i16 = lane & 15, g4 = lane >> 4;
   if ((int)blockIdx.x < bare) {
-    for (int64_t t0 = (blockIdx.x * kAddWaves + w) * kBareTokens; t0 < a.map.rows; t0 += (int64_t)bare * kAddWaves * kBareTokens)
-      bare_rows<DT>(a, t0);
+    const int64_t at_once = (int64_t)bare * kAddWaves * kBareTokens;
+    for (int64_t t0 = (blockIdx.x * kAddWaves + w) * kBareTokens; t0 < a.map.rows; t0 += at_once) bare_rows<DT>(a, t0);
     return;
   }
   const int blocks = (a.N + 64 * CT - 1) / (64 * CT);
@@ -805,8 +806,8 @@ template <int DT, int RT> hipError_t rank_of(const LoraRank& b, hipStream_t s) {
 
 template <int DT, int RT> hipError_t add_of(const LoraAdd& a, hipStream_t s) {
   const int64_t blocks = (a.N + 64 * kAddBlocks<DT, RT> - 1) / (64 * kAddBlocks<DT, RT>);
-  // twelve waves a compute unit (eight 39 us, sixteen 41 at 8192 x 4096), but no
-  // less than a row each
+  // twelve waves a compute unit (eight 39 us, sixteen 41 at 8192 x 4096 of rank 16, bf16;
+  // fp16 and ranks past 16 have registers for eight or four), but no less than a row each
   int64_t ranges = (12 * kNumCUs + blocks - 1) / blocks;
   if (ranges > a.map.rows) ranges = a.map.rows;
   int bare = a.map.row_of_pair && a.out != a.base

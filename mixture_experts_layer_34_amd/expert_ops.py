@@ -337,7 +337,10 @@ class LoraWeights:
     [G, N, r] of one floating type, 1 <= r <= 128, scale fp32 [G] (None: 1), for
     lora_rows; or A [L, E, r, K], B [L, E, N, r] and scale [L], adapter l of
     expert e, for few_token_layer.  They may be held on the CPU and moved by
-    `to`; the operators take them on x's GPU."""
+    `to`; the operators take them on x's GPU.  A, B and scale are the caller's
+    own arrays, read at each call, but for one that is not contiguous (or not
+    16-byte aligned): it is copied here, and what is written to the original
+    afterwards is not seen."""
     A: torch.Tensor
     B: torch.Tensor
     scale: torch.Tensor | None = None
@@ -431,7 +434,8 @@ def lora_rows(x: torch.Tensor, amap: PairMap, w: LoraWeights, y: torch.Tensor | 
     One adapter on each expert's projection: the pairs' map with sorted_rows, and
     all of them in the experts' sorted rows; rows of no expert are left as they
     are.  `out` may be y itself.  With save the result is (out, u), u = A_g x_q
-    in fp32 [rows, r] and sorted rows, for lora_rows_backward."""
+    in fp32 [rows, r] and sorted rows (rows of no group uninitialised), for
+    lora_rows_backward."""
     fn = "lora_rows"
     rows, N, K, r, wc, (cfg, nws, _), (pair, rop, offsets) = _lora_args(fn, x, y, amap, w, sorted_rows)
     _unrecorded(fn, x, y, out, w.scale)

@@ -40,7 +40,8 @@ WIDTHS = [(25088, 24576, "bf16"), (64, 72, "bf16"), (12500, 12100, "f32"), (96, 
 
 @pytest.mark.parametrize("K,N,dt", WIDTHS)
 @pytest.mark.parametrize("offsets,rows", [([0, 50, 30], (0, 30, 0)), ([10, 0, 20], (10, 20, 1)),
-                                          ([0, 2 ** 31 - 1, 17], (0, 17, 0)), ([-(2 ** 31), 64, 2 ** 31 - 1], (0, 64, 0)),
+                                          ([0, 2 ** 31 - 1, 17], (0, 17, 0)),
+                                          ([-(2 ** 31), 64, 2 ** 31 - 1], (0, 64, 0)),
                                           ([40, -5, 2 ** 31 - 1], (40, 64, 1)), ([30, 10, 5], (0, 0, 0))])
 def test_gradients_of_falling_offsets(K, N, dt, offsets, rows):
     note(f"lora grad, falling offsets {offsets} K={K} N={N} {dt}")
