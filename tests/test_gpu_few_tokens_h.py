@@ -48,7 +48,8 @@ SHAPES = [(1, 64, 128, 4, 2, "bf16"), (16, 96, 256, 8, 4, "bf16"), (5, 130, 67, 
 # halves of a thread's slots), beside ones with eight or fewer
 SHAPES += [(16, 72, 136, 1, 1, "bf16"), (9, 64, 64, 1, 1, "f16"), (16, 72, 264, 3, 3, "bf16"),
            (13, 4104, 72, 2, 2, "f16"), (16, 48, 40, 700, 64, "bf16"), (16, 64, 48, 4, 2, "f16"),
-           (16, 40, 24, 90, 50, "bf16"), (10, 200, 520, 5, 4, "f16")]
+           (16, 40, 24, 90, 50, "bf16"), (10, 200, 520, 5, 4, "f16"), (12, 56, 130, 5, 3, "bf16"),
+           (11, 4104, 66, 3, 2, "f16"), (14, 4104, 258, 2, 2, "bf16")]
 
 
 @pytest.mark.parametrize("T,d,F,E,k,dt", SHAPES)
